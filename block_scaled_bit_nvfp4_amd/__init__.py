@@ -24,6 +24,9 @@ __all__ = [
     "mxfp4_repacked_code_bytes", "mxfp4_repacked_scale_bytes", "mxfp4_quantize", "mxfp4_repack",
     "mxfp4_dequant", "mxfp4_gemv",
     "alloc_repacked", "alloc_mx_repacked",
+    "NVFP4_KV_MXFP4", "NVFP4_KV_MXFP8", "KvCache", "KvBatch", "alloc_kv_cache", "nvfp4_kv_code_bytes",
+    "nvfp4_kv_scale_bytes", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_kv_attention_workspace_bytes",
+    "nvfp4_kv_attention",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -33,12 +36,27 @@ _lib = None
 
 NVFP4_MAX_N = 65536
 NVFP4_MAX_BATCH = 4
+NVFP4_KV_MXFP4 = 4
+NVFP4_KV_MXFP8 = 8
+_KV_DTYPE = {torch.bfloat16: 0, torch.float32: 1}      # NVFP4_KV_BF16, NVFP4_KV_F32
 
 
 class _Product(ctypes.Structure):
     """struct nvfp4_product of nvfp4.h."""
     _fields_ = [("wq", ctypes.c_void_p), ("ws", ctypes.c_void_p), ("tscale", ctypes.c_float),
                 ("rows", ctypes.c_int64), ("y", ctypes.c_void_p), ("argmax", ctypes.c_void_p)]
+
+
+class _KvCache(ctypes.Structure):
+    """struct nvfp4_kv_cache of nvfp4.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("k_codes", "k_scales", "v_codes", "v_scales")] +
+                [(n, ctypes.c_int32) for n in ("k_format", "v_format", "pages", "page_tokens", "heads", "head_dim")])
+
+
+class _KvBatch(ctypes.Structure):
+    """struct nvfp4_kv_batch of nvfp4.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("page_table", "offsets", "past")] + [("tokens", ctypes.c_int64)] +
+                [(n, ctypes.c_int32) for n in ("seqs", "table_width", "max_new", "max_context")])
 
 
 class NVFP4Error(RuntimeError):
@@ -84,6 +102,12 @@ def load():
             "mxfp4_repack": (i32, [P, P, i64, i64, P, P, P]),
             "mxfp4_dequant": (i32, [P, P, f32, i64, i64, P, P, P]),
             "mxfp4_gemv": (i32, [P, P, f32, i64, i64, P, i32, P, P]),
+            "nvfp4_kv_code_bytes": (sz, [i32, i32, i32, i32, i32]),
+            "nvfp4_kv_scale_bytes": (sz, [i32, i32, i32, i32, i32]),
+            "nvfp4_kv_append": (i32, [P, P, i32, P, i64, P, i64, P]),
+            "nvfp4_kv_read": (i32, [P, P, i32, P, i64, P, i64, P]),
+            "nvfp4_kv_attention_workspace_bytes": (sz, [P, P, i32]),
+            "nvfp4_kv_attention": (i32, [P, P, P, i64, i32, f32, i32, P, P, i64, P, P, sz, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -333,3 +357,144 @@ def alloc_mx_repacked(rows: int, cols: int, device="cuda"):
         raise NVFP4Error(-2, "alloc_mx_repacked")
     return (torch.empty(nq, dtype=torch.uint8, device=device),
             torch.empty(ns, dtype=torch.uint8, device=device))
+
+
+# ------------------------------------------- paged, quantised key/value cache
+
+def nvfp4_kv_code_bytes(format: int, pages: int, page_tokens: int, heads: int, head_dim: int) -> int:
+    return int(load().nvfp4_kv_code_bytes(format, pages, page_tokens, heads, head_dim))
+
+
+def nvfp4_kv_scale_bytes(format: int, pages: int, page_tokens: int, heads: int, head_dim: int) -> int:
+    return int(load().nvfp4_kv_scale_bytes(format, pages, page_tokens, heads, head_dim))
+
+
+class KvCache:
+    """struct nvfp4_kv_cache over four plane tensors (uint8), checked once and
+    kept by the caller: each side's planes hold the same number of pages, which
+    the key codes' size gives."""
+
+    def __init__(self, k_codes, k_scales, v_codes, v_scales, k_format, v_format, page_tokens, heads, head_dim):
+        page = nvfp4_kv_code_bytes(k_format, 1, page_tokens, heads, head_dim)
+        if page == 0 or nvfp4_kv_code_bytes(v_format, 1, page_tokens, heads, head_dim) == 0:
+            raise NVFP4Error(-2, "KvCache")
+        _checked(("k_codes", k_codes, _U8, page, False))
+        pages = k_codes.numel() // page
+        shape = (pages, page_tokens, heads, head_dim)
+        _checked(("k_codes", k_codes, _U8, page, False),
+                 ("k_scales", k_scales, _U8, nvfp4_kv_scale_bytes(k_format, *shape), False),
+                 ("v_codes", v_codes, _U8, nvfp4_kv_code_bytes(v_format, *shape), False),
+                 ("v_scales", v_scales, _U8, nvfp4_kv_scale_bytes(v_format, *shape), False))
+        self.planes = (k_codes, k_scales, v_codes, v_scales)
+        self.device = k_codes.device
+        self.pages, self.page_tokens, self.heads, self.head_dim = shape
+        self.k_format, self.v_format = int(k_format), int(v_format)
+        self._c = _KvCache(*[t.data_ptr() for t in self.planes], self.k_format, self.v_format, *shape)
+        self._ref = ctypes.addressof(self._c)
+
+
+class KvBatch:
+    """struct nvfp4_kv_batch: the new tokens of a step.  page_table [seqs, width],
+    offsets [seqs + 1] and past [seqs] are int32 tensors that the kernels read
+    when they run, so a program may keep one KvBatch and change their contents;
+    tokens, max_new and max_context are host numbers (bounds, see nvfp4.h)."""
+
+    def __init__(self, page_table, offsets, past, tokens, max_new, max_context):
+        if not isinstance(page_table, torch.Tensor) or page_table.dim() != 2:
+            raise ValueError("page_table must be an int32 tensor [seqs, width]")
+        seqs, width = page_table.shape
+        _checked(("page_table", page_table, _I32, 4, False), ("offsets", offsets, _I32, 4 * (seqs + 1), False),
+                 ("past", past, _I32, 4 * seqs, False))
+        self.arrays = (page_table, offsets, past)
+        self.device = page_table.device
+        self.tokens, self.max_new, self.max_context = int(tokens), int(max_new), int(max_context)
+        self._c = _KvBatch(*[t.data_ptr() for t in self.arrays], self.tokens, seqs, width, self.max_new,
+                           self.max_context)
+        self._ref = ctypes.addressof(self._c)
+
+
+def alloc_kv_cache(pages, page_tokens, heads, head_dim, k_format=NVFP4_KV_MXFP8, v_format=NVFP4_KV_MXFP8,
+                   device="cuda"):
+    """A KvCache over newly allocated (uninitialised) planes."""
+    shape = (pages, page_tokens, heads, head_dim)
+    sizes = [nvfp4_kv_code_bytes(k_format, *shape), nvfp4_kv_scale_bytes(k_format, *shape),
+             nvfp4_kv_code_bytes(v_format, *shape), nvfp4_kv_scale_bytes(v_format, *shape)]
+    if 0 in sizes:
+        raise NVFP4Error(-2, "alloc_kv_cache")
+    return KvCache(*[torch.empty(n, dtype=torch.uint8, device=device) for n in sizes], k_format, v_format,
+                   page_tokens, heads, head_dim)
+
+
+def _rows(name, t, cache, batch, heads, dtypes):
+    """Check a [tokens, heads, head_dim] tensor whose tokens may be strided (the
+    heads of a token are not); its token stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor, got %r" % (name, type(t)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
+    dim = cache.head_dim
+    if t.shape != (batch.tokens, heads, dim):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (batch.tokens, heads, dim)))
+    stride = t.stride()
+    if batch.tokens and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    if t.device != cache.device:
+        raise ValueError("%s is on %s, the cache on %s" % (name, t.device, cache.device))
+    return stride[0] if batch.tokens > 1 else heads * dim
+
+
+def _kv_pair(cache, batch):
+    if not isinstance(cache, KvCache) or not isinstance(batch, KvBatch):
+        raise TypeError("expected a KvCache and a KvBatch")
+    if cache.device != batch.device:
+        raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
+
+
+def nvfp4_kv_append(cache, batch, K, V, stream=None):
+    _kv_pair(cache, batch)
+    ks = _rows("K", K, cache, batch, cache.heads, _KV_DTYPE)
+    vs = _rows("V", V, cache, batch, cache.heads, (K.dtype,))
+    _check(load().nvfp4_kv_append(cache._ref, batch._ref, _KV_DTYPE[K.dtype], K.data_ptr(), ks, V.data_ptr(), vs,
+                                  _stream(stream, K)), "nvfp4_kv_append")
+
+
+def nvfp4_kv_read(cache, batch, K=None, V=None, stream=None):
+    _kv_pair(cache, batch)
+    given = [t for t in (K, V) if t is not None]
+    if not given:
+        raise ValueError("K or V is required")
+    ks, vs = (0 if t is None else _rows(n, t, cache, batch, cache.heads, _KV_DTYPE) for n, t in (("K", K), ("V", V)))
+    if given[0].dtype != given[-1].dtype:
+        raise ValueError("K is %s, V %s" % (K.dtype, V.dtype))
+    _check(load().nvfp4_kv_read(cache._ref, batch._ref, _KV_DTYPE[given[0].dtype],
+                                None if K is None else K.data_ptr(), ks, None if V is None else V.data_ptr(), vs,
+                                _stream(stream, given[0])), "nvfp4_kv_read")
+
+
+def nvfp4_kv_attention_workspace_bytes(cache, batch, q_heads) -> int:
+    _kv_pair(cache, batch)
+    return int(load().nvfp4_kv_attention_workspace_bytes(cache._ref, batch._ref, int(q_heads)))
+
+
+def nvfp4_kv_attention(cache, batch, Q, scale, out, lse=None, window=0, tree=None, workspace=None, stream=None):
+    """Attention of the batch's new tokens over the cache: Q and out bfloat16
+    [tokens, q_heads, head_dim], lse float32 [tokens, q_heads] or None, tree int64
+    [tokens] (bit patterns) or None."""
+    _kv_pair(cache, batch)
+    heads = Q.shape[1] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else 0
+    qs = _rows("Q", Q, cache, batch, heads, _BF16[:1])
+    os_ = _rows("out", out, cache, batch, heads, _BF16[:1])
+    for name, t, dtype, n in (("lse", lse, torch.float32, batch.tokens * heads), ("tree", tree, torch.int64, batch.tokens)):
+        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_contiguous() and
+                                  t.numel() >= n and t.device == cache.device):
+            raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (name, dtype, n, cache.device))
+    nbytes = 0
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.device != cache.device:
+            raise ValueError("workspace must be contiguous, on %s" % cache.device)
+        nbytes = workspace.numel() * workspace.element_size()
+    _check(load().nvfp4_kv_attention(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale), int(window),
+                                     None if tree is None else tree.data_ptr(), out.data_ptr(), os_,
+                                     None if lse is None else lse.data_ptr(),
+                                     workspace.data_ptr() if nbytes else None, nbytes, _stream(stream, Q)),
+           "nvfp4_kv_attention")

@@ -1,0 +1,185 @@
+// nvfp4_attn.h -- what the attention kernels over the paged cache share: their
+// arguments, the map from workgroups to rows and keys, the loads and decodes of a
+// 16-token unit as matrix operands, and the softmax state.  Internal to the
+// library.
+//
+// Both kernels compute S^T = K Q^T with keys as the rows of the A operand and query
+// rows as the columns of B, and O^T = V^T P^T.  The accumulator of the first product
+// then holds, in one lane, several keys of one query row: row sums and rescales
+// need no other lane, and the exponentials, rounded to bf16, are the B operand of the
+// second product as they stand (the order of keys in that contraction is chosen to
+// match, and the cache's value layout with it).
+#pragma once
+
+#include "nvfp4_kv.h"
+
+namespace nvfp4 {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNegInf = -__builtin_inff();
+
+// A running maximum is moved only when a score passes it by more than this (in
+// powers of two): the weights then reach 2^8 at most, far inside fp32 and with
+// bf16's relative rounding unchanged, and most tiles rescale nothing.
+constexpr float kMaxSlack = 8.0f;
+
+struct AttnArgs {
+    KvView kv;
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    const unsigned long long *tree;
+    int64_t q_stride, out_stride;
+    int q_heads, group;
+    int window;
+    float scale_log2;      // scale * log2(e)
+    int split_keys;        // keys of a split (a multiple of the kernels' tiles), and how many splits
+    int splits;
+    float *part_o;         // [splits][tokens * q_heads][D], relative to 2^m
+    float *part_ml;        // [splits][tokens * q_heads][4]: m (base 2), l, lr, unused
+};
+
+// One workgroup's rows: rows (token, head of the group) of one sequence, token
+// major, in tiles of TR; tile t of sequence s is work item
+// floor(offsets[s] * group / TR) + s + t, so items are found without a prefix sum
+// over the sequences (some items have no tile).
+struct RowTile {
+    int s;                 // sequence
+    int begin;             // its first token row
+    int n;                 // its new tokens
+    int past;
+    int row0, rows;        // first row of the tile, and the sequence's rows
+    int lo, hi;            // the keys that some row of the tile may see: lo <= j < hi
+    int inner_lo, inner_hi;  // the keys that every row sees (by position)
+    bool some;             // whether the item has a tile
+};
+
+template <int TR>
+__host__ __device__ __forceinline__ int64_t tile_items(int64_t tokens, int group, int seqs) {
+    return tokens * group / TR + seqs;
+}
+
+__device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int item, int tile_rows) {
+    const KvView &v = a.kv;
+    RowTile r;
+    const int c = wave_count_le(v.seqs, item, [&](int s) {
+        return int64_t(min(max(v.offsets[s], 0), v.tokens)) * a.group / tile_rows + s;
+    });
+    r.s = __builtin_amdgcn_readfirstlane(max(c - 1, 0));
+    int end;
+    v.sequence(r.s, r.begin, end, r.past);
+    r.n = end - r.begin;
+    r.rows = r.n * a.group;
+    const int tile = item - (int(int64_t(r.begin) * a.group / tile_rows) + r.s);
+    r.row0 = tile * tile_rows;
+    r.some = c > 0 && tile >= 0 && r.row0 < r.rows;
+    const int first = r.some ? r.row0 / a.group : 0;
+    const int last = r.some ? min(r.row0 + tile_rows, r.rows) - 1 : 0;
+    const int i1 = last / a.group;
+    r.lo = a.window > 0 ? max(0, r.past + first + 1 - a.window) : 0;
+    r.hi = min(a.tree ? r.past + r.n : r.past + i1 + 1, v.capacity);
+    r.inner_lo = a.window > 0 ? max(0, r.past + i1 + 1 - a.window) : 0;
+    r.inner_hi = min(a.tree ? r.past : r.past + first + 1, v.capacity);
+    return r;
+}
+
+// The keys of split z of a tile's range, as [lo, hi) with lo a multiple of 64 but
+// for rounding down of the range's start; the last split takes what is left.
+struct KeyRange {
+    int lo, hi, splits;
+};
+__device__ __forceinline__ KeyRange key_range(const AttnArgs &a, const RowTile &r, int z) {
+    KeyRange k;
+    const int base = r.lo & ~63;
+    const int all = max(r.hi - base, 0);
+    k.splits = min((all + a.split_keys - 1) / a.split_keys, a.splits);
+    k.lo = base + z * a.split_keys;
+    k.hi = z + 1 >= k.splits ? r.hi : k.lo + a.split_keys;
+    return k;
+}
+
+// Eight codes -> the bf16 operand, times the power of two in `unit`'s exponent.
+__device__ __forceinline__ bf16x8 codes8(uint32_t lo, uint32_t hi, float unit) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, unit, false);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(lo, unit, true);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, unit, false);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(hi, unit, true);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+__device__ __forceinline__ bf16x8 codes4(uint32_t w, float unit) {
+    const bf16x2 a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 0);
+    const bf16x2 b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 1);
+    const bf16x2 c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 2);
+    const bf16x2 d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, unit, 3);
+    return bf16x8{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+// Byte `i` of `w` as the fp32 whose exponent field it is.
+__device__ __forceinline__ float unit_of_byte(uint32_t w, int i) {
+    return __uint_as_float(__builtin_amdgcn_ubfe(w, 8 * i, 8) << 23);
+}
+
+// A load of BYTES per lane into words.
+template <int BYTES>
+__device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
+    if constexpr (BYTES == 16) {
+        const u32x4 t = *reinterpret_cast<const u32x4 *>(p);
+        w[0] = t[0]; w[1] = t[1]; w[2] = t[2]; w[3] = t[3];
+    } else if constexpr (BYTES == 8) {
+        const u32x2 t = *reinterpret_cast<const u32x2 *>(p);
+        w[0] = t[0]; w[1] = t[1];
+    } else if constexpr (BYTES == 4) {
+        w[0] = *reinterpret_cast<const uint32_t *>(p);
+    } else {
+        w[0] = *reinterpret_cast<const uint16_t *>(p);
+    }
+}
+
+// Two elements (2 jp, 2 jp + 1 of a row's D / 16) of token i of a lane's quad.
+template <int D, int BITS>
+__device__ __forceinline__ uint32_t value_pair(const uint32_t *w, int i, int jp, float unit) {
+    if constexpr (BITS == 8) {
+        const uint32_t x = w[i * (D / 64) + jp / 2];
+        return jp & 1 ? as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, unit, true))
+                      : as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(x, unit, false));
+    } else {
+        const int byte = i * (D / 32) + jp;
+        const uint32_t x = w[byte / 4];
+        switch (byte & 3) {
+            case 0: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, unit, 0));
+            case 1: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, unit, 1));
+            case 2: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, unit, 2));
+            default: return as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(x, unit, 3));
+        }
+    }
+}
+
+// Low and high halves of a pair of words side by side.
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
+__device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
+    bf16x2 v;
+    v[0] = static_cast<__bf16>(a);
+    v[1] = static_cast<__bf16>(b);
+    return as_u32(v);
+}
+
+// sum + the two halves of a packed bf16 pair.
+__device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
+    return __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(pair), as_bf16x2(0x3F803F80u), sum, false);
+}
+
+// log(sum of exponentials) from a base-2 maximum and the sum relative to it.
+__device__ __forceinline__ float lse_of(float m, float l) {
+    return m == kNegInf && l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+}
+
+// What the launchers are given: the arguments and the grid's first two extents.
+int launch_attn_narrow(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream);
+int launch_attn_join(const AttnArgs &a, int dim, int tile_rows, hipStream_t stream);
+
+}  // namespace nvfp4

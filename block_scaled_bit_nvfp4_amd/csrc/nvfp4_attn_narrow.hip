@@ -1,0 +1,382 @@
+// nvfp4_attn_narrow.hip -- attention of few query rows over the paged cache
+// (decode, speculative verify) on gfx950.
+#include "nvfp4_attn.h"
+
+namespace nvfp4 {
+
+constexpr int kNarrowWaves = 4;
+constexpr int kTileKeys = 32;      // keys of a wave's tile: two units
+
+// The operands of one 32-key tile as loaded.
+template <int D, int KB, int VB>
+struct NarrowTile {
+    typedef KvSide<D, KB> KS;
+    typedef KvSide<D, VB> VS;
+    static constexpr int kLoads = KS::kPieces / 4;
+    uint32_t k[2][kLoads][KS::kPiece / 4];
+    uint32_t ks[2][(KS::kBlocks + 3) / 4];
+    uint32_t v[2][VS::kSlots * VS::kSlot / 4];
+    uint32_t vs[2];
+    bool some[2];                  // the unit has a page (wave-uniform)
+
+    __device__ __forceinline__ void load(const KvView &kv, int s, int head, int key) {
+        const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int pos = key + u * kKvUnit;
+            const int page = kv.page_of(s, pos);
+            some[u] = page >= 0;
+            const int64_t unit = kv.unit_of(max(page, 0), head, pos);
+            const uint8_t *kc = kv.codes[0] + unit * KS::kUnitCodes + lane * KS::kPiece;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) load_words<KS::kPiece>(kc + j * kLanes * KS::kPiece, k[u][j]);
+            load_words<KS::kBlocks>(kv.scales[0] + unit * KS::kUnitScales + r * KS::kBlocks, ks[u]);
+            const uint8_t *vc = kv.codes[1] + unit * VS::kUnitCodes + lane * VS::kSlot;
+#pragma unroll
+            for (int j = 0; j < VS::kSlots; ++j) load_words<VS::kSlot>(vc + j * kLanes * VS::kSlot, &v[u][j * (VS::kSlot / 4)]);
+            load_words<4>(kv.scales[1] + unit * VS::kUnitScales + (g * VS::kBlocks + r * VS::kBlocks / 16) * 4, &vs[u]);
+        }
+    }
+};
+
+template <int D, int KB, int VB, int NT>
+__global__ void __launch_bounds__(kNarrowWaves * kLanes)
+    attn_narrow_kernel(AttnArgs a) {
+    typedef KvSide<D, KB> KS;
+    constexpr int TR = 16 * NT;
+    constexpr int kSlices = D / 32;            // MFMAs of one unit's scores
+    constexpr int kRowDims = D / 16;           // elements of a value row
+    const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const RowTile tile = row_tile(a, blockIdx.x, TR);
+    if (!tile.some) return;
+    const int head = blockIdx.y, z = blockIdx.z;
+    const KeyRange keys = key_range(a, tile, z);
+    if (z > 0 && z >= keys.splits) return;
+
+    // The rows of this lane's columns, and their query operands.
+    bf16x8 q[NT][kSlices];
+    int token[NT], qhead[NT], klo[NT], khi[NT];
+    unsigned long long tree[NT];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        const int row = tile.row0 + 16 * t + c;
+        const bool in = row < tile.rows;
+        const int i = in ? row / a.group : 0;
+        token[t] = in ? tile.begin + i : -1;
+        qhead[t] = head * a.group + (in ? row - i * a.group : 0);
+        const int pos = tile.past + i;
+        klo[t] = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+        khi[t] = in ? (a.tree ? tile.past : pos + 1) : 0;
+        tree[t] = in && a.tree ? a.tree[token[t]] : 0ull;
+        const uint16_t *src = a.q + max(token[t], 0) * a.q_stride + qhead[t] * D;
+#pragma unroll
+        for (int m = 0; m < kSlices; ++m) {
+            // slice m takes the lane's m-th group of eight elements of its pieces
+            constexpr int per = KS::kPieceDims / 8;
+            const int d = (4 * (m / per) + g) * KS::kPieceDims + 8 * (m % per);
+            u32x4 w = {0, 0, 0, 0};
+            if (in) w = *reinterpret_cast<const u32x4 *>(src + d);
+            q[t][m] = __builtin_bit_cast(bf16x8, w);
+        }
+    }
+
+    floatx4 o[NT][kRowDims];
+    float mx[NT], sub[NT], l[NT], lr[NT];     // lr: the sum of the weights as rounded, which normalises the outputs
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        mx[t] = kNegInf; sub[t] = 0.0f; l[t] = 0.0f; lr[t] = 0.0f;
+#pragma unroll
+        for (int j = 0; j < kRowDims; ++j) o[t][j] = floatx4{0, 0, 0, 0};
+    }
+
+    const auto step = [&](const NarrowTile<D, KB, VB> &x, int key, auto edge_tag) {
+        constexpr bool EDGE = decltype(edge_tag)::value != 0;
+        // scores of two units: lane (g, c) has keys 4 g + i of each, row c
+        floatx4 s[NT][2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) s[t][u] = floatx4{0, 0, 0, 0};
+#pragma unroll
+            for (int m = 0; m < kSlices; ++m) {
+                constexpr int per = KS::kPieceDims / 8;
+                const int j = m / per, e = m % per;
+                // the block of piece 4 j + g; the four lanes' blocks of a piece never cross a word
+                const int block = ((4 * j + g) * KS::kPieceDims) / kMxBlock;
+                const float unit = unit_of_byte(x.ks[u][4 * j * KS::kPieceDims / kMxBlock / 4], block & 3);
+                bf16x8 k;
+                if constexpr (KB == 8) k = codes8(x.k[u][j][2 * e], x.k[u][j][2 * e + 1], unit);
+                else k = codes4(x.k[u][j][e], unit);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) s[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[t][m], s[t][u], 0, 0, 0);
+            }
+        }
+        uint32_t ones[NT][4];                  // EDGE: the allowed keys as a bf16 operand of ones
+        uint32_t p[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            float f[8];
+            float top = kNegInf;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                f[i] = s[t][i >> 2][i & 3] * a.scale_log2;
+                if constexpr (EDGE) {
+                    const int pos = key + (i >> 2) * kKvUnit + 4 * g + (i & 3);
+                    bool ok = pos >= klo[t] && pos < khi[t];
+                    if (a.tree) {
+                        const int b = pos - tile.past;
+                        ok = ok || (b >= 0 && b < tile.n && b < 64 && ((tree[t] >> (b & 63)) & 1));
+                    }
+                    ok = ok && x.some[i >> 2] && pos < tile.hi;
+                    if (!ok) f[i] = kNegInf;
+                    const uint32_t one = ok ? 0x3F80u : 0u;
+                    if (i & 1) ones[t][i >> 1] |= one << 16;
+                    else ones[t][i >> 1] = one;
+                }
+                top = fmaxf(top, f[i]);
+            }
+            if (__any(top > mx[t] + kMaxSlack)) {
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32));
+                const float m = fmaxf(mx[t], top);
+                const float by = m == mx[t] ? 1.0f : exp2_fast(mx[t] - m);
+                mx[t] = m;
+                sub[t] = m == kNegInf ? 0.0f : m;
+                l[t] *= by;
+                lr[t] *= by;
+#pragma unroll
+                for (int j = 0; j < kRowDims; ++j) o[t][j] *= by;
+            }
+            float e[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                e[i] = exp2_fast(f[i] - sub[t]);
+                l[t] += e[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                p[t][i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+                lr[t] = add_pair(p[t][i], lr[t]);
+            }
+        }
+        // values: the lane's row holds D / 16 elements of eight keys; two
+        // elements of a key come at a time and are paired over keys
+        uint32_t keep[2] = {~0u, ~0u};         // EDGE: per token a byte of ones where its values count
+        uint32_t bad = 0;                      // EDGE: bit i where key slot i's block is NaN
+        if constexpr (EDGE) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int pos = key + u * kKvUnit + 4 * g + i;
+                    const bool held = x.some[u] && pos >= tile.lo && pos < tile.hi;
+                    const bool nan = ((x.vs[u] >> (8 * i)) & 0xFFu) == 0xFFu;
+                    if (!held || nan) keep[u] &= ~(0xFFu << (8 * i));
+                    if (held && nan) bad |= 1u << (4 * u + i);
+                }
+        }
+#pragma unroll
+        for (int jp = 0; jp < kRowDims / 2; ++jp) {
+            uint32_t w[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    w[u][i] = value_pair<D, VB>(x.v[u], i, jp, unit_of_byte(x.vs[u], i));
+                    if constexpr (EDGE) w[u][i] = (keep[u] >> (8 * i)) & 1u ? w[u][i] : 0u;
+                }
+            const u32x4 even = {low_halves(w[0][0], w[0][1]), low_halves(w[0][2], w[0][3]),
+                                low_halves(w[1][0], w[1][1]), low_halves(w[1][2], w[1][3])};
+            const u32x4 odd = {high_halves(w[0][0], w[0][1]), high_halves(w[0][2], w[0][3]),
+                               high_halves(w[1][0], w[1][1]), high_halves(w[1][2], w[1][3])};
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[t][0], p[t][1], p[t][2], p[t][3]});
+                o[t][2 * jp] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), pb, o[t][2 * jp], 0, 0, 0);
+                o[t][2 * jp + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), pb, o[t][2 * jp + 1], 0, 0, 0);
+            }
+        }
+        if constexpr (EDGE) {
+            // A NaN block counts only for the rows that see its key: its values
+            // were left out above (zero weights times NaN would reach every
+            // row), and a product of the NaN marks with the allowed keys says
+            // which rows and elements are NaN.
+            if (__any(bad != 0)) {
+                u32x4 mark;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mark[i] = ((bad >> (2 * i)) & 1 ? 0x3F80u : 0u) | ((bad >> (2 * i + 1)) & 1 ? 0x3F800000u : 0u);
+#pragma unroll
+                for (int t = 0; t < NT; ++t) {
+                    const bf16x8 on = __builtin_bit_cast(bf16x8, u32x4{ones[t][0], ones[t][1], ones[t][2], ones[t][3]});
+                    const floatx4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, mark), on, floatx4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (n[i] > 0.0f)
+#pragma unroll
+                            for (int j = 0; j < kRowDims; ++j) o[t][j][i] = __builtin_nanf("");
+                }
+            }
+        }
+    };
+
+    for (int key = keys.lo + wave * kTileKeys; key < keys.hi; key += kNarrowWaves * kTileKeys) {
+        NarrowTile<D, KB, VB> x;
+        x.load(a.kv, tile.s, head, key);
+        const bool inner = key >= tile.inner_lo && key + kTileKeys <= min(tile.inner_hi, keys.hi) && x.some[0] && x.some[1];
+        if (inner) step(x, key, IntC<0>());
+        else step(x, key, IntC<1>());
+    }
+
+    // Join the four waves: their maxima and sums, then their outputs, kRowDims in
+    // parts of at most 8 to bound the shared memory.
+    constexpr int kPart = kRowDims < 8 ? kRowDims : 8;
+    constexpr int kCols = 16 * kPart + 4;              // floats of one row's part, padded against bank conflicts
+    __shared__ float sm[kNarrowWaves][TR], sl[kNarrowWaves][TR], sr[kNarrowWaves][TR];
+    __shared__ float so[kNarrowWaves][16][kCols];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        l[t] += __shfl_xor(l[t], 16);
+        l[t] += __shfl_xor(l[t], 32);
+        lr[t] += __shfl_xor(lr[t], 16);
+        lr[t] += __shfl_xor(lr[t], 32);
+        if (g == 0) {
+            sr[wave][16 * t + c] = lr[t];
+            sm[wave][16 * t + c] = mx[t];
+            sl[wave][16 * t + c] = l[t];
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+        float m = kNegInf;
+#pragma unroll
+        for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, sm[w][16 * t + c]);
+        const float by = mx[t] == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mx[t] - m);
+#pragma unroll
+        for (int part = 0; part < kRowDims / kPart; ++part) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < kPart; ++j) so[wave][c][(4 * g + i) * kPart + j] = o[t][part * kPart + j][i] * by;
+            __syncthreads();
+            // thread (row, piece): kPart / ... elements of one row
+            constexpr int kEach = 16 * kPart / 16;
+            const int row16 = threadIdx.x >> 4, piece = threadIdx.x & 15;
+            const int row = tile.row0 + 16 * t + row16;
+            if (row < tile.rows) {
+                float mm = kNegInf, ll = 0.0f, rr = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kNarrowWaves; ++w) mm = fmaxf(mm, sm[w][16 * t + row16]);
+#pragma unroll
+                for (int w = 0; w < kNarrowWaves; ++w) {
+                    const float mw = sm[w][16 * t + row16];
+                    const float by = mw == kNegInf ? (mm == kNegInf ? 1.0f : 0.0f) : exp2_fast(mw - mm);
+                    ll += sl[w][16 * t + row16] * by;
+                    rr += sr[w][16 * t + row16] * by;
+                }
+                float y[kEach];
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) {
+                    y[j] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < kNarrowWaves; ++w) y[j] += so[w][row16][piece * kEach + j];
+                }
+                const int i = row / a.group;
+                const int64_t at = int64_t(tile.begin + i) * a.q_heads + head * a.group + (row - i * a.group);
+                const int d = piece * kRowDims + part * kPart;
+                if (keys.splits > 1) {
+                    float *dst = a.part_o + (int64_t(z) * a.kv.tokens * a.q_heads + at) * D + d;
+#pragma unroll
+                    for (int j = 0; j < kEach; ++j) dst[j] = y[j];
+                    if (piece == 0 && part == 0) {
+                        float *ml = a.part_ml + (int64_t(z) * a.kv.tokens * a.q_heads + at) * 4;
+                        *reinterpret_cast<float4 *>(ml) = float4{mm, ll, rr, 0.0f};
+                    }
+                } else {
+                    const float inv = mm == kNegInf && ll == 0.0f ? 0.0f : 1.0f / rr;
+                    uint16_t *dst = a.out + int64_t(tile.begin + i) * a.out_stride + (head * a.group + (row - i * a.group)) * D + d;
+#pragma unroll
+                    for (int j = 0; j < kEach; j += 2)
+                        *reinterpret_cast<uint32_t *>(dst + j) = pack_bf16(y[j] * inv, y[j + 1] * inv);
+                    if (a.lse && piece == 0 && part == 0) a.lse[at] = lse_of(mm, ll);
+                }
+            }
+            __syncthreads();
+        }
+    }
+}
+
+// --------------------------------------------------------------------- join
+
+// One thread takes four elements of a row: sums the row's splits in order.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int tile_rows) {
+    constexpr int kThreads = D / 4;            // of one row
+    const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int64_t rows = int64_t(a.kv.tokens) * a.q_heads;
+    const int64_t at = min(u / kThreads, rows - 1);
+    const int d = int(u % kThreads) * 4;
+    const int token = int(at / a.q_heads), qhead = int(at - int64_t(token) * a.q_heads);
+    const int t0 = __builtin_amdgcn_readfirstlane(token);
+    const KvView &v = a.kv;
+    int s = max(wave_count_le(v.seqs, t0, [&](int i) { return v.offsets[i]; }) - 1, 0);
+    while (s + 1 < v.seqs && v.offsets[s + 1] <= token) ++s;
+    int begin, end, past;
+    v.sequence(s, begin, end, past);
+    if (u >= rows * kThreads || token < begin || token >= end) return;
+    // the tile that the row was in, and so its splits
+    const int row = (token - begin) * a.group + qhead % a.group;
+    const int first = row / tile_rows * tile_rows;
+    const int n = end - begin;
+    RowTile r;
+    const int i0 = first / a.group, i1 = (min(first + tile_rows, n * a.group) - 1) / a.group;
+    r.lo = a.window > 0 ? max(0, past + i0 + 1 - a.window) : 0;
+    r.hi = min(a.tree ? past + n : past + i1 + 1, v.capacity);
+    const int splits = key_range(a, r, 0).splits;
+    if (splits <= 1) return;
+    float m = kNegInf;
+    for (int z = 0; z < splits; ++z) m = fmaxf(m, a.part_ml[(z * rows + at) * 4]);
+    float l = 0.0f, lr = 0.0f, y[4] = {0, 0, 0, 0};
+    for (int z = 0; z < splits; ++z) {
+        const float4 part = *reinterpret_cast<const float4 *>(a.part_ml + (z * rows + at) * 4);
+        const float mz = part.x;
+        const float by = mz == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mz - m);
+        const float4 o = *reinterpret_cast<const float4 *>(a.part_o + (z * rows + at) * D + d);
+        l += part.y * by;
+        lr += part.z * by;
+        y[0] += o.x * by; y[1] += o.y * by; y[2] += o.z * by; y[3] += o.w * by;
+    }
+    const float inv = m == kNegInf && l == 0.0f ? 0.0f : 1.0f / lr;
+    uint16_t *dst = a.out + token * a.out_stride + qhead * D + d;
+    *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
+    if (a.lse && d == 0) a.lse[at] = lse_of(m, l);
+}
+
+int launch_attn_join(const AttnArgs &a, int dim, int tile_rows, hipStream_t stream) {
+    return kv_dim(dim, [&](auto tag) {
+        constexpr int D = decltype(tag)::value;
+        const int64_t grid = ceil_div(int64_t(a.kv.tokens) * a.q_heads * (D / 4), 256);
+        if (grid >= kMaxGrid / 256) return NVFP4_ESHAPE;
+        attn_join_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a, tile_rows);
+        return launch_status();
+    });
+}
+
+int launch_attn_narrow(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream) {
+    return kv_dim(dim, [&](auto d) {
+        return kv_bits(k_format, [&](auto k) {
+            return kv_bits(v_format, [&](auto v) {
+                constexpr int D = decltype(d)::value, K = decltype(k)::value, V = decltype(v)::value;
+                const int64_t items = tile_items<16>(a.kv.tokens, a.group, a.kv.seqs);
+                if (items >= kMaxGrid / (kNarrowWaves * kLanes)) return NVFP4_ESHAPE;
+                attn_narrow_kernel<D, K, V, 1><<<dim3(unsigned(items), unsigned(a.kv.heads), unsigned(a.splits)),
+                                                 kNarrowWaves * kLanes, 0, stream>>>(a);
+                return launch_status();
+            });
+        });
+    });
+}
+
+}  // namespace nvfp4

@@ -314,6 +314,123 @@ int mxfp4_dequant(const uint8_t *wq, const uint8_t *ws, float tscale, int64_t ro
 int mxfp4_gemv(const uint8_t *wq, const uint8_t *ws, float tscale, int64_t rows, int64_t cols,
                const uint16_t *X, int n, float *Y, hipStream_t stream);
 
+/* ------------------------------------------- paged, quantised key/value cache
+ * What a decode, verify or prefill step needs beside its products: the new
+ * tokens' keys and values are quantised into a paged cache as they are written
+ * (nvfp4_kv_append), attention reads the cache (nvfp4_kv_attention), and
+ * nvfp4_kv_read gives it back (the pages' engines attend over FP8 and 4-bit
+ * caches with a split key axis and lengths that live on the device: bw24 wiki,
+ * feature list; qwentin README, "How it works").
+ *
+ * Elements.  Keys and values are microscaled: E4M3 codes (NVFP4_KV_MXFP8) or
+ * E2M1 codes (NVFP4_KV_MXFP4), chosen for each side, with one E8M0 scale byte
+ * b (2^(b - 127), 0xFF NaN) per 32 consecutive elements of a token's head
+ * vector.  Power-of-two scales make every value code * 2^(b - 127) a bf16
+ * value, which the matrix cores multiply exactly.  A block with largest
+ * magnitude a gets b = 127 + E, E clamped to [-127, 127]:
+ *   MXFP4: E = floor(log2(a)) - 2, codes saturating at 6 (mxfp4_quantize's rule);
+ *   MXFP8: the least E with a <= 448 * 2^E (E4M3 has exponents to spare, so the
+ *          larger unit costs nothing, while saturating would cost the largest
+ *          element up to 1/8);
+ * a = 0 gives E = -127; codes are nearest, ties to the even code.  A block that
+ * holds an infinity or a NaN gets b = 0xFF and zero codes: it reads as NaN.
+ *
+ * Pool.  `pages` pages of page_tokens tokens (a power of two, 16..1024); a page
+ * holds each head's tokens in units of 16: code planes
+ * uint8 [pages][heads][page_tokens / 16][16 * D * bits / 8], scale planes
+ * uint8 [pages][heads][page_tokens / 16][16 * D / 32], D = head_dim = 64, 128 or
+ * 256.  Within a unit the bytes stand in the order in which the attention's
+ * matrix operands take them:
+ *   key codes    [piece][16 tokens][16 bytes]: 16 bytes of a token's codes (8
+ *                for MXFP4 at D = 64); element k sits in byte k (MXFP8) or k / 2
+ *                (MXFP4, the low nibble when k is even) of the token's codes;
+ *   key scales   [16 tokens][D / 32];
+ *   value codes  [slot][4 quads][16 rows][tokens of a slot][D / 16 elements]:
+ *                row r holds elements r * D / 16 .. of a token; token
+ *                4 * quad + slot * (tokens of a slot) + t; a slot has as many of
+ *                a quad's 4 tokens as fit 16 bytes;
+ *   value scales [4 quads][D / 32][4 tokens].
+ *
+ * Batch.  The new tokens of `seqs` sequences stand one after another: rows
+ * offsets[s] .. offsets[s + 1] - 1 are sequence s's, and its first new token has
+ * position past[s].  Position p of sequence s lives in page
+ * page_table[s * table_width + p / page_tokens].  An entry outside 0..pages - 1,
+ * and a position past the table, names no page: tokens appended there are
+ * dropped, read as zeros and attended by nobody (a table may so leave out pages
+ * that have left every window).  No page may be named twice for tokens that one
+ * append writes.  The arrays are device memory, read by the kernels when
+ * they run, so a captured graph follows their contents; their values are
+ * checked there (offsets are clamped to 0..tokens, past to the table's
+ * positions).  max_new and max_context are upper bounds of any sequence's new
+ * tokens and of past + new, known to the host: they pick the launch's shape and
+ * never the results' correctness. */
+#define NVFP4_KV_MXFP4 4
+#define NVFP4_KV_MXFP8 8
+
+/* Element types of nvfp4_kv_append's inputs and nvfp4_kv_read's outputs. */
+#define NVFP4_KV_BF16 0
+#define NVFP4_KV_F32 1
+
+typedef struct nvfp4_kv_cache {
+    uint8_t *k_codes, *k_scales, *v_codes, *v_scales;   /* planes, 16-byte aligned */
+    int32_t k_format, v_format;                         /* NVFP4_KV_MXFP8 or NVFP4_KV_MXFP4 */
+    int32_t pages, page_tokens, heads, head_dim;
+} nvfp4_kv_cache;
+
+typedef struct nvfp4_kv_batch {
+    const int32_t *page_table;      /* [seqs][table_width] */
+    const int32_t *offsets;         /* [seqs + 1], not decreasing, from 0 */
+    const int32_t *past;            /* [seqs] */
+    int64_t tokens;                 /* rows of the inputs and outputs */
+    int32_t seqs, table_width;
+    int32_t max_new, max_context;   /* upper bounds over the sequences */
+} nvfp4_kv_batch;
+
+/* Bytes of one side's planes of a pool in `format` (0 for an invalid shape). */
+size_t nvfp4_kv_code_bytes(int format, int32_t pages, int32_t page_tokens, int32_t heads, int32_t head_dim);
+size_t nvfp4_kv_scale_bytes(int format, int32_t pages, int32_t page_tokens, int32_t heads, int32_t head_dim);
+
+/* Quantise the new tokens' keys and values into the cache: k and v are
+ * [tokens][heads][head_dim] of `dtype`, k_stride and v_stride elements from one
+ * token to the next (at least heads * head_dim; they may be column ranges of one
+ * projection's output).  Pointers 16-byte aligned, strides multiples of 16
+ * bytes, else NVFP4_EALIGN. */
+int nvfp4_kv_append(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int dtype, const void *k,
+                    int64_t k_stride, const void *v, int64_t v_stride, hipStream_t stream);
+
+/* The values that the cache holds for the batch's tokens (positions past[s] ..),
+ * to k and v laid out as nvfp4_kv_append's inputs; exact in either type.  Either
+ * may be NULL, not both. */
+int nvfp4_kv_read(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int dtype, void *k, int64_t k_stride,
+                  void *v, int64_t v_stride, hipStream_t stream);
+
+/* Attention of the batch's new tokens (whose keys and values have been appended)
+ * over their sequences: for token i of sequence s, at position p = past[s] + i,
+ * and query head h, with key/value head h / (q_heads / heads),
+ *   z_j = scale * sum_d q[d] * k_j[d] over the allowed positions j,
+ *   out[d] = sum_j exp(z_j) v_j[d] / sum_j exp(z_j),  lse = log sum_j exp(z_j).
+ * Allowed are j <= p, with window > 0 only j > p - window, and with `tree` (one
+ * word per new token; at most 64 new tokens per sequence, window 0) the
+ * positions before past[s] and past[s] + b for each set bit b of the token's
+ * word -- the ancestors of a drafted token in a speculative verify.  A token with
+ * nothing allowed gets zeros and lse = -infinity.  What stands in masked or
+ * unwritten places, NaN too, does not reach the outputs.
+ *   q   bf16 bits [tokens][q_heads][head_dim], q_stride elements between tokens;
+ *   out bf16 bits, the same with out_stride;  lse fp32 [tokens][q_heads] or NULL.
+ * q_heads is a multiple of heads, scale finite and > 0; q and out 16-byte
+ * aligned with strides of whole 16 bytes, lse 4-byte, tree 8-byte aligned.
+ * Products accumulate in fp32 and the softmax is fp32; its weights are rounded to
+ * bf16 for the second product.  Sums run in an order fixed by the arguments and the
+ * arrays' values: results are the same bits on every run.
+ * workspace: nvfp4_kv_attention_workspace_bytes bytes (for the same cache shape,
+ * tokens, seqs, max_new, max_context and q_heads; 0 where the key axis is not
+ * split), 16-byte aligned, any contents; not shared by calls that may overlap. */
+size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int q_heads);
+int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, const uint16_t *q,
+                       int64_t q_stride, int q_heads, float scale, int window, const uint64_t *tree,
+                       uint16_t *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
+                       hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
