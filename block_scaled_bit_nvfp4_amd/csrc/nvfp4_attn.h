@@ -15,6 +15,7 @@
 
 namespace nvfp4 {
 
+constexpr int kMaxSplits = 256;     // splits of the key axis (the join's threads)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();

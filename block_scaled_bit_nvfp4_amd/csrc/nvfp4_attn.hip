@@ -4,8 +4,6 @@
 
 namespace nvfp4 {
 
-constexpr int kMaxSplits = 256;
-
 // How the keys are split: as many splits as bring the launch to about kTarget
 // workgroups, none shorter than kLeast keys.
 struct AttnPlan {

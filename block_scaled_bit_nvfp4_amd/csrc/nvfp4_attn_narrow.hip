@@ -310,9 +310,39 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes)
 
 // --------------------------------------------------------------------- join
 
-// One thread takes four elements of a row: sums the row's splits in order.
+// The splits that a row's keys were in (a row's tile decides them), or 0 where
+// the row is no sequence's.
+__device__ __forceinline__ int row_splits(const AttnArgs &a, int token, int qhead, int s, int tile_rows) {
+    const KvView &v = a.kv;
+    int begin, end, past;
+    v.sequence(s, begin, end, past);
+    if (token < begin || token >= end) return 0;
+    const int row = (token - begin) * a.group + qhead % a.group;
+    const int first = row / tile_rows * tile_rows, n = end - begin;
+    const int i0 = first / a.group, i1 = (min(first + tile_rows, n * a.group) - 1) / a.group;
+    RowTile r;
+    r.lo = a.window > 0 ? max(0, past + i0 + 1 - a.window) : 0;
+    r.hi = min(a.tree ? past + n : past + i1 + 1, v.capacity);
+    return key_range(a, r, 0).splits;
+}
+
+__device__ __forceinline__ float split_weight(float mz, float m) {
+    return mz == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mz - m);
+}
+
+__device__ __forceinline__ void store_row4(const AttnArgs &a, int D, int token, int qhead, int d, float m, float l,
+                                           float lr, const float4 &y) {
+    const float inv = m == kNegInf && l == 0.0f ? 0.0f : 1.0f / lr;
+    uint16_t *dst = a.out + token * a.out_stride + qhead * D + d;
+    *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv)};
+    if (a.lse && d == 0) a.lse[int64_t(token) * a.q_heads + qhead] = lse_of(m, l);
+}
+
+// At most kFewSplits splits: a thread takes four elements of a row and all its
+// splits, whose loads go out together.
+constexpr int kFewSplits = 8;
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int tile_rows) {
+__global__ void __launch_bounds__(256) attn_join_few_kernel(AttnArgs a, int tile_rows) {
     constexpr int kThreads = D / 4;            // of one row
     const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int64_t rows = int64_t(a.kv.tokens) * a.q_heads;
@@ -320,46 +350,97 @@ __global__ void __launch_bounds__(256) attn_join_kernel(AttnArgs a, int tile_row
     const int d = int(u % kThreads) * 4;
     const int token = int(at / a.q_heads), qhead = int(at - int64_t(token) * a.q_heads);
     const int t0 = __builtin_amdgcn_readfirstlane(token);
-    const KvView &v = a.kv;
-    int s = max(wave_count_le(v.seqs, t0, [&](int i) { return v.offsets[i]; }) - 1, 0);
-    while (s + 1 < v.seqs && v.offsets[s + 1] <= token) ++s;
-    int begin, end, past;
-    v.sequence(s, begin, end, past);
-    if (u >= rows * kThreads || token < begin || token >= end) return;
-    // the tile that the row was in, and so its splits
-    const int row = (token - begin) * a.group + qhead % a.group;
-    const int first = row / tile_rows * tile_rows;
-    const int n = end - begin;
-    RowTile r;
-    const int i0 = first / a.group, i1 = (min(first + tile_rows, n * a.group) - 1) / a.group;
-    r.lo = a.window > 0 ? max(0, past + i0 + 1 - a.window) : 0;
-    r.hi = min(a.tree ? past + n : past + i1 + 1, v.capacity);
-    const int splits = key_range(a, r, 0).splits;
+    int s = max(wave_count_le(a.kv.seqs, t0, [&](int i) { return a.kv.offsets[i]; }) - 1, 0);
+    while (s + 1 < a.kv.seqs && a.kv.offsets[s + 1] <= token) ++s;
+    const int splits = u < rows * kThreads ? row_splits(a, token, qhead, s, tile_rows) : 0;
     if (splits <= 1) return;
-    float m = kNegInf;
-    for (int z = 0; z < splits; ++z) m = fmaxf(m, a.part_ml[(z * rows + at) * 4]);
-    float l = 0.0f, lr = 0.0f, y[4] = {0, 0, 0, 0};
-    for (int z = 0; z < splits; ++z) {
-        const float4 part = *reinterpret_cast<const float4 *>(a.part_ml + (z * rows + at) * 4);
-        const float mz = part.x;
-        const float by = mz == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mz - m);
-        const float4 o = *reinterpret_cast<const float4 *>(a.part_o + (z * rows + at) * D + d);
-        l += part.y * by;
-        lr += part.z * by;
-        y[0] += o.x * by; y[1] += o.y * by; y[2] += o.z * by; y[3] += o.w * by;
+    float4 part[kFewSplits], o[kFewSplits];
+#pragma unroll
+    for (int z = 0; z < kFewSplits; ++z) {
+        const int64_t from = int64_t(min(z, splits - 1)) * rows + at;
+        part[z] = *reinterpret_cast<const float4 *>(a.part_ml + from * 4);
+        o[z] = *reinterpret_cast<const float4 *>(a.part_o + from * D + d);
     }
-    const float inv = m == kNegInf && l == 0.0f ? 0.0f : 1.0f / lr;
-    uint16_t *dst = a.out + token * a.out_stride + qhead * D + d;
-    *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv)};
-    if (a.lse && d == 0) a.lse[at] = lse_of(m, l);
+    float m = kNegInf;
+#pragma unroll
+    for (int z = 0; z < kFewSplits; ++z) m = fmaxf(m, part[z].x);
+    float l = 0.0f, lr = 0.0f;
+    float4 y = {0, 0, 0, 0};
+#pragma unroll
+    for (int z = 0; z < kFewSplits; ++z) {
+        if (z >= splits) break;
+        const float by = split_weight(part[z].x, m);
+        l += part[z].y * by;
+        lr += part[z].z * by;
+        y.x += o[z].x * by; y.y += o[z].y * by; y.z += o[z].z * by; y.w += o[z].w * by;
+    }
+    store_row4(a, D, token, qhead, d, m, l, lr, y);
+}
+
+// A workgroup of 256 threads takes one row: thread z weighs split z, then groups
+// of D / 4 threads sum every kGroups-th split and meet in shared memory.
+template <int D>
+__global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a, int tile_rows) {
+    constexpr int kThreads = D / 4, kGroups = 256 / kThreads;
+    __shared__ float4 red[4];
+    __shared__ float weight[kMaxSplits];
+    __shared__ float4 sum[kGroups][kThreads];
+    const int64_t rows = int64_t(a.kv.tokens) * a.q_heads, at = blockIdx.x;
+    const int token = int(at / a.q_heads), qhead = int(at - int64_t(token) * a.q_heads);
+    const int s = max(wave_count_le(a.kv.seqs, token, [&](int i) { return a.kv.offsets[i]; }) - 1, 0);
+    const int splits = row_splits(a, token, qhead, s, tile_rows);
+    if (splits <= 1) return;
+    const int tid = threadIdx.x, wave = tid >> 6;
+    float4 part = {kNegInf, 0, 0, 0};
+    if (tid < splits) part = *reinterpret_cast<const float4 *>(a.part_ml + (int64_t(tid) * rows + at) * 4);
+    float m = part.x;
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
+    if ((tid & 63) == 0) red[wave].x = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0].x, red[1].x), fmaxf(red[2].x, red[3].x));
+    const float by = tid < splits ? split_weight(part.x, m) : 0.0f;
+    weight[tid] = by;
+    float l = tid < splits ? part.y * by : 0.0f, lr = tid < splits ? part.z * by : 0.0f;
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2) {
+        l += __shfl_xor(l, k);
+        lr += __shfl_xor(lr, k);
+    }
+    if ((tid & 63) == 0) {
+        red[wave].y = l;
+        red[wave].z = lr;
+    }
+    __syncthreads();
+    l = red[0].y + red[1].y + red[2].y + red[3].y;
+    lr = red[0].z + red[1].z + red[2].z + red[3].z;
+    const int grp = tid / kThreads, d = tid % kThreads * 4;
+    float4 y = {0, 0, 0, 0};
+#pragma unroll 8
+    for (int z = grp; z < splits; z += kGroups) {
+        const float4 o = *reinterpret_cast<const float4 *>(a.part_o + (int64_t(z) * rows + at) * D + d);
+        const float w = weight[z];
+        y.x += o.x * w; y.y += o.y * w; y.z += o.z * w; y.w += o.w * w;
+    }
+    sum[grp][tid % kThreads] = y;
+    __syncthreads();
+    if (grp != 0) return;
+#pragma unroll
+    for (int k = 1; k < kGroups; ++k) {
+        const float4 o = sum[k][tid];
+        y.x += o.x; y.y += o.y; y.z += o.z; y.w += o.w;
+    }
+    store_row4(a, D, token, qhead, d, m, l, lr, y);
 }
 
 int launch_attn_join(const AttnArgs &a, int dim, int tile_rows, hipStream_t stream) {
     return kv_dim(dim, [&](auto tag) {
         constexpr int D = decltype(tag)::value;
-        const int64_t grid = ceil_div(int64_t(a.kv.tokens) * a.q_heads * (D / 4), 256);
+        const int64_t rows = int64_t(a.kv.tokens) * a.q_heads;
+        const int64_t grid = a.splits <= kFewSplits ? ceil_div(rows * (D / 4), 256) : rows;
         if (grid >= kMaxGrid / 256) return NVFP4_ESHAPE;
-        attn_join_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a, tile_rows);
+        if (a.splits <= kFewSplits) attn_join_few_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a, tile_rows);
+        else attn_join_many_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a, tile_rows);
         return launch_status();
     });
 }
