@@ -25,6 +25,12 @@ constexpr float kNegInf = -__builtin_inff();
 // bf16's relative rounding unchanged, and most tiles rescale nothing.
 constexpr float kMaxSlack = 8.0f;
 
+// How a kernel cuts the work: rows of a tile, keys of a split (a multiple of 128),
+// and how many splits at most.
+struct AttnSplit {
+    int tile_rows, keys, splits;
+};
+
 struct AttnArgs {
     KvView kv;
     const uint16_t *q;
@@ -35,8 +41,8 @@ struct AttnArgs {
     int q_heads, group;
     int window;
     float scale_log2;      // scale * log2(e)
-    int split_keys;        // keys of a split (a multiple of the kernels' tiles), and how many splits
-    int splits;
+    AttnSplit split[2];    // narrow kernel's, wide kernel's
+    int narrow_rows;       // sequences of at most so many rows (new tokens x group) are the narrow kernel's
     float *part_o;         // [splits][tokens * q_heads][D], relative to 2^m
     float *part_ml;        // [splits][tokens * q_heads][4]: m (base 2), l, lr, unused
 };
@@ -56,25 +62,37 @@ struct RowTile {
     bool some;             // whether the item has a tile
 };
 
-template <int TR>
-__host__ __device__ __forceinline__ int64_t tile_items(int64_t tokens, int group, int seqs) {
-    return tokens * group / TR + seqs;
+inline int64_t tile_items(int64_t tokens, int group, int seqs, int tile_rows) {
+    return tokens * group / tile_rows + seqs;
 }
 
 __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int item, int tile_rows) {
     const KvView &v = a.kv;
     RowTile r;
-    const int c = wave_count_le(v.seqs, item, [&](int s) {
-        return int64_t(min(max(v.offsets[s], 0), v.tokens)) * a.group / tile_rows + s;
-    });
-    r.s = __builtin_amdgcn_readfirstlane(max(c - 1, 0));
-    int end;
-    v.sequence(r.s, r.begin, end, r.past);
+    // The item's sequence is the last one whose first item is not past it; the
+    // lanes load 64 sequences' facts at once, so the whole search costs one
+    // memory latency for each 64 sequences.
+    const int lane = threadIdx.x & 63;
+    int first_item = -1, end = 0;
+    r.s = r.begin = r.past = 0;
+    for (int base = 0; base < v.seqs; base += kLanes) {
+        const int s = min(base + lane, v.seqs - 1);
+        int begin, stop, past;
+        v.sequence(s, begin, stop, past);
+        const int item0 = int(int64_t(begin) * a.group / tile_rows) + s;
+        const int c = __popcll(__ballot(base + lane < v.seqs && item0 <= item));
+        if (c == 0) break;
+        r.s = base + c - 1;
+        first_item = __builtin_amdgcn_readlane(item0, c - 1);
+        r.begin = __builtin_amdgcn_readlane(begin, c - 1);
+        end = __builtin_amdgcn_readlane(stop, c - 1);
+        r.past = __builtin_amdgcn_readlane(past, c - 1);
+        if (c < kLanes) break;
+    }
     r.n = end - r.begin;
     r.rows = r.n * a.group;
-    const int tile = item - (int(int64_t(r.begin) * a.group / tile_rows) + r.s);
-    r.row0 = tile * tile_rows;
-    r.some = c > 0 && tile >= 0 && r.row0 < r.rows;
+    r.row0 = (item - first_item) * tile_rows;
+    r.some = first_item >= 0 && r.row0 < r.rows;
     const int first = r.some ? r.row0 / a.group : 0;
     const int last = r.some ? min(r.row0 + tile_rows, r.rows) - 1 : 0;
     const int i1 = last / a.group;
@@ -90,13 +108,13 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int item, int til
 struct KeyRange {
     int lo, hi, splits;
 };
-__device__ __forceinline__ KeyRange key_range(const AttnArgs &a, const RowTile &r, int z) {
+__device__ __forceinline__ KeyRange key_range(const AttnSplit &s, const RowTile &r, int z) {
     KeyRange k;
     const int base = r.lo & ~63;
     const int all = max(r.hi - base, 0);
-    k.splits = min((all + a.split_keys - 1) / a.split_keys, a.splits);
-    k.lo = base + z * a.split_keys;
-    k.hi = z + 1 >= k.splits ? r.hi : k.lo + a.split_keys;
+    k.splits = min((all + s.keys - 1) / s.keys, s.splits);
+    k.lo = base + z * s.keys;
+    k.hi = z + 1 >= k.splits ? r.hi : k.lo + s.keys;
     return k;
 }
 
@@ -125,7 +143,7 @@ __device__ __forceinline__ float unit_of_byte(uint32_t w, int i) {
 template <int BYTES>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
     if constexpr (BYTES == 16) {
-        const u32x4 t = *reinterpret_cast<const u32x4 *>(p);
+        const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
         w[0] = t[0]; w[1] = t[1]; w[2] = t[2]; w[3] = t[3];
     } else if constexpr (BYTES == 8) {
         const u32x2 t = *reinterpret_cast<const u32x2 *>(p);
@@ -179,8 +197,11 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return m == kNegInf && l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-// What the launchers are given: the arguments and the grid's first two extents.
+constexpr int kNarrowRows = 16;    // rows of the narrow kernel's tile
+int wide_rows(int dim);            // rows of the wide kernel's
+
 int launch_attn_narrow(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream);
-int launch_attn_join(const AttnArgs &a, int dim, int tile_rows, hipStream_t stream);
+int launch_attn_wide(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream);
+int launch_attn_join(const AttnArgs &a, int dim, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -1,29 +1,69 @@
 // nvfp4_attn.hip -- nvfp4_kv_attention: argument checks, the launch's shape, and
 // the choice of kernel.
+#include <limits.h>
+
+#include <algorithm>
+
 #include "nvfp4_attn.h"
 
 namespace nvfp4 {
 
-// How the keys are split: as many splits as bring the launch to about kTarget
-// workgroups, none shorter than kLeast keys.
+// Sequences of at most so many rows (new tokens x group) go to the narrow kernel.
+constexpr int kNarrowMost = 64;
+constexpr int kCus = 256;
+
+// Which kernels a call needs and how each cuts its work.
 struct AttnPlan {
-    int split_keys, splits;
+    AttnSplit split[2];
+    int narrow_rows;
+    bool narrow, wide;
+    int splits() const { return std::max(split[0].splits, split[1].splits); }
 };
-static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads) {
-    constexpr int64_t kTarget = 1024, kLeast = 256;
-    const int group = q_heads / c->heads;
-    const int64_t tiles = (tile_items<16>(b->tokens, group, 0) + b->seqs) * c->heads;
-    const int64_t context = b->max_context < 1 ? 1 : b->max_context;
-    int64_t splits = ceil_div(kTarget, tiles);
-    int64_t keys = ceil_div(ceil_div(context, splits), 128) * 128;
-    if (keys < kLeast) keys = kLeast;
-    // the range's start is rounded down to a multiple of 64
-    splits = ceil_div(context + 63, keys);
+
+// Splits of `keys` keys, a multiple of 128, over a context; its start is rounded
+// down to a multiple of 64.
+static AttnSplit cut_keys(int tile_rows, int64_t context, int64_t keys) {
+    keys = ceil_div(std::max<int64_t>(keys, 128), 128) * 128;
+    int64_t splits = ceil_div(context + 63, keys);
     if (splits > kMaxSplits) {
-        splits = kMaxSplits;
-        keys = ceil_div(ceil_div(context + 63, splits), 128) * 128;
+        keys = ceil_div(ceil_div(context + 63, kMaxSplits), 128) * 128;
+        splits = ceil_div(context + 63, keys);
     }
-    return AttnPlan{int(keys), int(splits)};
+    return AttnSplit{tile_rows, int(keys), int(splits)};
+}
+
+static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads) {
+    const int group = q_heads / c->heads;
+    const int64_t most = int64_t(std::max(b->max_new, 1)) * group;
+    const int64_t context = std::max(b->max_context, 1);
+    AttnPlan p;
+    p.wide = most > kNarrowMost;
+    p.narrow = !p.wide || b->tokens < int64_t(b->seqs) * b->max_new;     // all the same length otherwise
+    p.narrow_rows = !p.wide ? INT_MAX : p.narrow ? kNarrowMost : -1;
+    p.split[0] = p.split[1] = AttnSplit{kNarrowRows, 128, 1};
+    if (p.narrow) {
+        constexpr int64_t kTarget = 768, kLeast = 256;
+        const int64_t tiles = tile_items(p.wide ? 0 : b->tokens, group, b->seqs, kNarrowRows) * c->heads;
+        p.split[0] = cut_keys(kNarrowRows, context, std::max(ceil_div(context, ceil_div(kTarget, tiles)), kLeast));
+    }
+    if (p.wide) {
+        // the number of splits that takes the fewest key tiles in all, a CU
+        // taking one workgroup at a time, a split costing about 256 keys more
+        const int rows = wide_rows(c->head_dim);
+        const int64_t tiles = (ceil_div(b->tokens * group, rows) + (p.narrow ? 0 : b->seqs - 1)) * c->heads;
+        int64_t best = 0, keys = context;
+        for (int n = 1; n <= 16; ++n) {
+            const int64_t each = ceil_div(context, n);
+            if (n > 1 && each < 256) break;
+            const int64_t cost = ceil_div(tiles * n, kCus) * (each + 256);
+            if (n == 1 || cost < best) {
+                best = cost;
+                keys = each;
+            }
+        }
+        p.split[1] = cut_keys(rows, context, keys + 63);
+    }
+    return p;
 }
 
 static int attn_check(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads, KvView &v) {
@@ -34,7 +74,7 @@ static int attn_check(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_he
 }
 
 static size_t attn_bytes(const AttnPlan &p, int64_t tokens, int q_heads, int dim) {
-    return p.splits <= 1 ? 0 : size_t(p.splits) * size_t(tokens) * q_heads * (dim + 4) * sizeof(float);
+    return p.splits() <= 1 ? 0 : size_t(p.splits()) * size_t(tokens) * q_heads * (dim + 4) * sizeof(float);
 }
 
 }  // namespace nvfp4
@@ -79,11 +119,15 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
     a.group = q_heads / cache->heads;
     a.window = window;
     a.scale_log2 = scale * kLog2e;
-    a.split_keys = plan.split_keys;
-    a.splits = plan.splits;
+    a.split[0] = plan.split[0];
+    a.split[1] = plan.split[1];
+    a.narrow_rows = plan.narrow_rows;
     a.part_o = static_cast<float *>(workspace);
-    a.part_ml = a.part_o + size_t(plan.splits) * batch->tokens * wide;
-    if (int st = launch_attn_narrow(a, cache->head_dim, cache->k_format, cache->v_format, stream)) return st;
-    if (plan.splits > 1) return launch_attn_join(a, cache->head_dim, 16, stream);
-    return NVFP4_OK;
+    a.part_ml = a.part_o + size_t(plan.splits()) * batch->tokens * wide;
+    const int dim = cache->head_dim;
+    if (plan.narrow)
+        if (int st = launch_attn_narrow(a, dim, cache->k_format, cache->v_format, stream)) return st;
+    if (plan.wide)
+        if (int st = launch_attn_wide(a, dim, cache->k_format, cache->v_format, stream)) return st;
+    return plan.splits() > 1 ? launch_attn_join(a, dim, stream) : NVFP4_OK;
 }

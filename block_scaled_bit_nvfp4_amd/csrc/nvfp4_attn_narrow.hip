@@ -7,6 +7,18 @@ namespace nvfp4 {
 constexpr int kNarrowWaves = 4;
 constexpr int kTileKeys = 32;      // keys of a wave's tile: two units
 
+// The pages of a tile's two units, wave-uniform.
+struct TilePages {
+    int page[2];
+    __device__ __forceinline__ void load(const KvView &kv, int s, int key, int end) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int pos = key + u * kKvUnit;
+            page[u] = __builtin_amdgcn_readfirstlane(pos < end ? kv.page_of(s, pos) : -1);
+        }
+    }
+};
+
 // The operands of one 32-key tile as loaded.
 template <int D, int KB, int VB>
 struct NarrowTile {
@@ -19,12 +31,11 @@ struct NarrowTile {
     uint32_t vs[2];
     bool some[2];                  // the unit has a page (wave-uniform)
 
-    __device__ __forceinline__ void load(const KvView &kv, int s, int head, int key) {
+    __device__ __forceinline__ void load(const KvView &kv, const TilePages &pages, int head, int key) {
         const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int pos = key + u * kKvUnit;
-            const int page = kv.page_of(s, pos);
+            const int pos = key + u * kKvUnit, page = pages.page[u];
             some[u] = page >= 0;
             const int64_t unit = kv.unit_of(max(page, 0), head, pos);
             const uint8_t *kc = kv.codes[0] + unit * KS::kUnitCodes + lane * KS::kPiece;
@@ -39,65 +50,56 @@ struct NarrowTile {
     }
 };
 
-template <int D, int KB, int VB, int NT>
-__global__ void __launch_bounds__(kNarrowWaves * kLanes)
-    attn_narrow_kernel(AttnArgs a) {
+template <int D, int KB, int VB>
+__global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_narrow_kernel(AttnArgs a) {
     typedef KvSide<D, KB> KS;
-    constexpr int TR = 16 * NT;
     constexpr int kSlices = D / 32;            // MFMAs of one unit's scores
     constexpr int kRowDims = D / 16;           // elements of a value row
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const RowTile tile = row_tile(a, blockIdx.x, TR);
-    if (!tile.some) return;
+    const RowTile tile = row_tile(a, blockIdx.x, kNarrowRows);
+    if (!tile.some || tile.rows > a.narrow_rows) return;
     const int head = blockIdx.y, z = blockIdx.z;
-    const KeyRange keys = key_range(a, tile, z);
+    const KeyRange keys = key_range(a.split[0], tile, z);
     if (z > 0 && z >= keys.splits) return;
 
-    // The rows of this lane's columns, and their query operands.
-    bf16x8 q[NT][kSlices];
-    int token[NT], qhead[NT], klo[NT], khi[NT];
-    unsigned long long tree[NT];
+    // The row of this lane's column, and its query operands.
+    bf16x8 q[kSlices];
+    int token, qhead, klo, khi;
+    unsigned long long tree;
+    const int row = tile.row0 + c;
+    const bool in = row < tile.rows;
+    const int i = in ? row / a.group : 0;
+    token = in ? tile.begin + i : -1;
+    qhead = head * a.group + (in ? row - i * a.group : 0);
+    const int pos = tile.past + i;
+    klo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+    khi = in ? (a.tree ? tile.past : pos + 1) : 0;
+    tree = in && a.tree ? a.tree[token] : 0ull;
+    const uint16_t *src = a.q + max(token, 0) * a.q_stride + qhead * D;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        const int row = tile.row0 + 16 * t + c;
-        const bool in = row < tile.rows;
-        const int i = in ? row / a.group : 0;
-        token[t] = in ? tile.begin + i : -1;
-        qhead[t] = head * a.group + (in ? row - i * a.group : 0);
-        const int pos = tile.past + i;
-        klo[t] = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
-        khi[t] = in ? (a.tree ? tile.past : pos + 1) : 0;
-        tree[t] = in && a.tree ? a.tree[token[t]] : 0ull;
-        const uint16_t *src = a.q + max(token[t], 0) * a.q_stride + qhead[t] * D;
-#pragma unroll
-        for (int m = 0; m < kSlices; ++m) {
-            // slice m takes the lane's m-th group of eight elements of its pieces
-            constexpr int per = KS::kPieceDims / 8;
-            const int d = (4 * (m / per) + g) * KS::kPieceDims + 8 * (m % per);
-            u32x4 w = {0, 0, 0, 0};
-            if (in) w = *reinterpret_cast<const u32x4 *>(src + d);
-            q[t][m] = __builtin_bit_cast(bf16x8, w);
-        }
+    for (int m = 0; m < kSlices; ++m) {
+        // slice m takes the lane's m-th group of eight elements of its pieces
+        constexpr int per = KS::kPieceDims / 8;
+        const int d = (4 * (m / per) + g) * KS::kPieceDims + 8 * (m % per);
+        u32x4 w = {0, 0, 0, 0};
+        if (in) w = *reinterpret_cast<const u32x4 *>(src + d);
+        q[m] = __builtin_bit_cast(bf16x8, w);
     }
 
-    floatx4 o[NT][kRowDims];
-    float mx[NT], sub[NT], l[NT], lr[NT];     // lr: the sum of the weights as rounded, which normalises the outputs
+    floatx4 o[kRowDims];
+    float mx, sub, l, lr;     // lr: the sum of the weights as rounded, which normalises the outputs
+    mx = kNegInf; sub = 0.0f; l = 0.0f; lr = 0.0f;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        mx[t] = kNegInf; sub[t] = 0.0f; l[t] = 0.0f; lr[t] = 0.0f;
-#pragma unroll
-        for (int j = 0; j < kRowDims; ++j) o[t][j] = floatx4{0, 0, 0, 0};
-    }
+    for (int j = 0; j < kRowDims; ++j) o[j] = floatx4{0, 0, 0, 0};
 
     const auto step = [&](const NarrowTile<D, KB, VB> &x, int key, auto edge_tag) {
         constexpr bool EDGE = decltype(edge_tag)::value != 0;
         // scores of two units: lane (g, c) has keys 4 g + i of each, row c
-        floatx4 s[NT][2];
+        floatx4 s[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-#pragma unroll
-            for (int t = 0; t < NT; ++t) s[t][u] = floatx4{0, 0, 0, 0};
+            s[u] = floatx4{0, 0, 0, 0};
 #pragma unroll
             for (int m = 0; m < kSlices; ++m) {
                 constexpr int per = KS::kPieceDims / 8;
@@ -108,57 +110,53 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes)
                 bf16x8 k;
                 if constexpr (KB == 8) k = codes8(x.k[u][j][2 * e], x.k[u][j][2 * e + 1], unit);
                 else k = codes4(x.k[u][j][e], unit);
-#pragma unroll
-                for (int t = 0; t < NT; ++t) s[t][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[t][m], s[t][u], 0, 0, 0);
+                s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[m], s[u], 0, 0, 0);
             }
         }
-        uint32_t ones[NT][4];                  // EDGE: the allowed keys as a bf16 operand of ones
-        uint32_t p[NT][4];
+        uint32_t ones[4];                  // EDGE: the allowed keys as a bf16 operand of ones
+        uint32_t p[4];
+        float f[8];
+        float top = kNegInf;
 #pragma unroll
-        for (int t = 0; t < NT; ++t) {
-            float f[8];
-            float top = kNegInf;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                f[i] = s[t][i >> 2][i & 3] * a.scale_log2;
-                if constexpr (EDGE) {
-                    const int pos = key + (i >> 2) * kKvUnit + 4 * g + (i & 3);
-                    bool ok = pos >= klo[t] && pos < khi[t];
-                    if (a.tree) {
-                        const int b = pos - tile.past;
-                        ok = ok || (b >= 0 && b < tile.n && b < 64 && ((tree[t] >> (b & 63)) & 1));
-                    }
-                    ok = ok && x.some[i >> 2] && pos < tile.hi;
-                    if (!ok) f[i] = kNegInf;
-                    const uint32_t one = ok ? 0x3F80u : 0u;
-                    if (i & 1) ones[t][i >> 1] |= one << 16;
-                    else ones[t][i >> 1] = one;
+        for (int i = 0; i < 8; ++i) {
+            f[i] = s[i >> 2][i & 3] * a.scale_log2;
+            if constexpr (EDGE) {
+                const int pos = key + (i >> 2) * kKvUnit + 4 * g + (i & 3);
+                bool ok = pos >= klo && pos < khi;
+                if (a.tree) {
+                    const int b = pos - tile.past;
+                    ok = ok || (b >= 0 && b < tile.n && b < 64 && ((tree >> (b & 63)) & 1));
                 }
-                top = fmaxf(top, f[i]);
+                ok = ok && x.some[i >> 2] && pos < tile.hi;
+                if (!ok) f[i] = kNegInf;
+                const uint32_t one = ok ? 0x3F80u : 0u;
+                if (i & 1) ones[i >> 1] |= one << 16;
+                else ones[i >> 1] = one;
             }
-            if (__any(top > mx[t] + kMaxSlack)) {
-                top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32));
-                const float m = fmaxf(mx[t], top);
-                const float by = m == mx[t] ? 1.0f : exp2_fast(mx[t] - m);
-                mx[t] = m;
-                sub[t] = m == kNegInf ? 0.0f : m;
-                l[t] *= by;
-                lr[t] *= by;
+            top = fmaxf(top, f[i]);
+        }
+        if (__any(top > mx + kMaxSlack)) {
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float m = fmaxf(mx, top);
+            const float by = m == mx ? 1.0f : exp2_fast(mx - m);
+            mx = m;
+            sub = m == kNegInf ? 0.0f : m;
+            l *= by;
+            lr *= by;
 #pragma unroll
-                for (int j = 0; j < kRowDims; ++j) o[t][j] *= by;
-            }
-            float e[8];
+            for (int j = 0; j < kRowDims; ++j) o[j] *= by;
+        }
+        float e[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                e[i] = exp2_fast(f[i] - sub[t]);
-                l[t] += e[i];
-            }
+        for (int i = 0; i < 8; ++i) {
+            e[i] = exp2_fast(f[i] - sub);
+            l += e[i];
+        }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                p[t][i] = pack_bf16(e[2 * i], e[2 * i + 1]);
-                lr[t] = add_pair(p[t][i], lr[t]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            p[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
+            lr = add_pair(p[i], lr);
         }
         // values: the lane's row holds D / 16 elements of eight keys; two
         // elements of a key come at a time and are paired over keys
@@ -190,12 +188,9 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes)
                                 low_halves(w[1][0], w[1][1]), low_halves(w[1][2], w[1][3])};
             const u32x4 odd = {high_halves(w[0][0], w[0][1]), high_halves(w[0][2], w[0][3]),
                                high_halves(w[1][0], w[1][1]), high_halves(w[1][2], w[1][3])};
-#pragma unroll
-            for (int t = 0; t < NT; ++t) {
-                const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[t][0], p[t][1], p[t][2], p[t][3]});
-                o[t][2 * jp] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), pb, o[t][2 * jp], 0, 0, 0);
-                o[t][2 * jp + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), pb, o[t][2 * jp + 1], 0, 0, 0);
-            }
+            const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]});
+            o[2 * jp] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), pb, o[2 * jp], 0, 0, 0);
+            o[2 * jp + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), pb, o[2 * jp + 1], 0, 0, 0);
         }
         if constexpr (EDGE) {
             // A NaN block counts only for the rows that see its key: its values
@@ -207,23 +202,29 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     mark[i] = ((bad >> (2 * i)) & 1 ? 0x3F80u : 0u) | ((bad >> (2 * i + 1)) & 1 ? 0x3F800000u : 0u);
+                const bf16x8 on = __builtin_bit_cast(bf16x8, u32x4{ones[0], ones[1], ones[2], ones[3]});
+                const floatx4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, mark), on, floatx4{0, 0, 0, 0}, 0, 0, 0);
 #pragma unroll
-                for (int t = 0; t < NT; ++t) {
-                    const bf16x8 on = __builtin_bit_cast(bf16x8, u32x4{ones[t][0], ones[t][1], ones[t][2], ones[t][3]});
-                    const floatx4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, mark), on, floatx4{0, 0, 0, 0}, 0, 0, 0);
+                for (int i = 0; i < 4; ++i)
+                    if (n[i] > 0.0f)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (n[i] > 0.0f)
-#pragma unroll
-                            for (int j = 0; j < kRowDims; ++j) o[t][j][i] = __builtin_nanf("");
-                }
+                        for (int j = 0; j < kRowDims; ++j) o[j][i] = __builtin_nanf("");
             }
         }
     };
 
-    for (int key = keys.lo + wave * kTileKeys; key < keys.hi; key += kNarrowWaves * kTileKeys) {
+    // A wave takes every fourth tile; the page numbers of its next one are
+    // fetched while one is worked on.  Codes are not: three waves of a SIMD cover
+    // each other's loads, and a ring of two or three tiles in registers (two
+    // waves of a SIMD) measured 82 -> 92 us on 64 sequences of 4096 keys.
+    constexpr int kStep = kNarrowWaves * kTileKeys;
+    int key = keys.lo + wave * kTileKeys;
+    TilePages pages;
+    pages.load(a.kv, tile.s, key, keys.hi);
+    for (; key < keys.hi; key += kStep) {
         NarrowTile<D, KB, VB> x;
-        x.load(a.kv, tile.s, head, key);
+        x.load(a.kv, pages, head, key);
+        pages.load(a.kv, tile.s, key + kStep, keys.hi);
         const bool inner = key >= tile.inner_lo && key + kTileKeys <= min(tile.inner_hi, keys.hi) && x.some[0] && x.some[1];
         if (inner) step(x, key, IntC<0>());
         else step(x, key, IntC<1>());
@@ -233,78 +234,72 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes)
     // parts of at most 8 to bound the shared memory.
     constexpr int kPart = kRowDims < 8 ? kRowDims : 8;
     constexpr int kCols = 16 * kPart + 4;              // floats of one row's part, padded against bank conflicts
-    __shared__ float sm[kNarrowWaves][TR], sl[kNarrowWaves][TR], sr[kNarrowWaves][TR];
+    __shared__ float sm[kNarrowWaves][kNarrowRows], sl[kNarrowWaves][kNarrowRows], sr[kNarrowWaves][kNarrowRows];
     __shared__ float so[kNarrowWaves][16][kCols];
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        l[t] += __shfl_xor(l[t], 16);
-        l[t] += __shfl_xor(l[t], 32);
-        lr[t] += __shfl_xor(lr[t], 16);
-        lr[t] += __shfl_xor(lr[t], 32);
-        if (g == 0) {
-            sr[wave][16 * t + c] = lr[t];
-            sm[wave][16 * t + c] = mx[t];
-            sl[wave][16 * t + c] = l[t];
-        }
+    l += __shfl_xor(l, 16);
+    l += __shfl_xor(l, 32);
+    lr += __shfl_xor(lr, 16);
+    lr += __shfl_xor(lr, 32);
+    if (g == 0) {
+        sr[wave][c] = lr;
+        sm[wave][c] = mx;
+        sl[wave][c] = l;
     }
     __syncthreads();
+    float m = kNegInf;
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-        float m = kNegInf;
+    for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, sm[w][c]);
+    const float by = mx == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mx - m);
 #pragma unroll
-        for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, sm[w][16 * t + c]);
-        const float by = mx[t] == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mx[t] - m);
+    for (int part = 0; part < kRowDims / kPart; ++part) {
 #pragma unroll
-        for (int part = 0; part < kRowDims / kPart; ++part) {
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int j = 0; j < kPart; ++j) so[wave][c][(4 * g + i) * kPart + j] = o[part * kPart + j][i] * by;
+        __syncthreads();
+        // thread (row, piece): kPart / ... elements of one row
+        constexpr int kEach = 16 * kPart / 16;
+        const int row16 = threadIdx.x >> 4, piece = threadIdx.x & 15;
+        const int row = tile.row0 + row16;
+        if (row < tile.rows) {
+            float mm = kNegInf, ll = 0.0f, rr = 0.0f;
 #pragma unroll
-                for (int j = 0; j < kPart; ++j) so[wave][c][(4 * g + i) * kPart + j] = o[t][part * kPart + j][i] * by;
-            __syncthreads();
-            // thread (row, piece): kPart / ... elements of one row
-            constexpr int kEach = 16 * kPart / 16;
-            const int row16 = threadIdx.x >> 4, piece = threadIdx.x & 15;
-            const int row = tile.row0 + 16 * t + row16;
-            if (row < tile.rows) {
-                float mm = kNegInf, ll = 0.0f, rr = 0.0f;
+            for (int w = 0; w < kNarrowWaves; ++w) mm = fmaxf(mm, sm[w][row16]);
 #pragma unroll
-                for (int w = 0; w < kNarrowWaves; ++w) mm = fmaxf(mm, sm[w][16 * t + row16]);
-#pragma unroll
-                for (int w = 0; w < kNarrowWaves; ++w) {
-                    const float mw = sm[w][16 * t + row16];
-                    const float by = mw == kNegInf ? (mm == kNegInf ? 1.0f : 0.0f) : exp2_fast(mw - mm);
-                    ll += sl[w][16 * t + row16] * by;
-                    rr += sr[w][16 * t + row16] * by;
-                }
-                float y[kEach];
-#pragma unroll
-                for (int j = 0; j < kEach; ++j) {
-                    y[j] = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < kNarrowWaves; ++w) y[j] += so[w][row16][piece * kEach + j];
-                }
-                const int i = row / a.group;
-                const int64_t at = int64_t(tile.begin + i) * a.q_heads + head * a.group + (row - i * a.group);
-                const int d = piece * kRowDims + part * kPart;
-                if (keys.splits > 1) {
-                    float *dst = a.part_o + (int64_t(z) * a.kv.tokens * a.q_heads + at) * D + d;
-#pragma unroll
-                    for (int j = 0; j < kEach; ++j) dst[j] = y[j];
-                    if (piece == 0 && part == 0) {
-                        float *ml = a.part_ml + (int64_t(z) * a.kv.tokens * a.q_heads + at) * 4;
-                        *reinterpret_cast<float4 *>(ml) = float4{mm, ll, rr, 0.0f};
-                    }
-                } else {
-                    const float inv = mm == kNegInf && ll == 0.0f ? 0.0f : 1.0f / rr;
-                    uint16_t *dst = a.out + int64_t(tile.begin + i) * a.out_stride + (head * a.group + (row - i * a.group)) * D + d;
-#pragma unroll
-                    for (int j = 0; j < kEach; j += 2)
-                        *reinterpret_cast<uint32_t *>(dst + j) = pack_bf16(y[j] * inv, y[j + 1] * inv);
-                    if (a.lse && piece == 0 && part == 0) a.lse[at] = lse_of(mm, ll);
-                }
+            for (int w = 0; w < kNarrowWaves; ++w) {
+                const float mw = sm[w][row16];
+                const float by = mw == kNegInf ? (mm == kNegInf ? 1.0f : 0.0f) : exp2_fast(mw - mm);
+                ll += sl[w][row16] * by;
+                rr += sr[w][row16] * by;
             }
-            __syncthreads();
+            float y[kEach];
+#pragma unroll
+            for (int j = 0; j < kEach; ++j) {
+                y[j] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kNarrowWaves; ++w) y[j] += so[w][row16][piece * kEach + j];
+            }
+            const int i = row / a.group;
+            const int64_t at = int64_t(tile.begin + i) * a.q_heads + head * a.group + (row - i * a.group);
+            const int d = piece * kRowDims + part * kPart;
+            if (keys.splits > 1) {
+                float *dst = a.part_o + (int64_t(z) * a.kv.tokens * a.q_heads + at) * D + d;
+#pragma unroll
+                for (int j = 0; j < kEach; ++j) dst[j] = y[j];
+                if (piece == 0 && part == 0) {
+                    float *ml = a.part_ml + (int64_t(z) * a.kv.tokens * a.q_heads + at) * 4;
+                    *reinterpret_cast<float4 *>(ml) = float4{mm, ll, rr, 0.0f};
+                }
+            } else {
+                const float inv = mm == kNegInf && ll == 0.0f ? 0.0f : 1.0f / rr;
+                uint16_t *dst = a.out + int64_t(tile.begin + i) * a.out_stride + (head * a.group + (row - i * a.group)) * D + d;
+#pragma unroll
+                for (int j = 0; j < kEach; j += 2)
+                    *reinterpret_cast<uint32_t *>(dst + j) = pack_bf16(y[j] * inv, y[j + 1] * inv);
+                if (a.lse && piece == 0 && part == 0) a.lse[at] = lse_of(mm, ll);
+            }
         }
+        __syncthreads();
     }
 }
 
@@ -312,18 +307,20 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes)
 
 // The splits that a row's keys were in (a row's tile decides them), or 0 where
 // the row is no sequence's.
-__device__ __forceinline__ int row_splits(const AttnArgs &a, int token, int qhead, int s, int tile_rows) {
+__device__ __forceinline__ int row_splits(const AttnArgs &a, int token, int qhead, int s) {
     const KvView &v = a.kv;
     int begin, end, past;
     v.sequence(s, begin, end, past);
     if (token < begin || token >= end) return 0;
     const int row = (token - begin) * a.group + qhead % a.group;
-    const int first = row / tile_rows * tile_rows, n = end - begin;
-    const int i0 = first / a.group, i1 = (min(first + tile_rows, n * a.group) - 1) / a.group;
+    const int n = end - begin;
+    const AttnSplit &split = a.split[n * a.group > a.narrow_rows];
+    const int first = row / split.tile_rows * split.tile_rows;
+    const int i0 = first / a.group, i1 = (min(first + split.tile_rows, n * a.group) - 1) / a.group;
     RowTile r;
     r.lo = a.window > 0 ? max(0, past + i0 + 1 - a.window) : 0;
     r.hi = min(a.tree ? past + n : past + i1 + 1, v.capacity);
-    return key_range(a, r, 0).splits;
+    return key_range(split, r, 0).splits;
 }
 
 __device__ __forceinline__ float split_weight(float mz, float m) {
@@ -342,7 +339,7 @@ __device__ __forceinline__ void store_row4(const AttnArgs &a, int D, int token, 
 // splits, whose loads go out together.
 constexpr int kFewSplits = 8;
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_few_kernel(AttnArgs a, int tile_rows) {
+__global__ void __launch_bounds__(256) attn_join_few_kernel(AttnArgs a) {
     constexpr int kThreads = D / 4;            // of one row
     const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
     const int64_t rows = int64_t(a.kv.tokens) * a.q_heads;
@@ -352,7 +349,7 @@ __global__ void __launch_bounds__(256) attn_join_few_kernel(AttnArgs a, int tile
     const int t0 = __builtin_amdgcn_readfirstlane(token);
     int s = max(wave_count_le(a.kv.seqs, t0, [&](int i) { return a.kv.offsets[i]; }) - 1, 0);
     while (s + 1 < a.kv.seqs && a.kv.offsets[s + 1] <= token) ++s;
-    const int splits = u < rows * kThreads ? row_splits(a, token, qhead, s, tile_rows) : 0;
+    const int splits = u < rows * kThreads ? row_splits(a, token, qhead, s) : 0;
     if (splits <= 1) return;
     float4 part[kFewSplits], o[kFewSplits];
 #pragma unroll
@@ -380,7 +377,7 @@ __global__ void __launch_bounds__(256) attn_join_few_kernel(AttnArgs a, int tile
 // A workgroup of 256 threads takes one row: thread z weighs split z, then groups
 // of D / 4 threads sum every kGroups-th split and meet in shared memory.
 template <int D>
-__global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a, int tile_rows) {
+__global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a) {
     constexpr int kThreads = D / 4, kGroups = 256 / kThreads;
     __shared__ float4 red[4];
     __shared__ float weight[kMaxSplits];
@@ -388,7 +385,7 @@ __global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a, int til
     const int64_t rows = int64_t(a.kv.tokens) * a.q_heads, at = blockIdx.x;
     const int token = int(at / a.q_heads), qhead = int(at - int64_t(token) * a.q_heads);
     const int s = max(wave_count_le(a.kv.seqs, token, [&](int i) { return a.kv.offsets[i]; }) - 1, 0);
-    const int splits = row_splits(a, token, qhead, s, tile_rows);
+    const int splits = row_splits(a, token, qhead, s);
     if (splits <= 1) return;
     const int tid = threadIdx.x, wave = tid >> 6;
     float4 part = {kNegInf, 0, 0, 0};
@@ -433,14 +430,15 @@ __global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a, int til
     store_row4(a, D, token, qhead, d, m, l, lr, y);
 }
 
-int launch_attn_join(const AttnArgs &a, int dim, int tile_rows, hipStream_t stream) {
+int launch_attn_join(const AttnArgs &a, int dim, hipStream_t stream) {
     return kv_dim(dim, [&](auto tag) {
         constexpr int D = decltype(tag)::value;
         const int64_t rows = int64_t(a.kv.tokens) * a.q_heads;
-        const int64_t grid = a.splits <= kFewSplits ? ceil_div(rows * (D / 4), 256) : rows;
+        const bool few = max(a.split[0].splits, a.split[1].splits) <= kFewSplits;
+        const int64_t grid = few ? ceil_div(rows * (D / 4), 256) : rows;
         if (grid >= kMaxGrid / 256) return NVFP4_ESHAPE;
-        if (a.splits <= kFewSplits) attn_join_few_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a, tile_rows);
-        else attn_join_many_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a, tile_rows);
+        if (few) attn_join_few_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a);
+        else attn_join_many_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a);
         return launch_status();
     });
 }
@@ -450,10 +448,11 @@ int launch_attn_narrow(const AttnArgs &a, int dim, int k_format, int v_format, h
         return kv_bits(k_format, [&](auto k) {
             return kv_bits(v_format, [&](auto v) {
                 constexpr int D = decltype(d)::value, K = decltype(k)::value, V = decltype(v)::value;
-                const int64_t items = tile_items<16>(a.kv.tokens, a.group, a.kv.seqs);
-                if (items >= kMaxGrid / (kNarrowWaves * kLanes)) return NVFP4_ESHAPE;
-                attn_narrow_kernel<D, K, V, 1><<<dim3(unsigned(items), unsigned(a.kv.heads), unsigned(a.splits)),
-                                                 kNarrowWaves * kLanes, 0, stream>>>(a);
+                constexpr int kThreads = kNarrowWaves * kLanes;
+                const int64_t items = tile_items(a.kv.tokens, a.group, a.kv.seqs, kNarrowRows);
+                if (items >= kMaxGrid / kThreads) return NVFP4_ESHAPE;
+                attn_narrow_kernel<D, K, V><<<dim3(unsigned(items), unsigned(a.kv.heads), unsigned(a.split[0].splits)),
+                                              kThreads, 0, stream>>>(a);
                 return launch_status();
             });
         });
