@@ -24,6 +24,7 @@ constexpr float kNegInf = -__builtin_inff();
 // powers of two): the weights then reach 2^8 at most, far inside fp32 and with
 // bf16's relative rounding unchanged, and most tiles rescale nothing.
 constexpr float kMaxSlack = 8.0f;
+constexpr float kMaxSum = 1024.0f;      // the same on the sum of a lane's weights of a tile
 
 // How a kernel cuts the work: rows of a tile, keys of a split (a multiple of 128),
 // and how many splits at most.
@@ -139,11 +140,12 @@ __device__ __forceinline__ float unit_of_byte(uint32_t w, int i) {
     return __uint_as_float(__builtin_amdgcn_ubfe(w, 8 * i, 8) << 23);
 }
 
-// A load of BYTES per lane into words.
-template <int BYTES>
+// A load of BYTES per lane into words; STREAM: of bytes that nobody reads again.
+template <int BYTES, bool STREAM = false>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
     if constexpr (BYTES == 16) {
-        const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+        const u32x4 t = STREAM ? __builtin_nontemporal_load(q) : *q;
         w[0] = t[0]; w[1] = t[1]; w[2] = t[2]; w[3] = t[3];
     } else if constexpr (BYTES == 8) {
         const u32x2 t = *reinterpret_cast<const u32x2 *>(p);

@@ -7,15 +7,13 @@ namespace nvfp4 {
 constexpr int kNarrowWaves = 4;
 constexpr int kTileKeys = 32;      // keys of a wave's tile: two units
 
-// The pages of a tile's two units, wave-uniform.
-struct TilePages {
-    int page[2];
-    __device__ __forceinline__ void load(const KvView &kv, int s, int key, int end) {
+// The table's entries of a tile's two units, wave-uniform; made pages when the tile
+// is loaded, so that nothing waits for them before.
+struct TileEntries {
+    int entry[2];
+    __device__ __forceinline__ void load(const KvView &kv, int s, int key) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const int pos = key + u * kKvUnit;
-            page[u] = __builtin_amdgcn_readfirstlane(pos < end ? kv.page_of(s, pos) : -1);
-        }
+        for (int u = 0; u < 2; ++u) entry[u] = kv.entry_at(s, key + u * kKvUnit);
     }
 };
 
@@ -31,20 +29,21 @@ struct NarrowTile {
     uint32_t vs[2];
     bool some[2];                  // the unit has a page (wave-uniform)
 
-    __device__ __forceinline__ void load(const KvView &kv, const TilePages &pages, int head, int key) {
+    __device__ __forceinline__ void load(const KvView &kv, const TileEntries &entries, int head, int key, int end) {
         const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int pos = key + u * kKvUnit, page = pages.page[u];
+            const int pos = key + u * kKvUnit;
+            const int page = pos < end ? kv.page_in(__builtin_amdgcn_readfirstlane(entries.entry[u]), pos) : -1;
             some[u] = page >= 0;
             const int64_t unit = kv.unit_of(max(page, 0), head, pos);
             const uint8_t *kc = kv.codes[0] + unit * KS::kUnitCodes + lane * KS::kPiece;
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) load_words<KS::kPiece>(kc + j * kLanes * KS::kPiece, k[u][j]);
+            for (int j = 0; j < kLoads; ++j) load_words<KS::kPiece, true>(kc + j * kLanes * KS::kPiece, k[u][j]);
             load_words<KS::kBlocks>(kv.scales[0] + unit * KS::kUnitScales + r * KS::kBlocks, ks[u]);
             const uint8_t *vc = kv.codes[1] + unit * VS::kUnitCodes + lane * VS::kSlot;
 #pragma unroll
-            for (int j = 0; j < VS::kSlots; ++j) load_words<VS::kSlot>(vc + j * kLanes * VS::kSlot, &v[u][j * (VS::kSlot / 4)]);
+            for (int j = 0; j < VS::kSlots; ++j) load_words<VS::kSlot, true>(vc + j * kLanes * VS::kSlot, &v[u][j * (VS::kSlot / 4)]);
             load_words<4>(kv.scales[1] + unit * VS::kUnitScales + (g * VS::kBlocks + r * VS::kBlocks / 16) * 4, &vs[u]);
         }
     }
@@ -219,12 +218,12 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
     // waves of a SIMD) measured 82 -> 92 us on 64 sequences of 4096 keys.
     constexpr int kStep = kNarrowWaves * kTileKeys;
     int key = keys.lo + wave * kTileKeys;
-    TilePages pages;
-    pages.load(a.kv, tile.s, key, keys.hi);
+    TileEntries entries;
+    entries.load(a.kv, tile.s, key);
     for (; key < keys.hi; key += kStep) {
         NarrowTile<D, KB, VB> x;
-        x.load(a.kv, pages, head, key);
-        pages.load(a.kv, tile.s, key + kStep, keys.hi);
+        x.load(a.kv, entries, head, key, keys.hi);
+        entries.load(a.kv, tile.s, key + kStep);
         const bool inner = key >= tile.inner_lo && key + kTileKeys <= min(tile.inner_hi, keys.hi) && x.some[0] && x.some[1];
         if (inner) step(x, key, IntC<0>());
         else step(x, key, IntC<1>());

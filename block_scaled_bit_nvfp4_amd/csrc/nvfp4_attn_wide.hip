@@ -1,29 +1,37 @@
 // nvfp4_attn_wide.hip -- attention of many query rows over the paged cache
 // (prefill chunks, wide verifies) on gfx950.
 //
-// A workgroup owns 32 rows per wave and walks the keys in tiles of kKeys = 8192 / D.
-// Keys and values are decoded to bf16 once per workgroup, into shared memory and
-// as whole operands of v_mfma_f32_32x32x16_bf16: the waves read them with
-// conflict-free 16-byte loads, and the cache's byte order makes each thread's share
-// of the decode one load and a few stores.  Two buffers: while the waves work on one
-// tile, the next one's codes, loaded a tile earlier, are decoded into the other,
-// so a tile costs one barrier.
+// A workgroup of eight waves walks the keys in tiles of kKeys = 8192 / D.  Keys and
+// values are decoded to bf16 once per workgroup, into shared memory and as whole
+// operands of v_mfma_f32_32x32x16_bf16: the waves read them with conflict-free
+// 16-byte loads, and the cache's byte order makes each thread's share of the decode
+// one load and a few stores.
+//
+// The two waves of a SIMD work in opposite phases, a barrier between phases: while
+// one multiplies (the values of tile i - 1 by its weights, then the keys of tile i by
+// its queries), the other takes tile i's softmax and decodes its share of the tiles
+// to come, so that the matrix and the vector pipe of a SIMD both stay busy.  Keys are
+// decoded two tiles ahead, values one, into rings of three, codes loaded one
+// tile before that.
+//
+// At D <= 128 a wave owns 32 rows.  At D = 256 two waves own 32 rows together,
+// each half the elements: they add their halves of the scores through shared
+// memory, take the same softmax, and each keeps half of the output.
 #include <mutex>
 
 #include "nvfp4_attn.h"
 
 namespace nvfp4 {
 
+typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
-// The shape at head dimension D: 256 rows in 8 waves, two to a SIMD, whose matrix
-// and vector instructions overlap; at D = 256 a row's accumulators and query
-// operands take 192 registers of a lane, so 4 waves, one to a SIMD, and 128 rows.
 template <int D>
 struct WideShape {
-    static constexpr int kWaves = D == 256 ? 4 : 8;
+    static constexpr int kWaves = 8;
     static constexpr int kThreads = kWaves * kLanes;
-    static constexpr int kRows = 32 * kWaves;
+    static constexpr int kHalves = D == 256 ? 2 : 1;   // waves that share 32 rows
+    static constexpr int kRows = 32 * kWaves / kHalves;
     static constexpr int kKeys = 8192 / D;             // of a tile
     static constexpr int kUnits = kKeys / kKvUnit;
     static constexpr int kBlocks32 = kKeys / 32;
@@ -31,126 +39,111 @@ struct WideShape {
     static constexpr int kDimBlocks = D / 32;          // accumulators of the output
     static constexpr int kSide = kKeys * D * 2;        // bytes of a tile's keys (and of its values): 16 KiB
     static constexpr int kMarks = kKeys * (D / kMxBlock);
-    static constexpr int kBuffer = 2 * kSide + kMarks;
-    static constexpr int kLds = 2 * kBuffer;
+    static constexpr int kRing = 3;
+    // shared memory: keys, values, marks, and the halves' scores
+    static constexpr int kValuesAt = kRing * kSide;
+    static constexpr int kMarksAt = 2 * kRing * kSide;
+    static constexpr int kScoresAt = kMarksAt + kRing * kMarks;
+    static constexpr int kLds = kScoresAt + (kHalves == 2 ? kWaves * kLanes * 64 : 0);
 };
 
-// One thread's share of a tile between its load and its store to shared memory.
+// One thread's share of a tile between its load and its store to shared memory: 16
+// elements of one key, and 8 elements of a value row of two keys (D = 64: 4
+// elements of four).  A wave's items are all of one unit.
 template <int D, int KB, int VB>
 struct WideStage {
     typedef WideShape<D> W;
     typedef KvSide<D, KB> KS;
     typedef KvSide<D, VB> VS;
-    // keys: 16 elements of one key; values: two keys' (D = 64: four keys')
-    // elements of a row, 16 or (D = 256) 32
-    static constexpr int kKeyItems = kKvUnit * D / 16;               // of a unit
-    static constexpr int kKeyEach = W::kUnits * kKeyItems / W::kThreads;
-    static constexpr int kTokens = D == 64 ? 4 : 2;
-    static constexpr int kValueItems = kKvUnit / kTokens * 16;
-    static constexpr int kValueEach = W::kUnits * kValueItems / W::kThreads;
-    static constexpr int kRowDims = D / 16;
-    static constexpr int kValueWords = kTokens * kRowDims * VB / 32;
-    static_assert(kValueEach == 1, "one value item per thread");
+    static constexpr int kItems = W::kThreads / W::kUnits;           // of a unit, keys or values
+    static_assert(kItems == kKvUnit * D / 16 && kItems % kLanes == 0, "a key item per thread, a unit per wave");
+    static constexpr int kTokens = D == 64 ? 4 : 2, kDims = 16 / kTokens;
+    static constexpr int kParts = D / 16 / kDims;                    // of a value row
+    static_assert(kItems == kKvUnit / kTokens * 16 * kParts, "a value item per thread");
+    static constexpr int kValueWords = 16 * VB / 32;
+    // an item's value bytes stand together unless a slot, or a row's part, splits them
+    static constexpr int kRun = VS::kSlotTokens >= kTokens && kParts == 1 ? kValueWords * 4 : kDims * VB / 8;
+    static constexpr int kRunTokens = kRun * 8 / (kDims * VB);
 
-    uint32_t k[kKeyEach][KB / 2], ks[kKeyEach];
-    uint32_t v[kValueWords], vs;
+    uint32_t k[KB / 2], ks, v[kValueWords], vs;
+    // offsets of the item's bytes in its unit, and of its operands in a ring slot
+    uint32_t k_at, ks_at, v_at, vs_at, k_to, v_to;
+    int token, block;              // the value item's first token in the tile, and its block
 
-    // The place of a key item: unit, token, and which 16 elements.
-    static __device__ __forceinline__ void key_item(int e, int &unit, int &r, int &part) {
-        unit = e / kKeyItems;
-        const int i = e % kKeyItems;
-        if (KB == 4 && KS::kPiece == 16) {          // two items of a piece side by side
-            r = (i >> 1) & 15;
-            part = (i >> 5) * 2 + (i & 1);
-        } else {
-            r = i & 15;
-            part = i >> 4;
-        }
-    }
-    // The place of a value item: unit, quad (half + 2 * upper), which tokens, row.
-    static __device__ __forceinline__ void value_item(int e, int &unit, int &quad, int &pair, int &r) {
-        unit = e / kValueItems;
-        const int i = e % kValueItems;
-        r = i & 15;
-        if (D == 64) {
-            quad = i >> 4;
-            pair = 0;
-        } else {
-            quad = ((i >> 4) & 1) * 2 + (i >> 6);
-            pair = (i >> 5) & 1;
-        }
-    }
-
-    // `pages`: lane u holds the page of the tile's unit u (or -1).
-    __device__ __forceinline__ void load(const KvView &kv, int pages, int head, int key) {
-        const int tid = threadIdx.x;
-#pragma unroll
-        for (int n = 0; n < kKeyEach; ++n) {
-            int unit, r, part;
-            key_item(n * W::kThreads + tid, unit, r, part);
-            unit = __builtin_amdgcn_readfirstlane(unit);
-            const int page = max(__builtin_amdgcn_readlane(pages, unit), 0);
-            const int64_t u = kv.unit_of(page, head, key + unit * kKvUnit);
-            load_words<2 * KB>(kv.codes[0] + u * KS::kUnitCodes + KS::key_code(r, part * 2 * KB), k[n]);
-            ks[n] = kv.scales[0][u * KS::kUnitScales + KS::key_scale(r, part / 2)];
-        }
-        int unit, quad, pair, r;
-        value_item(tid, unit, quad, pair, r);
-        unit = __builtin_amdgcn_readfirstlane(unit);
-        const int page = max(__builtin_amdgcn_readlane(pages, unit), 0);
-        const int64_t u = kv.unit_of(page, head, key + unit * kKvUnit);
-        const uint8_t *base = kv.codes[1] + u * VS::kUnitCodes;
+    __device__ __forceinline__ WideStage() {
+        const int i = threadIdx.x % kItems, unit = threadIdx.x / kItems;
+        // keys; in 16-byte pieces of 4-bit codes, two items of a piece side by side
+        const bool two = KB == 4 && KS::kPiece == 16;
+        const int r = two ? (i >> 1) & 15 : i & 15, part = two ? (i >> 5) * 2 + (i & 1) : i >> 4;
+        k_at = KS::key_code(r, part * 2 * KB);
+        ks_at = KS::key_scale(r, part / 2);
+        k_to = (((unit >> 1) * W::kDimSteps + part) * kLanes + (unit & 1) * 16 + r) * 16;
+        // values: quad (half + 2 * upper), pair of its tokens, row, part of the row
+        const int row = i & 15, quad = D == 64 ? i >> 4 : ((i >> 4) & 1) * 2 + ((i >> 6) & 1);
+        const int pair = D == 64 ? 0 : (i >> 5) & 1, piece = D == 64 ? 0 : i >> 7;
         const int t0 = quad * 4 + pair * 2;
-        constexpr int kRun = VS::kSlotTokens < kTokens ? VS::kPart : kValueWords * 4;   // contiguous bytes
-#pragma unroll
-        for (int n = 0; n < kValueWords * 4 / kRun; ++n)
-            load_words<kRun>(base + VS::value_code(t0 + n * VS::kSlotTokens, r * VS::kPart), v + n * kRun / 4);
-        load_words<kTokens>(kv.scales[1] + u * VS::kUnitScales + VS::value_scale(t0, r * VS::kBlocks / 16), &vs);
-    }
-
-    // Decode to the operands in `lds`.  EDGE: values of keys outside lo..hi - 1 or
-    // without a page, and NaN blocks, become zeros, the latter marked.
-    template <bool EDGE>
-    __device__ __forceinline__ void store(uint8_t *lds, int key, int lo, int hi, unsigned some) const {
-        const int tid = threadIdx.x;
-#pragma unroll
-        for (int n = 0; n < kKeyEach; ++n) {
-            int unit, r, part;
-            key_item(n * W::kThreads + tid, unit, r, part);
-            const float scale = __uint_as_float(ks[n] << 23);
-            const int row = (unit & 1) * 16 + r;
-            bf16x8 *dst = reinterpret_cast<bf16x8 *>(lds) + ((unit >> 1) * W::kDimSteps + part) * kLanes + row;
-            if constexpr (KB == 8) {
-                dst[0] = codes8(k[n][0], k[n][1], scale);
-                dst[32] = codes8(k[n][2], k[n][3], scale);
-            } else {
-                dst[0] = codes4(k[n][0], scale);
-                dst[32] = codes4(k[n][1], scale);
-            }
-        }
-        int unit, quad, pair, r;
-        value_item(tid, unit, quad, pair, r);
-        uint32_t keep[kTokens];
-        if constexpr (EDGE) {
-            uint8_t *marks = lds + 2 * W::kSide;
-#pragma unroll
-            for (int i = 0; i < kTokens; ++i) {
-                const int token = quad * 4 + pair * 2 + i, pos = key + unit * kKvUnit + token;
-                const bool held = ((some >> unit) & 1) && pos >= lo && pos < hi;
-                const bool nan = ((vs >> (8 * i)) & 0xFFu) == 0xFFu;
-                keep[i] = held && !nan ? ~0u : 0u;
-                marks[(unit * kKvUnit + token) * VS::kBlocks + r * VS::kBlocks / 16] = held && nan ? 1 : 0;
-            }
-        }
+        v_at = VS::value_code(t0, row * VS::kPart + piece * (kDims * VB / 8));
+        vs_at = VS::value_scale(t0, row * VS::kBlocks / 16);
         // operand (unit, dim block, half, row): eight keys, the quad's four at
         // 8 * (quad / 2) bytes
-        uint8_t *dst = lds + W::kSide + (unit * W::kDimBlocks * kLanes + (quad & 1) * 32 + r) * 16 + (quad >> 1) * 8 + pair * 4;
+        v_to = ((unit * W::kDimBlocks + piece * kDims / 2) * kLanes + (quad & 1) * 32 + row) * 16 + (quad >> 1) * 8 + pair * 4;
+        token = unit * kKvUnit + t0;
+        block = row * VS::kBlocks / 16;
+    }
+
+    // `unit`: the pool's unit that this wave's items are of.
+    __device__ __forceinline__ void load_keys(const KvView &kv, int64_t unit) {
+        load_words<2 * KB>(kv.codes[0] + unit * KS::kUnitCodes + k_at, k);
+        ks = (kv.scales[0] + unit * KS::kUnitScales)[ks_at];
+    }
+    __device__ __forceinline__ void load_values(const KvView &kv, int64_t unit) {
+        const uint8_t *base = kv.codes[1] + unit * VS::kUnitCodes;
+        // runs of tokens of a quad: in slots of their own, or one row's parts apart
 #pragma unroll
-        for (int jp = 0; jp < kRowDims / 2; ++jp) {
+        for (int n = 0; n < kValueWords * 4 / kRun; ++n) {
+            constexpr uint32_t kNext = VS::kSlotTokens >= kTokens ? VS::kPart : 4 * 16 * VS::kSlot;
+            load_words<kRun>(base + v_at + n * kNext, v + n * kRun / 4);
+        }
+        load_words<kTokens>(kv.scales[1] + unit * VS::kUnitScales + vs_at, &vs);
+    }
+    // Decode to the operands of a ring slot.
+    __device__ __forceinline__ void store_keys(uint8_t *slot) const {
+        const float scale = __uint_as_float(ks << 23);
+        bf16x8 *dst = reinterpret_cast<bf16x8 *>(slot + k_to);
+        if constexpr (KB == 8) {
+            dst[0] = codes8(k[0], k[1], scale);
+            dst[32] = codes8(k[2], k[3], scale);
+        } else {
+            dst[0] = codes4(k[0], scale);
+            dst[32] = codes4(k[1], scale);
+        }
+    }
+    // EDGE: values of keys outside lo..hi - 1 or without a page, and NaN blocks,
+    // become zeros, the latter marked.
+    template <bool EDGE>
+    __device__ __forceinline__ void store_values(uint8_t *slot, uint8_t *marks, int key, int lo, int hi,
+                                                 unsigned some) const {
+        uint32_t keep[kTokens];
+        if constexpr (EDGE) {
+#pragma unroll
+            for (int i = 0; i < kTokens; ++i) {
+                const int pos = key + token + i;
+                const bool held = ((some >> (token / kKvUnit)) & 1) && pos >= lo && pos < hi;
+                const bool nan = ((vs >> (8 * i)) & 0xFFu) == 0xFFu;
+                keep[i] = held && !nan ? ~0u : 0u;
+                marks[(token + i) * VS::kBlocks + block] = held && nan ? 1 : 0;
+            }
+        }
+        float unit[kTokens];
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) unit[i] = unit_of_byte(vs, i);
+        uint8_t *dst = slot + v_to;
+#pragma unroll
+        for (int jp = 0; jp < kDims / 2; ++jp) {
             uint32_t w[kTokens];
 #pragma unroll
             for (int i = 0; i < kTokens; ++i) {
-                w[i] = value_pair<D, VB>(v, i, jp, unit_of_byte(vs, i));
+                w[i] = value_pair<16 * kDims, VB>(v, i, jp, unit[i]);
                 if constexpr (EDGE) w[i] &= keep[i];
             }
             uint8_t *at = dst + jp * kLanes * 16;
@@ -165,16 +158,33 @@ struct WideStage {
     }
 };
 
-// The pages of the tile at `key`: lane u (u < units) that of its unit u.
+// The table's entries of the tile at `key`: lane u (u < units) that of its unit u.
+// They are made pages a tile later: a test here would wait for the load, and with
+// it for every load before it.
+__device__ __forceinline__ int wide_entries(const KvView &kv, int s, int key) {
+    return kv.entry_at(s, key + (threadIdx.x & 63) * kKvUnit);
+}
 template <int D>
-__device__ __forceinline__ int wide_pages(const KvView &kv, int s, int key, int end) {
+__device__ __forceinline__ int wide_pages(const KvView &kv, int entries, int key, int end) {
     const int u = threadIdx.x & 63, pos = key + u * kKvUnit;
-    return u < WideShape<D>::kUnits && pos < end ? kv.page_of(s, pos) : -1;
+    const bool ok = (u < WideShape<D>::kUnits) & (pos < end) & (pos < kv.capacity) & (entries >= 0) & (entries < kv.pages);
+    return ok ? entries : -1;
+}
+
+// A barrier of the workgroup that orders shared memory only: global loads stay in
+// flight across it.
+__device__ __forceinline__ void phase_barrier() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    __builtin_amdgcn_sched_barrier(0);
 }
 
 template <int D, int KB, int VB>
 __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnArgs a) {
     typedef WideShape<D> W;
+    constexpr int kSteps = W::kDimSteps / W::kHalves, kDims = W::kDimBlocks / W::kHalves;    // a wave's own
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -187,7 +197,10 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
     const KeyRange keys = key_range(a.split[1], tile, z);
     if (z > 0 && z >= keys.splits) return;
 
-    const int row = tile.row0 + wave * 32 + (lane & 31);
+    // Waves w and w + 4 share a SIMD and are in opposite phases; at D = 256 waves
+    // 2 k and 2 k + 1 share rows.
+    const int late = wave >> 2, half = W::kHalves == 2 ? wave & 1 : 0;
+    const int row = tile.row0 + (wave / W::kHalves) * 32 + (lane & 31);
     const bool in = row < tile.rows;
     const int i = in ? row / a.group : 0;
     const int token = tile.begin + i, qhead = head * a.group + (in ? row - i * a.group : 0);
@@ -195,197 +208,306 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
     const int klo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
     const int khi = in ? (a.tree ? tile.past : pos + 1) : 0;
     const unsigned long long tree = in && a.tree ? a.tree[token] : 0ull;
-    bf16x8 q[W::kDimSteps];
+    bf16x8 q[kSteps];
     {
-        const uint16_t *src = a.q + token * a.q_stride + qhead * D + 8 * h;
+        const uint16_t *src = a.q + token * a.q_stride + qhead * D + half * kSteps * 16 + 8 * h;
 #pragma unroll
-        for (int m = 0; m < W::kDimSteps; ++m) {
+        for (int m = 0; m < kSteps; ++m) {
             u32x4 w = {0, 0, 0, 0};
             if (in) w = *reinterpret_cast<const u32x4 *>(src + 16 * m);
             q[m] = __builtin_bit_cast(bf16x8, w);
         }
     }
-    floatx16 o[W::kDimBlocks];
+    floatx16 o[kDims], s[W::kBlocks32];
+    uint32_t p[W::kBlocks32][8];
+    unsigned long long seen = 0;           // in an edge tile, bit 16 b + e where score e of block b is allowed
 #pragma unroll
-    for (int d = 0; d < W::kDimBlocks; ++d) o[d] = floatx16{};
-    float mx = kNegInf, sub = 0.0f, l = 0.0f, lr = 0.0f;
+    for (int d = 0; d < kDims; ++d) o[d] = floatx16{};
+    // Weights are 2^(score - sub); l is their sum, lr the sum of the weights as
+    // rounded to bf16, which normalises the output.  lr comes from the smallest
+    // matrix instruction, whose sixteen 4 x 4 products give each lane the sum of its
+    // own four weights (dot2 runs on the matrix pipe as well, and waits for it: 60
+    // cycles each beside a busy one).
+    float sub = kNegInf, l = 0.0f;
+    floatx4 lr = {0, 0, 0, 0};
+    const s16x4 ones = {0x3F80, 0x3F80, 0x3F80, 0x3F80};
     const float scale = a.scale_log2;
+    // rows that see nothing never have a maximum, and need none
+    if (!in) sub = 0.0f;
 
-    const auto work = [&](const uint8_t *buf, int key, unsigned some, auto edge_tag) {
-        constexpr bool EDGE = decltype(edge_tag)::value != 0;
-        const bf16x8 *kop = reinterpret_cast<const bf16x8 *>(buf) + lane;
-        const bf16x8 *vop = reinterpret_cast<const bf16x8 *>(buf + W::kSide) + lane;
-        floatx16 s[W::kBlocks32];
-        float top = kNegInf;
+    // The matrix phase: the values of one tile by its weights, added to the output,
+    // then the scores of the next (its keys, rows, by the queries, columns).
+    // kAhead operands are in flight, in an order that the compiler is kept to: left
+    // to itself it waits for each pair.
+    const auto multiply = [&](int value_slot, int key_slot, auto first_tag) {
+        constexpr int kValues = decltype(first_tag)::value != 0 ? 0 : W::kUnits * kDims;
+        constexpr int kAll = kValues + W::kBlocks32 * kSteps, kAhead = 8;
+        const bf16x8 *vop = reinterpret_cast<const bf16x8 *>(lds + W::kValuesAt + value_slot * W::kSide) + half * kDims * kLanes + lane;
+        const bf16x8 *kop = reinterpret_cast<const bf16x8 *>(lds + key_slot * W::kSide) + half * kSteps * kLanes + lane;
+        const auto operand = [&](int n) {
+            if (n < kValues) return vop[(n / kDims * W::kDimBlocks + n % kDims) * kLanes];
+            n -= kValues;
+            return kop[(n % W::kBlocks32 * W::kDimSteps + n / W::kBlocks32) * kLanes];
+        };
+        bf16x8 ahead[kAhead];
 #pragma unroll
-        for (int b = 0; b < W::kBlocks32; ++b) {
-            s[b] = floatx16{};
+        for (int n = 0; n < kAhead; ++n) ahead[n] = operand(n);
+        __builtin_amdgcn_sched_barrier(0);
+        if (kValues > 0) {
+            // meanwhile: the sum of the rounded weights, each lane's own
 #pragma unroll
-            for (int m = 0; m < W::kDimSteps; ++m)
-                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(kop[(b * W::kDimSteps + m) * kLanes], q[m], s[b], 0, 0, 0);
+            for (int w = 0; w < 4 * W::kUnits; w += 2)
+                lr = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(s16x4, u32x2{p[w >> 3][w & 7], p[w >> 3][(w & 7) + 1]}), lr, 0, 0, 0);
         }
-        unsigned ones[W::kBlocks32];          // EDGE: bit e where score e of the block is allowed
 #pragma unroll
-        for (int b = 0; b < W::kBlocks32; ++b) {
-            if constexpr (EDGE) {
-                ones[b] = 0;
+        for (int b = 0; b < W::kBlocks32; ++b) s[b] = floatx16{};
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const int at = key + b * 32 + 8 * (e >> 2) + 4 * h + (e & 3);
-                    bool ok = at >= klo && at < khi;
-                    if (a.tree) {
-                        const int t = at - tile.past;
-                        ok = ok || (t >= 0 && t < tile.n && t < 64 && ((tree >> (t & 63)) & 1));
-                    }
-                    ok = ok && ((some >> (2 * b + (e >> 3))) & 1) && at < tile.hi;
-                    if (!ok) s[b][e] = kNegInf;
-                    ones[b] |= ok ? 1u << e : 0u;
+        for (int n = 0; n < kAll; ++n) {
+            if (n < kValues) {
+                const int u = n / kDims;
+                const uint32_t *w = &p[u >> 1][4 * (u & 1)];
+                o[n % kDims] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ahead[n % kAhead], __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}), o[n % kDims], 0, 0, 0);
+            } else {
+                const int b = (n - kValues) % W::kBlocks32, m = (n - kValues) / W::kBlocks32;
+                s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ahead[n % kAhead], q[m], s[b], 0, 0, 0);
+            }
+            if (n + kAhead < kAll) ahead[n % kAhead] = operand(n + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // In an edge tile NaN blocks, left out of the values, reach the rows that see
+    // their keys: the product of the marks with the allowed keys tells which.
+    unsigned nan_rows = 0;                 // bit e: accumulator element e is NaN
+    const auto spread_nan = [&](int slot) {
+        static_assert(W::kMarks == 256, "a word of marks per lane");
+        const uint8_t *marks = lds + W::kMarksAt + slot * W::kMarks;
+        if (!__any(reinterpret_cast<const uint32_t *>(marks)[lane] != 0)) return;
+        const int block = (lane & 15) * (D / kMxBlock) / 16;
+#pragma unroll 1
+        for (int u = 0; u < W::kUnits; ++u) {
+            const unsigned now = unsigned(seen >> (8 * u));
+            u32x4 mark, on;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                mark[e] = on[e] = 0;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int at = 2 * e + k, t = 8 * (at >> 2) + 4 * h + (at & 3);
+                    mark[e] |= (marks[(u * kKvUnit + t) * (D / kMxBlock) + block] ? 0x3F80u : 0u) << (16 * k);
+                    on[e] |= ((now >> at) & 1 ? 0x3F80u : 0u) << (16 * k);
                 }
             }
+            const floatx16 n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, mark), __builtin_bit_cast(bf16x8, on), floatx16{}, 0, 0, 0);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+            for (int e = 0; e < 16; ++e) nan_rows |= unsigned(n[e] > 0.0f) << e;
         }
-        top *= scale;
-        if (__any(top > mx + kMaxSlack)) {
+    };
+    // scores -> weights, and the running maximum and sums
+    const auto softmax = [&](int key, unsigned some, bool edge) {
+        if (edge) {
+            const int last = min(khi, tile.hi);
+            seen = 0;
+#pragma unroll
+            for (int b = 0; b < W::kBlocks32; ++b) {
+                const int base = key + b * 32 + 4 * h;
+                unsigned ok = 0;
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const int at = base + 8 * (e >> 2) + (e & 3);
+                    ok |= unsigned((at >= klo) & (at < last)) << e;
+                }
+                if (a.tree) {
+                    const int drafted = min(min(tile.n, 64), tile.hi - tile.past);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        const int t = base + 8 * (e >> 2) + (e & 3) - tile.past;
+                        ok |= (unsigned((t >= 0) & (t < drafted)) & unsigned(tree >> (t & 63))) << e;
+                    }
+                }
+                ok &= (((some >> (2 * b)) & 1) ? 0xFFu : 0u) | (((some >> (2 * b + 1)) & 1) ? 0xFF00u : 0u);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) s[b][e] = (ok >> e) & 1u ? s[b][e] : kNegInf;
+                seen |= static_cast<unsigned long long>(ok) << (16 * b);
+            }
+        }
+        // The weights, against the reference that earlier tiles left.  It moves up
+        // only where their sum shows a weight too large (or none was set), so most
+        // tiles never look for their maximum.
+        float sum[4];
+        const auto exponentials = [&](float ref) {
+#pragma unroll
+            for (int b = 0; b < W::kBlocks32; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; e += 2) {
+                    const float x = exp2_fast(__builtin_fmaf(s[b][e], scale, -ref));
+                    const float y = exp2_fast(__builtin_fmaf(s[b][e + 1], scale, -ref));
+                    float &to = sum[e / 2 % 4];        // four chains: one would wait for itself
+                    to = b == 0 && e < 8 ? x + y : to + (x + y);
+                    p[b][e / 2] = pack_bf16(x, y);
+                }
+            return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        };
+        float total = exponentials(sub == kNegInf ? 0.0f : sub);
+        if (__any(sub == kNegInf || total > kMaxSum)) {
+            float top = kNegInf;
+#pragma unroll
+            for (int b = 0; b < W::kBlocks32; ++b)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) top = fmaxf(top, s[b][e]);
+            top *= scale;
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float m = fmaxf(mx, top);
-            const float by = m == mx ? 1.0f : exp2_fast(mx - m);
-            mx = m;
-            sub = m == kNegInf ? 0.0f : m;
+            const float m = fmaxf(sub, top);
+            const float by = m == sub ? 1.0f : exp2_fast(sub - m);
+            sub = m;
             l *= by;
             lr *= by;
 #pragma unroll
-            for (int d = 0; d < W::kDimBlocks; ++d) o[d] *= by;
+            for (int d = 0; d < kDims; ++d) o[d] *= by;
+            total = exponentials(sub == kNegInf ? 0.0f : sub);
         }
-#pragma unroll
-        for (int b = 0; b < W::kBlocks32; ++b) {
-            uint32_t p[8];
-#pragma unroll
-            for (int e = 0; e < 16; e += 2) {
-                const float x = exp2_fast(__builtin_fmaf(s[b][e], scale, -sub));
-                const float y = exp2_fast(__builtin_fmaf(s[b][e + 1], scale, -sub));
-                l += x;
-                l += y;
-                p[e / 2] = pack_bf16(x, y);
-                lr = add_pair(p[e / 2], lr);
-            }
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[4 * u], p[4 * u + 1], p[4 * u + 2], p[4 * u + 3]});
-#pragma unroll
-                for (int d = 0; d < W::kDimBlocks; ++d)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(vop[((2 * b + u) * W::kDimBlocks + d) * kLanes], pb, o[d], 0, 0, 0);
-            }
-        }
-        if constexpr (EDGE) {
-            // NaN blocks, left out of the product above, reach the rows that see
-            // their keys: the product of the marks with the allowed keys tells
-            const uint8_t *marks = buf + 2 * W::kSide;
-            const uint32_t word = *reinterpret_cast<const uint32_t *>(marks + 4 * lane);      // kMarks is 256
-            if (__any(word != 0)) {
-                const int block = (lane & 15) * (D / kMxBlock) / 16;
-#pragma unroll
-                for (int u = 0; u < W::kUnits; ++u) {
-                    u32x4 mark, on;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t two = 0, two1 = 0;
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int slot = 2 * e + k, t = 8 * (slot >> 2) + 4 * h + (slot & 3);
-                            two |= (marks[(u * kKvUnit + t) * (D / kMxBlock) + block] ? 0x3F80u : 0u) << (16 * k);
-                            two1 |= ((ones[u >> 1] >> (8 * (u & 1) + slot)) & 1 ? 0x3F80u : 0u) << (16 * k);
-                        }
-                        mark[e] = two;
-                        on[e] = two1;
-                    }
-                    const floatx16 n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, mark), __builtin_bit_cast(bf16x8, on), floatx16{}, 0, 0, 0);
-#pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (n[e] > 0.0f)
-#pragma unroll
-                            for (int d = 0; d < W::kDimBlocks; ++d) o[d][e] = __builtin_nanf("");
-                }
-            }
-        }
+        l += total;
     };
 
-    // The walk.  Of tile t: its page numbers are loaded at t - 3, its codes at
-    // t - 2, decoded at t - 1.
-    static_assert(W::kMarks == 256, "a word of marks per lane");
     const unsigned all = (1u << W::kUnits) - 1;
     const auto valid = [&](int pages) { return unsigned(__ballot(pages >= 0)) & all; };
     const auto is_edge = [&](int key, unsigned some) {
-        return key < tile.inner_lo || key + W::kKeys > min(tile.inner_hi, keys.hi) || some != all;
+        return (key < tile.inner_lo) | (key + W::kKeys > min(tile.inner_hi, keys.hi)) | (some != all);
     };
-    WideStage<D, KB, VB> stage;
-    if (keys.lo < keys.hi) {
-        int key = keys.lo;
-        int pages = wide_pages<D>(a.kv, tile.s, key, keys.hi);
-        stage.load(a.kv, pages, head, key);
-        unsigned some = valid(pages), some1;
-        pages = wide_pages<D>(a.kv, tile.s, key + W::kKeys, keys.hi);
-        if (is_edge(key, some)) stage.template store<true>(lds, key, tile.lo, tile.hi, some);
-        else stage.template store<false>(lds, key, tile.lo, tile.hi, some);
-        stage.load(a.kv, pages, head, key + W::kKeys);
+    const int tiles = (max(keys.hi - keys.lo, 0) + W::kKeys - 1) / W::kKeys;
+    if (tiles > 0) {
+        WideStage<D, KB, VB> stage;
+        const auto key_at = [&](int t) { return keys.lo + t * W::kKeys; };
+        const auto entries_at = [&](int t) { return wide_entries(a.kv, tile.s, key_at(t)); };
+        const auto pages_of = [&](int entries, int t) { return wide_pages<D>(a.kv, entries, key_at(t), keys.hi); };
+        const auto put_values = [&](int t, int slot, unsigned some, bool edge) {
+            uint8_t *const to = lds + W::kValuesAt + slot * W::kSide, *const marks = lds + W::kMarksAt + slot * W::kMarks;
+            if (edge) stage.template store_values<true>(to, marks, key_at(t), tile.lo, tile.hi, some);
+            else stage.template store_values<false>(to, marks, key_at(t), tile.lo, tile.hi, some);
+        };
+        const int my_unit = wave * kLanes / WideStage<D, KB, VB>::kItems;
+        const auto unit_in = [&](int pages, int t) {
+            return a.kv.unit_of(max(__builtin_amdgcn_readlane(pages, my_unit), 0), head, key_at(t) + my_unit * kKvUnit);
+        };
+        // some0..: which units of tiles t, t + 1, .. have pages
+        const int entries0 = entries_at(0), entries1 = entries_at(1), entries2 = entries_at(2);
+        int entries = entries_at(3);              // of tile t + 3
+        int pages = pages_of(entries0, 0);
+        unsigned some0 = valid(pages), some1, some2;
+        int64_t unit = unit_in(pages, 0);
+        stage.load_keys(a.kv, unit);
+        stage.load_values(a.kv, unit);
+        stage.store_keys(lds);
+        bool edge = is_edge(key_at(0), some0);
+        put_values(0, 0, some0, edge);
+        pages = pages_of(entries1, 1);
         some1 = valid(pages);
-        pages = wide_pages<D>(a.kv, tile.s, key + 2 * W::kKeys, keys.hi);
-        __syncthreads();
-        for (int buf = 0;; buf ^= 1) {
-            const int next = key + W::kKeys;
-            uint8_t *const other = lds + (buf ^ 1) * W::kBuffer;
-            if (next < keys.hi) {
-                if (is_edge(next, some1)) stage.template store<true>(other, next, tile.lo, tile.hi, some1);
-                else stage.template store<false>(other, next, tile.lo, tile.hi, some1);
-                stage.load(a.kv, pages, head, next + W::kKeys);
-            }
-            const unsigned some2 = valid(pages);
-            pages = wide_pages<D>(a.kv, tile.s, next + 2 * W::kKeys, keys.hi);
-            if (is_edge(key, some)) work(lds + buf * W::kBuffer, key, some, IntC<1>());
-            else work(lds + buf * W::kBuffer, key, some, IntC<0>());
-            key = next;
-            if (key >= keys.hi) break;
-            some = some1;
+        unit = unit_in(pages, 1);
+        stage.load_keys(a.kv, unit);
+        stage.load_values(a.kv, unit);
+        stage.store_keys(lds + W::kSide);
+        pages = pages_of(entries2, 2);
+        some2 = valid(pages);
+        unit = unit_in(pages, 2);                 // of tile t + 2
+        stage.load_keys(a.kv, unit);
+        phase_barrier();
+        if (late) phase_barrier();
+        // D = 256: the halves of the scores meet
+        floatx4 *const shared = reinterpret_cast<floatx4 *>(lds + W::kScoresAt) + lane;
+        const auto give_scores = [&] {
+            if constexpr (W::kHalves == 2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    shared[(wave * 4 + e) * kLanes] = floatx4{s[0][4 * e], s[0][4 * e + 1], s[0][4 * e + 2], s[0][4 * e + 3]};
+        };
+        const auto take_scores = [&] {
+            if constexpr (W::kHalves == 2)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const floatx4 x = shared[((wave ^ 1) * 4 + e) * kLanes];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) s[0][4 * e + k] += x[k];
+                }
+        };
+        multiply(0, 0, IntC<1>());
+        give_scores();
+        phase_barrier();
+        int slot = 0;                             // of tile t
+        for (int t = 0; t < tiles; ++t) {
+            const int slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
+            // The page numbers of tile t + 3 first: their load is older than those
+            // that follow, and waiting for it later would be waiting for them.
+            // Nothing here asks whether the tiles to come exist: past the last
+            // one, loads go to some page and stores to slots that nobody reads.
+            pages = pages_of(entries, t + 3);
+            entries = entries_at(t + 4);
+            take_scores();
+            softmax(key_at(t), some0, edge);
+            if (edge) spread_nan(slot);
+            edge = is_edge(key_at(t + 1), some1);
+            put_values(t + 1, slot1, some1, edge);
+            stage.store_keys(lds + slot2 * W::kSide);
+            stage.load_values(a.kv, unit);
+            unit = unit_in(pages, t + 3);
+            stage.load_keys(a.kv, unit);
+            some0 = some1;
             some1 = some2;
-            __syncthreads();
+            some2 = valid(pages);
+            phase_barrier();
+            // after the last tile the scores are of old keys, and unused
+            __builtin_amdgcn_s_setprio(1);
+            multiply(slot, slot1, IntC<0>());
+            __builtin_amdgcn_s_setprio(0);
+            give_scores();
+            phase_barrier();
+            slot = slot1;
         }
+        if (!late) phase_barrier();
     }
 
+    if (nan_rows != 0) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e)
+#pragma unroll
+            for (int d = 0; d < kDims; ++d) o[d][e] = (nan_rows >> e) & 1 ? __builtin_nanf("") : o[d][e];
+    }
     l += __shfl_xor(l, 32);
-    lr += __shfl_xor(lr, 32);
+    const float norm = lr[0] + __shfl_xor(lr[0], 32);
     if (!in) return;
     const int64_t at = int64_t(token) * a.q_heads + qhead;
     // lane (h, row) holds value rows r = 8 x + 4 h + y, each D / 16 elements in
-    // a row: element 2 d + jj of it in o[d][8 jj + 4 x + y]
+    // a row: element 2 d + jj of it in accumulator d's 8 jj + 4 x + y
     constexpr int kRowDims = D / 16;
+    const int first = half * kDims * 2;          // of the row's elements that are this wave's
     if (keys.splits > 1) {
-        float *dst = a.part_o + (int64_t(z) * a.kv.tokens * a.q_heads + at) * D;
+        float *dst = a.part_o + (int64_t(z) * a.kv.tokens * a.q_heads + at) * D + first;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
             for (int y = 0; y < 4; ++y)
 #pragma unroll
-                for (int j = 0; j < kRowDims; j += 4) {
+                for (int d = 0; d < kDims; d += 2) {
                     const int e = 4 * x + y;
-                    *reinterpret_cast<float4 *>(dst + (8 * x + 4 * h + y) * kRowDims + j) =
-                        float4{o[j / 2][e], o[j / 2][8 + e], o[j / 2 + 1][e], o[j / 2 + 1][8 + e]};
+                    *reinterpret_cast<float4 *>(dst + (8 * x + 4 * h + y) * kRowDims + 2 * d) =
+                        float4{o[d][e], o[d][8 + e], o[d + 1][e], o[d + 1][8 + e]};
                 }
-        if (h == 0) *reinterpret_cast<float4 *>(a.part_ml + (int64_t(z) * a.kv.tokens * a.q_heads + at) * 4) = float4{mx, l, lr, 0.0f};
+        if (h == 0 && half == 0)
+            *reinterpret_cast<float4 *>(a.part_ml + (int64_t(z) * a.kv.tokens * a.q_heads + at) * 4) = float4{sub, l, norm, 0.0f};
         return;
     }
-    const float inv = mx == kNegInf && l == 0.0f ? 0.0f : 1.0f / lr;
-    uint16_t *dst = a.out + token * a.out_stride + qhead * D;
+    const float inv = sub == kNegInf && l == 0.0f ? 0.0f : 1.0f / norm;
+    uint16_t *dst = a.out + token * a.out_stride + qhead * D + first;
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
         for (int y = 0; y < 4; ++y)
 #pragma unroll
-            for (int j = 0; j < kRowDims; j += 4) {
+            for (int d = 0; d < kDims; d += 2) {
                 const int e = 4 * x + y;
-                *reinterpret_cast<u32x2 *>(dst + (8 * x + 4 * h + y) * kRowDims + j) =
-                    u32x2{pack_bf16(o[j / 2][e] * inv, o[j / 2][8 + e] * inv), pack_bf16(o[j / 2 + 1][e] * inv, o[j / 2 + 1][8 + e] * inv)};
+                *reinterpret_cast<u32x2 *>(dst + (8 * x + 4 * h + y) * kRowDims + 2 * d) =
+                    u32x2{pack_bf16(o[d][e] * inv, o[d][8 + e] * inv), pack_bf16(o[d + 1][e] * inv, o[d + 1][8 + e] * inv)};
             }
-    if (a.lse && h == 0) a.lse[at] = lse_of(mx, l);
+    if (a.lse && h == 0 && half == 0) a.lse[at] = lse_of(sub, l);
 }
 
 // The kernels' shared memory passes the default limit; it is raised once per

@@ -62,9 +62,15 @@ struct KvView {
     }
     // The page of sequence s's position `pos`, or -1 where the table has none.
     __device__ __forceinline__ int page_of(int s, int pos) const {
-        if (pos < 0 || pos >= capacity) return -1;
-        const int p = table[int64_t(s) * width + (pos >> page_shift)];
-        return p >= 0 && p < pages ? p : -1;
+        return page_in(entry_at(s, pos), pos);
+    }
+    // The same in two steps, for loads ahead of their use: the table's entry (any
+    // one where `pos` is past the table), then the page.
+    __device__ __forceinline__ int entry_at(int s, int pos) const {
+        return table[int64_t(s) * width + (min(max(pos, 0), capacity - 1) >> page_shift)];
+    }
+    __device__ __forceinline__ int page_in(int entry, int pos) const {
+        return pos >= 0 && pos < capacity && entry >= 0 && entry < pages ? entry : -1;
     }
     // The unit (of a head's units in the whole pool) of position `pos` in page `p`.
     __device__ __forceinline__ int64_t unit_of(int p, int head, int pos) const {
