@@ -39,7 +39,7 @@ struct WideShape {
     static constexpr int kDimBlocks = D / 32;          // accumulators of the output
     static constexpr int kSide = kKeys * D * 2;        // bytes of a tile's keys (and of its values): 16 KiB
     static constexpr int kMarks = kKeys * (D / kMxBlock);
-    static constexpr int kRing = 3;
+    static constexpr int kRing = 2;
     // shared memory: keys, values, marks, and the halves' scores
     static constexpr int kValuesAt = kRing * kSide;
     static constexpr int kMarksAt = 2 * kRing * kSide;
@@ -106,55 +106,57 @@ struct WideStage {
         }
         load_words<kTokens>(kv.scales[1] + unit * VS::kUnitScales + vs_at, &vs);
     }
-    // Decode to the operands of a ring slot.
-    __device__ __forceinline__ void store_keys(uint8_t *slot) const {
-        const float scale = __uint_as_float(ks << 23);
-        bf16x8 *dst = reinterpret_cast<bf16x8 *>(slot + k_to);
-        if constexpr (KB == 8) {
-            dst[0] = codes8(k[0], k[1], scale);
-            dst[32] = codes8(k[2], k[3], scale);
-        } else {
-            dst[0] = codes4(k[0], scale);
-            dst[32] = codes4(k[1], scale);
+    // In an edge tile: values of keys outside lo..hi - 1 or without a page, and NaN
+    // blocks, become zeros, the latter marked.
+    __device__ __forceinline__ void clear_values(uint8_t *marks, int key, int lo, int hi, unsigned some) {
+#pragma unroll
+        for (int i = 0; i < kTokens; ++i) {
+            const int pos = key + token + i;
+            const bool held = ((some >> (token / kKvUnit)) & 1) && pos >= lo && pos < hi;
+            const bool nan = ((vs >> (8 * i)) & 0xFFu) == 0xFFu;
+            marks[(token + i) * VS::kBlocks + block] = held && nan ? 1 : 0;
+            if (held && !nan) continue;
+            vs &= ~(0xFFu << (8 * i));
+#pragma unroll
+            for (int w = 0; w < kValueWords; ++w) {
+                // the bits of word w that are token i's
+                constexpr int kBits = kDims * VB;
+                const int from = i * kBits - 32 * w, to = from + kBits;
+                const uint32_t mine = to <= 0 || from >= 32 ? 0u
+                                      : (to >= 32 ? ~0u : (1u << to) - 1u) & (from <= 0 ? ~0u : ~0u << from);
+                v[w] &= ~mine;
+            }
         }
     }
-    // EDGE: values of keys outside lo..hi - 1 or without a page, and NaN blocks,
-    // become zeros, the latter marked.
-    template <bool EDGE>
-    __device__ __forceinline__ void store_values(uint8_t *slot, uint8_t *marks, int key, int lo, int hi,
-                                                 unsigned some) const {
-        uint32_t keep[kTokens];
-        if constexpr (EDGE) {
+    // The decode to the operands of ring slots, in steps that stand between matrix
+    // instructions: first the values' kDims / 2, then the keys' two.
+    static constexpr int kValueSteps = kDims / 2, kKeySteps = 2;
+    __device__ __forceinline__ void store_value_step(uint8_t *slot, int jp) const {
+        uint32_t w[kTokens];
 #pragma unroll
-            for (int i = 0; i < kTokens; ++i) {
-                const int pos = key + token + i;
-                const bool held = ((some >> (token / kKvUnit)) & 1) && pos >= lo && pos < hi;
-                const bool nan = ((vs >> (8 * i)) & 0xFFu) == 0xFFu;
-                keep[i] = held && !nan ? ~0u : 0u;
-                marks[(token + i) * VS::kBlocks + block] = held && nan ? 1 : 0;
-            }
+        for (int i = 0; i < kTokens; ++i) w[i] = value_pair<16 * kDims, VB>(v, i, jp, unit_of_byte(vs, i));
+        uint8_t *at = slot + v_to + jp * kLanes * 16;
+        if constexpr (kTokens == 4) {
+            *reinterpret_cast<u32x2 *>(at) = u32x2{low_halves(w[0], w[1]), low_halves(w[2], w[3])};
+            *reinterpret_cast<u32x2 *>(at + 16 * 16) = u32x2{high_halves(w[0], w[1]), high_halves(w[2], w[3])};
+        } else {
+            *reinterpret_cast<uint32_t *>(at) = low_halves(w[0], w[1]);
+            *reinterpret_cast<uint32_t *>(at + 16 * 16) = high_halves(w[0], w[1]);
         }
-        float unit[kTokens];
+    }
+    __device__ __forceinline__ void store_key_step(uint8_t *slot, int n) const {
+        const float scale = __uint_as_float(ks << 23);
+        bf16x8 *dst = reinterpret_cast<bf16x8 *>(slot + k_to);
+        if constexpr (KB == 8) dst[32 * n] = codes8(k[2 * n], k[2 * n + 1], scale);
+        else dst[32 * n] = codes4(k[n], scale);
+    }
+    __device__ __forceinline__ void store_values(uint8_t *slot) const {
 #pragma unroll
-        for (int i = 0; i < kTokens; ++i) unit[i] = unit_of_byte(vs, i);
-        uint8_t *dst = slot + v_to;
+        for (int n = 0; n < kValueSteps; ++n) store_value_step(slot, n);
+    }
+    __device__ __forceinline__ void store_keys(uint8_t *slot) const {
 #pragma unroll
-        for (int jp = 0; jp < kDims / 2; ++jp) {
-            uint32_t w[kTokens];
-#pragma unroll
-            for (int i = 0; i < kTokens; ++i) {
-                w[i] = value_pair<16 * kDims, VB>(v, i, jp, unit[i]);
-                if constexpr (EDGE) w[i] &= keep[i];
-            }
-            uint8_t *at = dst + jp * kLanes * 16;
-            if constexpr (kTokens == 4) {
-                *reinterpret_cast<u32x2 *>(at) = u32x2{low_halves(w[0], w[1]), low_halves(w[2], w[3])};
-                *reinterpret_cast<u32x2 *>(at + 16 * 16) = u32x2{high_halves(w[0], w[1]), high_halves(w[2], w[3])};
-            } else {
-                *reinterpret_cast<uint32_t *>(at) = low_halves(w[0], w[1]);
-                *reinterpret_cast<uint32_t *>(at + 16 * 16) = high_halves(w[0], w[1]);
-            }
-        }
+        for (int n = 0; n < kKeySteps; ++n) store_key_step(slot, n);
     }
 };
 
@@ -239,7 +241,7 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
     // then the scores of the next (its keys, rows, by the queries, columns).
     // kAhead operands are in flight, in an order that the compiler is kept to: left
     // to itself it waits for each pair.
-    const auto multiply = [&](int value_slot, int key_slot, auto first_tag) {
+    const auto multiply = [&](int value_slot, int key_slot, auto first_tag, auto between) {
         constexpr int kValues = decltype(first_tag)::value != 0 ? 0 : W::kUnits * kDims;
         constexpr int kAll = kValues + W::kBlocks32 * kSteps, kAhead = 8;
         const bf16x8 *vop = reinterpret_cast<const bf16x8 *>(lds + W::kValuesAt + value_slot * W::kSide) + half * kDims * kLanes + lane;
@@ -273,6 +275,7 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
                 s[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(ahead[n % kAhead], q[m], s[b], 0, 0, 0);
             }
             if (n + kAhead < kAll) ahead[n % kAhead] = operand(n + kAhead);
+            between(n);
             __builtin_amdgcn_sched_barrier(0);
         }
     };
@@ -380,16 +383,15 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
         const auto key_at = [&](int t) { return keys.lo + t * W::kKeys; };
         const auto entries_at = [&](int t) { return wide_entries(a.kv, tile.s, key_at(t)); };
         const auto pages_of = [&](int entries, int t) { return wide_pages<D>(a.kv, entries, key_at(t), keys.hi); };
-        const auto put_values = [&](int t, int slot, unsigned some, bool edge) {
-            uint8_t *const to = lds + W::kValuesAt + slot * W::kSide, *const marks = lds + W::kMarksAt + slot * W::kMarks;
-            if (edge) stage.template store_values<true>(to, marks, key_at(t), tile.lo, tile.hi, some);
-            else stage.template store_values<false>(to, marks, key_at(t), tile.lo, tile.hi, some);
-        };
         const int my_unit = wave * kLanes / WideStage<D, KB, VB>::kItems;
         const auto unit_in = [&](int pages, int t) {
             return a.kv.unit_of(max(__builtin_amdgcn_readlane(pages, my_unit), 0), head, key_at(t) + my_unit * kKvUnit);
         };
-        // some0..: which units of tiles t, t + 1, .. have pages
+        const auto values_slot = [&](int slot) { return lds + W::kValuesAt + slot * W::kSide; };
+        const auto marks_slot = [&](int slot) { return lds + W::kMarksAt + slot * W::kMarks; };
+        // Tile t's keys and values are in slot t mod 2.  some0, some1, ..: which
+        // units of tiles t, t + 1, .. have pages; unit: the wave's unit of tile
+        // t + 2, whose keys are loaded; the values of tile t + 1 are.
         const int entries0 = entries_at(0), entries1 = entries_at(1), entries2 = entries_at(2);
         int entries = entries_at(3);              // of tile t + 3
         int pages = pages_of(entries0, 0);
@@ -397,9 +399,10 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
         int64_t unit = unit_in(pages, 0);
         stage.load_keys(a.kv, unit);
         stage.load_values(a.kv, unit);
-        stage.store_keys(lds);
         bool edge = is_edge(key_at(0), some0);
-        put_values(0, 0, some0, edge);
+        stage.store_keys(lds);
+        if (edge) stage.clear_values(marks_slot(0), key_at(0), tile.lo, tile.hi, some0);
+        stage.store_values(values_slot(0));
         pages = pages_of(entries1, 1);
         some1 = valid(pages);
         unit = unit_in(pages, 1);
@@ -408,7 +411,7 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
         stage.store_keys(lds + W::kSide);
         pages = pages_of(entries2, 2);
         some2 = valid(pages);
-        unit = unit_in(pages, 2);                 // of tile t + 2
+        unit = unit_in(pages, 2);
         stage.load_keys(a.kv, unit);
         phase_barrier();
         if (late) phase_barrier();
@@ -429,12 +432,11 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
                     for (int k = 0; k < 4; ++k) s[0][4 * e + k] += x[k];
                 }
         };
-        multiply(0, 0, IntC<1>());
+        multiply(0, 0, IntC<1>(), [](int) {});
         give_scores();
         phase_barrier();
-        int slot = 0;                             // of tile t
         for (int t = 0; t < tiles; ++t) {
-            const int slot1 = slot == 2 ? 0 : slot + 1, slot2 = slot1 == 2 ? 0 : slot1 + 1;
+            const int slot = t & 1;
             // The page numbers of tile t + 3 first: their load is older than those
             // that follow, and waiting for it later would be waiting for them.
             // Nothing here asks whether the tiles to come exist: past the last
@@ -445,22 +447,32 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
             softmax(key_at(t), some0, edge);
             if (edge) spread_nan(slot);
             edge = is_edge(key_at(t + 1), some1);
-            put_values(t + 1, slot1, some1, edge);
-            stage.store_keys(lds + slot2 * W::kSide);
-            stage.load_values(a.kv, unit);
-            unit = unit_in(pages, t + 3);
-            stage.load_keys(a.kv, unit);
+            if (edge) stage.clear_values(marks_slot(slot ^ 1), key_at(t + 1), tile.lo, tile.hi, some1);
             some0 = some1;
             some1 = some2;
             some2 = valid(pages);
             phase_barrier();
-            // after the last tile the scores are of old keys, and unused
+            // Tile t's values and tile t + 1's keys (after the last tile: unused
+            // scores of old keys); meanwhile tile t + 1's values and tile t + 2's
+            // keys are decoded, and the next ones' codes loaded.
             __builtin_amdgcn_s_setprio(1);
-            multiply(slot, slot1, IntC<0>());
+            multiply(slot, slot ^ 1, IntC<0>(), [&](int n) {
+                typedef WideStage<D, KB, VB> S;
+                constexpr int kValuesDone = 1 + 2 * S::kValueSteps, kKeysDone = kValuesDone + 2 * S::kKeySteps;
+                if (n < kValuesDone) {
+                    if (n & 1) stage.store_value_step(values_slot(slot ^ 1), n / 2);
+                } else if (n < kKeysDone) {
+                    if (n & 1) stage.store_key_step(lds + slot * W::kSide, (n - kValuesDone) / 2);
+                } else if (n == kKeysDone) {
+                    stage.load_values(a.kv, unit);
+                    unit = unit_in(pages, t + 3);
+                } else if (n == kKeysDone + 1) {
+                    stage.load_keys(a.kv, unit);
+                }
+            });
             __builtin_amdgcn_s_setprio(0);
             give_scores();
             phase_barrier();
-            slot = slot1;
         }
         if (!late) phase_barrier();
     }
