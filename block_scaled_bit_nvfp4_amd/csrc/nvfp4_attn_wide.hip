@@ -128,33 +128,51 @@ struct WideStage {
             }
         }
     }
-    // The decode to the operands of ring slots, in steps that stand between matrix
-    // instructions: first the values' kDims / 2, then the keys' two.
-    static constexpr int kValueSteps = kDims / 2, kKeySteps = 2;
-    __device__ __forceinline__ void store_value_step(uint8_t *slot, int jp) const {
-        uint32_t w[kTokens];
+    // The decode to the operands of ring slots in steps of a few instructions,
+    // which stand between matrix instructions: the values' pairs of elements, each
+    // converted, then paired over tokens and stored; and the keys' two halves.
+    uint32_t held[4];
+    static constexpr int kValueSteps = kDims, kKeySteps = 4;
+    __device__ __forceinline__ void store_value_step(uint8_t *slot, int n) {
+        const int jp = n / 2;
+        if (n % 2 == 0) {
 #pragma unroll
-        for (int i = 0; i < kTokens; ++i) w[i] = value_pair<16 * kDims, VB>(v, i, jp, unit_of_byte(vs, i));
+            for (int i = 0; i < kTokens; ++i) held[i] = value_pair<16 * kDims, VB>(v, i, jp, unit_of_byte(vs, i));
+            return;
+        }
         uint8_t *at = slot + v_to + jp * kLanes * 16;
         if constexpr (kTokens == 4) {
-            *reinterpret_cast<u32x2 *>(at) = u32x2{low_halves(w[0], w[1]), low_halves(w[2], w[3])};
-            *reinterpret_cast<u32x2 *>(at + 16 * 16) = u32x2{high_halves(w[0], w[1]), high_halves(w[2], w[3])};
+            *reinterpret_cast<u32x2 *>(at) = u32x2{low_halves(held[0], held[1]), low_halves(held[2], held[3])};
+            *reinterpret_cast<u32x2 *>(at + 16 * 16) = u32x2{high_halves(held[0], held[1]), high_halves(held[2], held[3])};
         } else {
-            *reinterpret_cast<uint32_t *>(at) = low_halves(w[0], w[1]);
-            *reinterpret_cast<uint32_t *>(at + 16 * 16) = high_halves(w[0], w[1]);
+            *reinterpret_cast<uint32_t *>(at) = low_halves(held[0], held[1]);
+            *reinterpret_cast<uint32_t *>(at + 16 * 16) = high_halves(held[0], held[1]);
         }
     }
-    __device__ __forceinline__ void store_key_step(uint8_t *slot, int n) const {
+    __device__ __forceinline__ void store_key_step(uint8_t *slot, int n) {
         const float scale = __uint_as_float(ks << 23);
-        bf16x8 *dst = reinterpret_cast<bf16x8 *>(slot + k_to);
-        if constexpr (KB == 8) dst[32 * n] = codes8(k[2 * n], k[2 * n + 1], scale);
-        else dst[32 * n] = codes4(k[n], scale);
+        const int half = n / 2;
+        // words 2 (n mod 2) and the next of the operand
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int pair = 2 * (n % 2) + i;      // of the half's eight elements
+            uint32_t x;
+            if constexpr (KB == 8)
+                x = as_u32(i ? __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(k[2 * half + n % 2], scale, true)
+                             : __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(k[2 * half + n % 2], scale, false));
+            else if (pair == 0) x = as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(k[half], scale, 0));
+            else if (pair == 1) x = as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(k[half], scale, 1));
+            else if (pair == 2) x = as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(k[half], scale, 2));
+            else x = as_u32(__builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(k[half], scale, 3));
+            held[pair] = x;
+        }
+        if (n % 2 == 1) reinterpret_cast<u32x4 *>(slot + k_to)[32 * half] = u32x4{held[0], held[1], held[2], held[3]};
     }
-    __device__ __forceinline__ void store_values(uint8_t *slot) const {
+    __device__ __forceinline__ void store_values(uint8_t *slot) {
 #pragma unroll
         for (int n = 0; n < kValueSteps; ++n) store_value_step(slot, n);
     }
-    __device__ __forceinline__ void store_keys(uint8_t *slot) const {
+    __device__ __forceinline__ void store_keys(uint8_t *slot) {
 #pragma unroll
         for (int n = 0; n < kKeySteps; ++n) store_key_step(slot, n);
     }
@@ -451,6 +469,7 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
             some0 = some1;
             some1 = some2;
             some2 = valid(pages);
+            const int64_t unit1 = unit_in(pages, t + 3);
             phase_barrier();
             // Tile t's values and tile t + 1's keys (after the last tile: unused
             // scores of old keys); meanwhile tile t + 1's values and tile t + 2's
@@ -458,20 +477,15 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
             __builtin_amdgcn_s_setprio(1);
             multiply(slot, slot ^ 1, IntC<0>(), [&](int n) {
                 typedef WideStage<D, KB, VB> S;
-                constexpr int kValuesDone = 1 + 2 * S::kValueSteps, kKeysDone = kValuesDone + 2 * S::kKeySteps;
-                if (n < kValuesDone) {
-                    if (n & 1) stage.store_value_step(values_slot(slot ^ 1), n / 2);
-                } else if (n < kKeysDone) {
-                    if (n & 1) stage.store_key_step(lds + slot * W::kSide, (n - kValuesDone) / 2);
-                } else if (n == kKeysDone) {
-                    stage.load_values(a.kv, unit);
-                    unit = unit_in(pages, t + 3);
-                } else if (n == kKeysDone + 1) {
-                    stage.load_keys(a.kv, unit);
-                }
+                constexpr int kKeysFrom = S::kValueSteps, kLoadsFrom = kKeysFrom + S::kKeySteps;
+                if (n < kKeysFrom) stage.store_value_step(values_slot(slot ^ 1), n);
+                else if (n < kLoadsFrom) stage.store_key_step(lds + slot * W::kSide, n - kKeysFrom);
+                else if (n == kLoadsFrom) stage.load_values(a.kv, unit);
+                else if (n == kLoadsFrom + 1) stage.load_keys(a.kv, unit1);
             });
             __builtin_amdgcn_s_setprio(0);
             give_scores();
+            unit = unit1;
             phase_barrier();
         }
         if (!late) phase_barrier();
