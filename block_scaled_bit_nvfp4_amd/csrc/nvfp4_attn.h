@@ -27,9 +27,15 @@ constexpr float kMaxSlack = 8.0f;
 constexpr float kMaxSum = 1024.0f;      // the same on the sum of a lane's weights of a tile
 
 // How a kernel cuts the work: rows of a tile, keys of a split (a multiple of 128),
-// and how many splits at most.
-struct AttnSplit {
-    int tile_rows, keys, splits;
+// how many splits at most, how tiles are found (0: by the offsets; else so many tile
+// indexes per sequence), and its first part row in the workspace.
+struct AttnCut {
+    int rows, keys, splits, tiles_per_seq, first_row;
+};
+
+// Where a row's parts are: part row first + z * stride of each of `pieces` splits z.
+struct RowInfo {
+    int first, stride, pieces, unused;
 };
 
 struct AttnArgs {
@@ -42,16 +48,19 @@ struct AttnArgs {
     int q_heads, group;
     int window;
     float scale_log2;      // scale * log2(e)
-    AttnSplit split[2];    // narrow kernel's, wide kernel's
     int narrow_rows;       // sequences of at most so many rows (new tokens x group) are the narrow kernel's
-    float *part_o;         // [splits][tokens * q_heads][D], relative to 2^m
-    float *part_ml;        // [splits][tokens * q_heads][4]: m (base 2), l, lr, unused
+    AttnCut cut[2];        // the narrow kernel's, the wide kernel's
+    RowInfo *info;         // [tokens * q_heads]; NULL where no tile is split
+    int part_rows;
+    float *part_o;         // [part_rows][D], relative to 2^m
+    float *part_ml;        // [part_rows][4]: m (base 2), l, lr, unused
 };
 
 // One workgroup's rows: rows (token, head of the group) of one sequence, token
-// major, in tiles of TR; tile t of sequence s is work item
-// floor(offsets[s] * group / TR) + s + t, so items are found without a prefix sum
-// over the sequences (some items have no tile).
+// major, in tiles; tile t of sequence s has the index
+// floor(offsets[s] * group / rows) + s + t, so that it is found without a prefix sum
+// over the sequences (some indexes have no tile).  Where short sequences stand among
+// long ones, the narrow kernel has a few indexes for each sequence instead.
 struct RowTile {
     int s;                 // sequence
     int begin;             // its first token row
@@ -63,12 +72,9 @@ struct RowTile {
     bool some;             // whether the item has a tile
 };
 
-inline int64_t tile_items(int64_t tokens, int group, int seqs, int tile_rows) {
-    return tokens * group / tile_rows + seqs;
-}
-
-__device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int item, int tile_rows) {
+__device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int cls, int item) {
     const KvView &v = a.kv;
+    const int tile_rows = a.cut[cls].rows, each = a.cut[cls].tiles_per_seq;
     RowTile r;
     // The item's sequence is the last one whose first item is not past it; the
     // lanes load 64 sequences' facts at once, so the whole search costs one
@@ -80,7 +86,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int item, int til
         const int s = min(base + lane, v.seqs - 1);
         int begin, stop, past;
         v.sequence(s, begin, stop, past);
-        const int item0 = int(int64_t(begin) * a.group / tile_rows) + s;
+        const int item0 = each > 0 ? s * each : int(int64_t(begin) * a.group / tile_rows) + s;
         const int c = __popcll(__ballot(base + lane < v.seqs && item0 <= item));
         if (c == 0) break;
         r.s = base + c - 1;
@@ -93,7 +99,7 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int item, int til
     r.n = end - r.begin;
     r.rows = r.n * a.group;
     r.row0 = (item - first_item) * tile_rows;
-    r.some = first_item >= 0 && r.row0 < r.rows;
+    r.some = first_item >= 0 && r.row0 < r.rows && (r.rows > a.narrow_rows) == (cls == 1);
     const int first = r.some ? r.row0 / a.group : 0;
     const int last = r.some ? min(r.row0 + tile_rows, r.rows) - 1 : 0;
     const int i1 = last / a.group;
@@ -104,18 +110,24 @@ __device__ __forceinline__ RowTile row_tile(const AttnArgs &a, int item, int til
     return r;
 }
 
-// The keys of split z of a tile's range, as [lo, hi) with lo a multiple of 64 but
-// for rounding down of the range's start; the last split takes what is left.
+// The keys lo .. hi - 1 of split z of a tile, in `splits` in all: lo is a multiple of
+// 64 plus whole splits, and the last split takes what is left.  Its parts' first row in
+// the workspace, and whether there is work (split 0 has it always: rows that see
+// nothing are written too).
 struct KeyRange {
-    int lo, hi, splits;
+    int lo, hi, splits, part;
+    bool some;
 };
-__device__ __forceinline__ KeyRange key_range(const AttnSplit &s, const RowTile &r, int z) {
+__device__ __forceinline__ KeyRange key_range(const AttnArgs &a, int cls, const RowTile &r, int item, int head, int z) {
+    const AttnCut &c = a.cut[cls];
     KeyRange k;
     const int base = r.lo & ~63;
     const int all = max(r.hi - base, 0);
-    k.splits = min((all + s.keys - 1) / s.keys, s.splits);
-    k.lo = base + z * s.keys;
-    k.hi = z + 1 >= k.splits ? r.hi : k.lo + s.keys;
+    k.splits = min((all + c.keys - 1) / c.keys, c.splits);
+    k.lo = base + z * c.keys;
+    k.hi = z + 1 >= k.splits ? r.hi : k.lo + c.keys;
+    k.part = c.first_row + ((item * a.kv.heads + head) * c.splits + z) * c.rows;
+    k.some = z == 0 || z < k.splits;
     return k;
 }
 
@@ -202,8 +214,10 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 constexpr int kNarrowRows = 16;    // rows of the narrow kernel's tile
 int wide_rows(int dim);            // rows of the wide kernel's
 
-int launch_attn_narrow(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream);
-int launch_attn_wide(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream);
-int launch_attn_join(const AttnArgs &a, int dim, hipStream_t stream);
+// `tiles`: tile indexes.
+int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream);
+int launch_attn_wide(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream);
+// Joins the splits; `many`: a workgroup per row, for rows in many splits.
+int launch_attn_join(const AttnArgs &a, bool many, int dim, hipStream_t stream);
 
 }  // namespace nvfp4

@@ -14,56 +14,99 @@ constexpr int kCus = 256;
 
 // Which kernels a call needs and how each cuts its work.
 struct AttnPlan {
-    AttnSplit split[2];
+    AttnCut cut[2];
+    int64_t tiles[2];      // tile indexes; 0: the kernel is not needed
+    int64_t part_rows;     // of the workspace; 0: no tile is split
+    bool many;             // how the splits are joined
     int narrow_rows;
-    bool narrow, wide;
-    int splits() const { return std::max(split[0].splits, split[1].splits); }
 };
 
-// Splits of `keys` keys, a multiple of 128, over a context; its start is rounded
-// down to a multiple of 64.
-static AttnSplit cut_keys(int tile_rows, int64_t context, int64_t keys) {
-    keys = ceil_div(std::max<int64_t>(keys, 128), 128) * 128;
-    int64_t splits = ceil_div(context + 63, keys);
-    if (splits > kMaxSplits) {
-        keys = ceil_div(ceil_div(context + 63, kMaxSplits), 128) * 128;
-        splits = ceil_div(context + 63, keys);
-    }
-    return AttnSplit{tile_rows, int(keys), int(splits)};
+// Splits of about `keys` keys of tiles that span `span` (the range's start is rounded
+// down to a multiple of 64 where a window moves it).
+static void cut_keys(AttnCut &c, int64_t span, int64_t keys, bool window, int most_splits) {
+    if (window) span += 63;
+    keys = ceil_div(std::max(keys, ceil_div(span, most_splits)), 128) * 128;
+    c.keys = int(keys);
+    c.splits = int(ceil_div(span, keys));
 }
 
-static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads) {
-    const int group = q_heads / c->heads;
-    const int64_t most = int64_t(std::max(b->max_new, 1)) * group;
-    const int64_t context = std::max(b->max_context, 1);
-    AttnPlan p;
-    p.wide = most > kNarrowMost;
-    p.narrow = !p.wide || b->tokens < int64_t(b->seqs) * b->max_new;     // all the same length otherwise
-    p.narrow_rows = !p.wide ? INT_MAX : p.narrow ? kNarrowMost : -1;
-    p.split[0] = p.split[1] = AttnSplit{kNarrowRows, 128, 1};
-    if (p.narrow) {
-        constexpr int64_t kTarget = 768, kLeast = 256;
-        const int64_t tiles = tile_items(p.wide ? 0 : b->tokens, group, b->seqs, kNarrowRows) * c->heads;
-        p.split[0] = cut_keys(kNarrowRows, context, std::max(ceil_div(context, ceil_div(kTarget, tiles)), kLeast));
+static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads, int window) {
+    const int group = q_heads / c->heads, dim = c->head_dim;
+    // A caller asks for the workspace without saying the window: with one, no more
+    // splits than without.
+    int most_splits[2] = {kMaxSplits, kMaxSplits};
+    if (window > 0) {
+        const AttnPlan without = attn_plan(c, b, q_heads, 0);
+        for (int cls = 0; cls < 2; ++cls) most_splits[cls] = without.cut[cls].splits;
     }
-    if (p.wide) {
-        // the number of splits that takes the fewest key tiles in all, a CU
-        // taking one workgroup at a time, a split costing about 256 keys more
-        const int rows = wide_rows(c->head_dim);
-        const int64_t tiles = (ceil_div(b->tokens * group, rows) + (p.narrow ? 0 : b->seqs - 1)) * c->heads;
-        int64_t best = 0, keys = context;
+    const int64_t most = int64_t(std::max(b->max_new, 1)) * group;
+    AttnPlan p = {};
+    const bool wide = most > kNarrowMost;
+    const bool narrow = !wide || b->tokens < int64_t(b->seqs) * b->max_new;     // all the same length otherwise
+    p.narrow_rows = !wide ? INT_MAX : narrow ? kNarrowMost : -1;
+    // a tile sees its window and its own tokens
+    const auto span = [&](int rows) {
+        const int64_t context = std::max(b->max_context, 1);
+        return window > 0 ? std::min<int64_t>(context, int64_t(window) + rows / group + 1) : context;
+    };
+    p.cut[0] = AttnCut{kNarrowRows, 128, 1, 0, 0};
+    if (narrow) {
+        // Workgroups to aim at: two for each CU where one sequence is split (more
+        // cost the join more than they gain: 131008 keys 53 us, with twice as many 58),
+        // up to twelve where several sequences of unknown lengths balance each
+        // other (64 ragged sequences: 92 us at three for each CU, 86 at twelve).
+        p.cut[0].tiles_per_seq = wide ? kNarrowMost / kNarrowRows : 0;
+        p.tiles[0] = wide ? int64_t(b->seqs) * p.cut[0].tiles_per_seq : b->tokens * group / kNarrowRows + b->seqs;
+        const int64_t target = 2 * kCus * std::min(b->seqs, 6);
+        const int64_t keys = span(kNarrowRows);
+        cut_keys(p.cut[0], keys, std::max<int64_t>(ceil_div(keys, ceil_div(target, p.tiles[0] * c->heads)), 256), window > 0, most_splits[0]);
+    }
+    p.cut[1] = AttnCut{wide_rows(dim), 128, 1, 0, 0};
+    if (wide) {
+        // The number of splits that should take the least time, a CU taking one
+        // workgroup at a time: about 1.8 us for each tile of 8192 / dim keys
+        // (2.5 at 64), 5 us for a workgroup's start and end, and for split tiles
+        // the parts' way out and back at 4 TB/s and the join's launch.
+        const int rows = p.cut[1].rows;
+        p.tiles[1] = b->tokens * group / rows + b->seqs;
+        const int64_t keys = span(rows), tiles = ceil_div(b->tokens * group, rows) * c->heads;
+        double best = 0;
+        int64_t each = keys;
         for (int n = 1; n <= 16; ++n) {
-            const int64_t each = ceil_div(context, n);
-            if (n > 1 && each < 256) break;
-            const int64_t cost = ceil_div(tiles * n, kCus) * (each + 256);
+            const int64_t of = ceil_div(ceil_div(keys, n), 128) * 128;
+            if (n > 1 && of < 32768 / dim) break;
+            const double parts = n == 1 ? 0 : 4 + double(b->tokens) * q_heads * dim * 4 * 2 * n / 4e6;
+            const double cost = double(ceil_div(tiles * n, kCus)) * (double(of) * dim / 8192 * (dim == 64 ? 2.5 : 1.8) + 5) + parts;
             if (n == 1 || cost < best) {
                 best = cost;
-                keys = each;
+                each = of;
             }
         }
-        p.split[1] = cut_keys(rows, context, keys + 63);
+        cut_keys(p.cut[1], keys, each, window > 0, most_splits[1]);
     }
+    int64_t rows = 0;
+    for (int cls = 0; cls < 2; ++cls) {
+        AttnCut &k = p.cut[cls];
+        k.first_row = int(rows);
+        if (p.tiles[cls] == 0 || k.splits == 1) continue;
+        const int64_t more = p.tiles[cls] * c->heads * k.splits * k.rows;
+        if (rows + more > INT_MAX) {           // part rows are 32-bit: whole tiles then
+            k.splits = 1;
+            continue;
+        }
+        rows += more;
+    }
+    p.part_rows = rows;
+    p.many = !wide && p.cut[0].splits > 12;    // among many rows few are in many splits
     return p;
+}
+
+// Bytes of the workspace: the rows' facts, and the parts.
+static size_t info_bytes(const nvfp4_kv_batch *b, int q_heads) {
+    return size_t(b->tokens) * q_heads * sizeof(RowInfo);
+}
+static size_t plan_bytes(const AttnPlan &p, const nvfp4_kv_batch *b, int q_heads, int dim) {
+    return p.part_rows == 0 ? 0 : info_bytes(b, q_heads) + size_t(p.part_rows) * (dim + 4) * sizeof(float);
 }
 
 static int attn_check(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads, KvView &v) {
@@ -71,10 +114,6 @@ static int attn_check(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_he
     if (q_heads < 1 || q_heads % c->heads != 0) return NVFP4_ESHAPE;
     if (b->tokens > (int64_t(1) << 30) / q_heads) return NVFP4_ESHAPE;
     return NVFP4_OK;
-}
-
-static size_t attn_bytes(const AttnPlan &p, int64_t tokens, int q_heads, int dim) {
-    return p.splits() <= 1 ? 0 : size_t(p.splits()) * size_t(tokens) * q_heads * (dim + 4) * sizeof(float);
 }
 
 }  // namespace nvfp4
@@ -85,7 +124,7 @@ NVFP4_API size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_cache *cache,
                                                     int q_heads) {
     KvView v;
     if (attn_check(cache, batch, q_heads, v) != NVFP4_OK) return 0;
-    return attn_bytes(attn_plan(cache, batch, q_heads), batch->tokens, q_heads, cache->head_dim);
+    return plan_bytes(attn_plan(cache, batch, q_heads, 0), batch, q_heads, cache->head_dim);
 }
 
 NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, const uint16_t *q,
@@ -103,8 +142,8 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
         (tree && !aligned(tree, 8)))
         return NVFP4_EALIGN;
     if (batch->tokens == 0) return NVFP4_OK;
-    const AttnPlan plan = attn_plan(cache, batch, q_heads);
-    const size_t need = attn_bytes(plan, batch->tokens, q_heads, cache->head_dim);
+    const AttnPlan plan = attn_plan(cache, batch, q_heads, window);
+    const size_t need = plan_bytes(plan, batch, q_heads, cache->head_dim);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return NVFP4_EWORKSPACE;
         if (!aligned(workspace, 16)) return NVFP4_EALIGN;
@@ -119,15 +158,18 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
     a.group = q_heads / cache->heads;
     a.window = window;
     a.scale_log2 = scale * kLog2e;
-    a.split[0] = plan.split[0];
-    a.split[1] = plan.split[1];
     a.narrow_rows = plan.narrow_rows;
-    a.part_o = static_cast<float *>(workspace);
-    a.part_ml = a.part_o + size_t(plan.splits()) * batch->tokens * wide;
+    a.cut[0] = plan.cut[0];
+    a.cut[1] = plan.cut[1];
     const int dim = cache->head_dim;
-    if (plan.narrow)
-        if (int st = launch_attn_narrow(a, dim, cache->k_format, cache->v_format, stream)) return st;
-    if (plan.wide)
-        if (int st = launch_attn_wide(a, dim, cache->k_format, cache->v_format, stream)) return st;
-    return plan.splits() > 1 ? launch_attn_join(a, dim, stream) : NVFP4_OK;
+    const bool cut = plan.part_rows > 0;
+    a.part_rows = int(plan.part_rows);
+    a.info = cut ? static_cast<RowInfo *>(workspace) : nullptr;
+    a.part_o = cut ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + info_bytes(batch, q_heads)) : nullptr;
+    a.part_ml = cut ? a.part_o + size_t(plan.part_rows) * dim : nullptr;
+    if (plan.tiles[0] > 0)
+        if (int st = launch_attn_narrow(a, plan.tiles[0], dim, cache->k_format, cache->v_format, stream)) return st;
+    if (plan.tiles[1] > 0)
+        if (int st = launch_attn_wide(a, plan.tiles[1], dim, cache->k_format, cache->v_format, stream)) return st;
+    return cut ? launch_attn_join(a, plan.many, dim, stream) : NVFP4_OK;
 }

@@ -56,25 +56,22 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
     constexpr int kRowDims = D / 16;           // elements of a value row
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const RowTile tile = row_tile(a, blockIdx.x, kNarrowRows);
-    if (!tile.some || tile.rows > a.narrow_rows) return;
     const int head = blockIdx.y, z = blockIdx.z;
-    const KeyRange keys = key_range(a.split[0], tile, z);
-    if (z > 0 && z >= keys.splits) return;
+    const RowTile tile = row_tile(a, 0, blockIdx.x);
+    if (!tile.some) return;
+    const KeyRange keys = key_range(a, 0, tile, blockIdx.x, head, z);
+    if (!keys.some) return;
 
     // The row of this lane's column, and its query operands.
     bf16x8 q[kSlices];
-    int token, qhead, klo, khi;
-    unsigned long long tree;
     const int row = tile.row0 + c;
     const bool in = row < tile.rows;
     const int i = in ? row / a.group : 0;
-    token = in ? tile.begin + i : -1;
-    qhead = head * a.group + (in ? row - i * a.group : 0);
+    const int token = in ? tile.begin + i : -1, qhead = head * a.group + (in ? row - i * a.group : 0);
     const int pos = tile.past + i;
-    klo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
-    khi = in ? (a.tree ? tile.past : pos + 1) : 0;
-    tree = in && a.tree ? a.tree[token] : 0ull;
+    const int klo = a.window > 0 ? max(0, pos + 1 - a.window) : 0;
+    const int khi = in ? (a.tree ? tile.past : pos + 1) : 0;
+    const unsigned long long tree = in && a.tree ? a.tree[token] : 0ull;
     const uint16_t *src = a.q + max(token, 0) * a.q_stride + qhead * D;
 #pragma unroll
     for (int m = 0; m < kSlices; ++m) {
@@ -86,9 +83,12 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
         q[m] = __builtin_bit_cast(bf16x8, w);
     }
 
+    if (a.info && z == 0 && threadIdx.x < kNarrowRows && in)
+        a.info[int64_t(token) * a.q_heads + qhead] = RowInfo{keys.part + c, kNarrowRows, keys.splits, 0};
+
     floatx4 o[kRowDims];
-    float mx, sub, l, lr;     // lr: the sum of the weights as rounded, which normalises the outputs
-    mx = kNegInf; sub = 0.0f; l = 0.0f; lr = 0.0f;
+    // lr: the sum of the weights as rounded, which normalises the outputs
+    float mx = kNegInf, sub = 0.0f, l = 0.0f, lr = 0.0f;
 #pragma unroll
     for (int j = 0; j < kRowDims; ++j) o[j] = floatx4{0, 0, 0, 0};
 
@@ -282,11 +282,12 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
             const int64_t at = int64_t(tile.begin + i) * a.q_heads + head * a.group + (row - i * a.group);
             const int d = piece * kRowDims + part * kPart;
             if (keys.splits > 1) {
-                float *dst = a.part_o + (int64_t(z) * a.kv.tokens * a.q_heads + at) * D + d;
+                const int64_t to = keys.part + row16;
+                float *dst = a.part_o + to * D + d;
 #pragma unroll
                 for (int j = 0; j < kEach; ++j) dst[j] = y[j];
                 if (piece == 0 && part == 0) {
-                    float *ml = a.part_ml + (int64_t(z) * a.kv.tokens * a.q_heads + at) * 4;
+                    float *ml = a.part_ml + to * 4;
                     *reinterpret_cast<float4 *>(ml) = float4{mm, ll, rr, 0.0f};
                 }
             } else {
@@ -304,100 +305,111 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
 
 // --------------------------------------------------------------------- join
 
-// The splits that a row's keys were in (a row's tile decides them), or 0 where
-// the row is no sequence's.
-__device__ __forceinline__ int row_splits(const AttnArgs &a, int token, int qhead, int s) {
-    const KvView &v = a.kv;
-    int begin, end, past;
-    v.sequence(s, begin, end, past);
-    if (token < begin || token >= end) return 0;
-    const int row = (token - begin) * a.group + qhead % a.group;
-    const int n = end - begin;
-    const AttnSplit &split = a.split[n * a.group > a.narrow_rows];
-    const int first = row / split.tile_rows * split.tile_rows;
-    const int i0 = first / a.group, i1 = (min(first + split.tile_rows, n * a.group) - 1) / a.group;
-    RowTile r;
-    r.lo = a.window > 0 ? max(0, past + i0 + 1 - a.window) : 0;
-    r.hi = min(a.tree ? past + n : past + i1 + 1, v.capacity);
-    return key_range(split, r, 0).splits;
+constexpr int kMaxPieces = kMaxSplits;
+
+// Where row u = token * q_heads + head has its parts; no pieces, or one that wrote the
+// output itself, is nothing to join.  Rows of no sequence have no facts; and facts that
+// point outside the workspace, as arrays that change under the call may leave them,
+// are none.
+__device__ __forceinline__ RowInfo row_info(const AttnArgs &a, int64_t u) {
+    RowInfo r = a.info[u];
+    const int token = int(u / a.q_heads);
+    if (token < a.kv.offsets[0] || token >= a.kv.offsets[a.kv.seqs] || r.pieces > kMaxPieces || r.first < 0 ||
+        (r.stride != kNarrowRows && r.stride != a.cut[1].rows) ||
+        r.first + int64_t(r.pieces - 1) * r.stride >= a.part_rows)
+        r.pieces = 0;
+    return r;
 }
 
-__device__ __forceinline__ float split_weight(float mz, float m) {
+__device__ __forceinline__ float piece_weight(float mz, float m) {
     return mz == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mz - m);
 }
 
-__device__ __forceinline__ void store_row4(const AttnArgs &a, int D, int token, int qhead, int d, float m, float l,
-                                           float lr, const float4 &y) {
+__device__ __forceinline__ void store_row4(const AttnArgs &a, int D, int64_t u, int d, float m, float l, float lr,
+                                           const float4 &y) {
+    const int token = int(u / a.q_heads), qhead = int(u - int64_t(token) * a.q_heads);
     const float inv = m == kNegInf && l == 0.0f ? 0.0f : 1.0f / lr;
     uint16_t *dst = a.out + token * a.out_stride + qhead * D + d;
     *reinterpret_cast<u32x2 *>(dst) = u32x2{pack_bf16(y.x * inv, y.y * inv), pack_bf16(y.z * inv, y.w * inv)};
-    if (a.lse && d == 0) a.lse[int64_t(token) * a.q_heads + qhead] = lse_of(m, l);
+    if (a.lse && d == 0) a.lse[u] = lse_of(m, l);
 }
 
-// At most kFewSplits splits: a thread takes four elements of a row and all its
-// splits, whose loads go out together.
-constexpr int kFewSplits = 8;
+// For few pieces: a thread takes four elements of a row and eight pieces at a time,
+// whose loads go out together.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_few_kernel(AttnArgs a) {
-    constexpr int kThreads = D / 4;            // of one row
+    constexpr int kThreads = D / 4, kAtOnce = 8;
     const int64_t u = int64_t(blockIdx.x) * 256 + threadIdx.x;
-    const int64_t rows = int64_t(a.kv.tokens) * a.q_heads;
-    const int64_t at = min(u / kThreads, rows - 1);
+    const int64_t row = u / kThreads;
+    if (row >= int64_t(a.kv.tokens) * a.q_heads) return;
     const int d = int(u % kThreads) * 4;
-    const int token = int(at / a.q_heads), qhead = int(at - int64_t(token) * a.q_heads);
-    const int t0 = __builtin_amdgcn_readfirstlane(token);
-    int s = max(wave_count_le(a.kv.seqs, t0, [&](int i) { return a.kv.offsets[i]; }) - 1, 0);
-    while (s + 1 < a.kv.seqs && a.kv.offsets[s + 1] <= token) ++s;
-    const int splits = u < rows * kThreads ? row_splits(a, token, qhead, s) : 0;
-    if (splits <= 1) return;
-    float4 part[kFewSplits], o[kFewSplits];
-#pragma unroll
-    for (int z = 0; z < kFewSplits; ++z) {
-        const int64_t from = int64_t(min(z, splits - 1)) * rows + at;
-        part[z] = *reinterpret_cast<const float4 *>(a.part_ml + from * 4);
-        o[z] = *reinterpret_cast<const float4 *>(a.part_o + from * D + d);
-    }
-    float m = kNegInf;
-#pragma unroll
-    for (int z = 0; z < kFewSplits; ++z) m = fmaxf(m, part[z].x);
-    float l = 0.0f, lr = 0.0f;
+    const RowInfo r = row_info(a, row);
+    if (r.pieces <= 1) return;
+    float m = kNegInf, l = 0.0f, lr = 0.0f;
     float4 y = {0, 0, 0, 0};
+    for (int first = 0; first < r.pieces; first += kAtOnce) {
+        float4 part[kAtOnce], o[kAtOnce];
 #pragma unroll
-    for (int z = 0; z < kFewSplits; ++z) {
-        if (z >= splits) break;
-        const float by = split_weight(part[z].x, m);
-        l += part[z].y * by;
-        lr += part[z].z * by;
-        y.x += o[z].x * by; y.y += o[z].y * by; y.z += o[z].z * by; y.w += o[z].w * by;
+        for (int z = 0; z < kAtOnce; ++z) {
+            const int64_t from = r.first + int64_t(min(first + z, r.pieces - 1)) * r.stride;
+            part[z] = *reinterpret_cast<const float4 *>(a.part_ml + from * 4);
+            o[z] = *reinterpret_cast<const float4 *>(a.part_o + from * D + d);
+        }
+        float top = m;
+#pragma unroll
+        for (int z = 0; z < kAtOnce; ++z) top = fmaxf(top, part[z].x);
+        const float old = piece_weight(m, top);
+        m = top;
+        l *= old;
+        lr *= old;
+        y.x *= old; y.y *= old; y.z *= old; y.w *= old;
+#pragma unroll
+        for (int z = 0; z < kAtOnce; ++z) {
+            if (first + z >= r.pieces) break;
+            const float by = piece_weight(part[z].x, m);
+            l += part[z].y * by;
+            lr += part[z].z * by;
+            y.x += o[z].x * by; y.y += o[z].y * by; y.z += o[z].z * by; y.w += o[z].w * by;
+        }
     }
-    store_row4(a, D, token, qhead, d, m, l, lr, y);
+    store_row4(a, D, row, d, m, l, lr, y);
 }
 
-// A workgroup of 256 threads takes one row: thread z weighs split z, then groups
-// of D / 4 threads sum every kGroups-th split and meet in shared memory.
+// For many: a workgroup of 256 threads takes one row.  The threads weigh the
+// pieces, then groups of D / 4 sum every kGroups-th and meet in shared memory.
 template <int D>
 __global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a) {
     constexpr int kThreads = D / 4, kGroups = 256 / kThreads;
     __shared__ float4 red[4];
-    __shared__ float weight[kMaxSplits];
+    __shared__ float weight[kMaxPieces];
     __shared__ float4 sum[kGroups][kThreads];
-    const int64_t rows = int64_t(a.kv.tokens) * a.q_heads, at = blockIdx.x;
-    const int token = int(at / a.q_heads), qhead = int(at - int64_t(token) * a.q_heads);
-    const int s = max(wave_count_le(a.kv.seqs, token, [&](int i) { return a.kv.offsets[i]; }) - 1, 0);
-    const int splits = row_splits(a, token, qhead, s);
-    if (splits <= 1) return;
+    const RowInfo r = row_info(a, blockIdx.x);
+    if (r.pieces <= 1) return;
     const int tid = threadIdx.x, wave = tid >> 6;
-    float4 part = {kNegInf, 0, 0, 0};
-    if (tid < splits) part = *reinterpret_cast<const float4 *>(a.part_ml + (int64_t(tid) * rows + at) * 4);
-    float m = part.x;
+    constexpr int kEach = kMaxPieces / 256;
+    float4 part[kEach];
+    float m = kNegInf;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int z = tid + 256 * k;
+        part[k] = float4{kNegInf, 0, 0, 0};
+        if (z < r.pieces) part[k] = *reinterpret_cast<const float4 *>(a.part_ml + (r.first + int64_t(z) * r.stride) * 4);
+        m = fmaxf(m, part[k].x);
+    }
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) m = fmaxf(m, __shfl_xor(m, k));
     if ((tid & 63) == 0) red[wave].x = m;
     __syncthreads();
     m = fmaxf(fmaxf(red[0].x, red[1].x), fmaxf(red[2].x, red[3].x));
-    const float by = tid < splits ? split_weight(part.x, m) : 0.0f;
-    weight[tid] = by;
-    float l = tid < splits ? part.y * by : 0.0f, lr = tid < splits ? part.z * by : 0.0f;
+    float l = 0.0f, lr = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kEach; ++k) {
+        const int z = tid + 256 * k;
+        const float by = z < r.pieces ? piece_weight(part[k].x, m) : 0.0f;
+        weight[z] = by;
+        l += part[k].y * by;
+        lr += part[k].z * by;
+    }
 #pragma unroll
     for (int k = 1; k < 64; k *= 2) {
         l += __shfl_xor(l, k);
@@ -413,8 +425,8 @@ __global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a) {
     const int grp = tid / kThreads, d = tid % kThreads * 4;
     float4 y = {0, 0, 0, 0};
 #pragma unroll 8
-    for (int z = grp; z < splits; z += kGroups) {
-        const float4 o = *reinterpret_cast<const float4 *>(a.part_o + (int64_t(z) * rows + at) * D + d);
+    for (int z = grp; z < r.pieces; z += kGroups) {
+        const float4 o = *reinterpret_cast<const float4 *>(a.part_o + (r.first + int64_t(z) * r.stride) * D + d);
         const float w = weight[z];
         y.x += o.x * w; y.y += o.y * w; y.z += o.z * w; y.w += o.w * w;
     }
@@ -426,31 +438,28 @@ __global__ void __launch_bounds__(256) attn_join_many_kernel(AttnArgs a) {
         const float4 o = sum[k][tid];
         y.x += o.x; y.y += o.y; y.z += o.z; y.w += o.w;
     }
-    store_row4(a, D, token, qhead, d, m, l, lr, y);
+    store_row4(a, D, blockIdx.x, d, m, l, lr, y);
 }
 
-int launch_attn_join(const AttnArgs &a, int dim, hipStream_t stream) {
+int launch_attn_join(const AttnArgs &a, bool many, int dim, hipStream_t stream) {
     return kv_dim(dim, [&](auto tag) {
         constexpr int D = decltype(tag)::value;
-        const int64_t rows = int64_t(a.kv.tokens) * a.q_heads;
-        const bool few = max(a.split[0].splits, a.split[1].splits) <= kFewSplits;
-        const int64_t grid = few ? ceil_div(rows * (D / 4), 256) : rows;
+        const int64_t rows = int64_t(a.kv.tokens) * a.q_heads, grid = many ? rows : ceil_div(rows * (D / 4), 256);
         if (grid >= kMaxGrid / 256) return NVFP4_ESHAPE;
-        if (few) attn_join_few_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a);
-        else attn_join_many_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a);
+        if (many) attn_join_many_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a);
+        else attn_join_few_kernel<D><<<unsigned(grid), 256, 0, stream>>>(a);
         return launch_status();
     });
 }
 
-int launch_attn_narrow(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream) {
+int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream) {
     return kv_dim(dim, [&](auto d) {
         return kv_bits(k_format, [&](auto k) {
             return kv_bits(v_format, [&](auto v) {
                 constexpr int D = decltype(d)::value, K = decltype(k)::value, V = decltype(v)::value;
                 constexpr int kThreads = kNarrowWaves * kLanes;
-                const int64_t items = tile_items(a.kv.tokens, a.group, a.kv.seqs, kNarrowRows);
-                if (items >= kMaxGrid / kThreads) return NVFP4_ESHAPE;
-                attn_narrow_kernel<D, K, V><<<dim3(unsigned(items), unsigned(a.kv.heads), unsigned(a.split[0].splits)),
+                if (tiles >= kMaxGrid / kThreads) return NVFP4_ESHAPE;
+                attn_narrow_kernel<D, K, V><<<dim3(unsigned(tiles), unsigned(a.kv.heads), unsigned(a.cut[0].splits)),
                                               kThreads, 0, stream>>>(a);
                 return launch_status();
             });

@@ -211,11 +211,11 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
     // heads first: the tiles of a head, which read the same keys, meet in few
     // XCDs' caches; a sequence's last tiles, which have the most keys, go first
     const int item = int(gridDim.x / a.kv.heads) - 1 - int(blockIdx.x / a.kv.heads);
-    const RowTile tile = row_tile(a, item, W::kRows);
-    if (!tile.some || a.narrow_rows >= tile.rows) return;
     const int head = blockIdx.x % a.kv.heads, z = blockIdx.y;
-    const KeyRange keys = key_range(a.split[1], tile, z);
-    if (z > 0 && z >= keys.splits) return;
+    const RowTile tile = row_tile(a, 1, item);
+    if (!tile.some) return;
+    const KeyRange keys = key_range(a, 1, tile, item, head, z);
+    if (!keys.some) return;
 
     // Waves w and w + 4 share a SIMD and are in opposite phases; at D = 256 waves
     // 2 k and 2 k + 1 share rows.
@@ -238,6 +238,8 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
             q[m] = __builtin_bit_cast(bf16x8, w);
         }
     }
+    if (a.info && z == 0 && in && h == 0 && half == 0)
+        a.info[int64_t(token) * a.q_heads + qhead] = RowInfo{keys.part + (row - tile.row0), W::kRows, keys.splits, 0};
     floatx16 o[kDims], s[W::kBlocks32];
     uint32_t p[W::kBlocks32][8];
     unsigned long long seen = 0;           // in an edge tile, bit 16 b + e where score e of block b is allowed
@@ -499,14 +501,14 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
     }
     l += __shfl_xor(l, 32);
     const float norm = lr[0] + __shfl_xor(lr[0], 32);
-    if (!in) return;
-    const int64_t at = int64_t(token) * a.q_heads + qhead;
     // lane (h, row) holds value rows r = 8 x + 4 h + y, each D / 16 elements in
     // a row: element 2 d + jj of it in accumulator d's 8 jj + 4 x + y
     constexpr int kRowDims = D / 16;
     const int first = half * kDims * 2;          // of the row's elements that are this wave's
-    if (keys.splits > 1) {
-        float *dst = a.part_o + (int64_t(z) * a.kv.tokens * a.q_heads + at) * D + first;
+    const bool facts = h == 0 && half == 0;
+    if (in && keys.splits > 1) {
+        const int64_t to = keys.part + (row - tile.row0);
+        float *dst = a.part_o + to * D + first;
 #pragma unroll
         for (int x = 0; x < 2; ++x)
 #pragma unroll
@@ -517,23 +519,22 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
                     *reinterpret_cast<float4 *>(dst + (8 * x + 4 * h + y) * kRowDims + 2 * d) =
                         float4{o[d][e], o[d][8 + e], o[d + 1][e], o[d + 1][8 + e]};
                 }
-        if (h == 0 && half == 0)
-            *reinterpret_cast<float4 *>(a.part_ml + (int64_t(z) * a.kv.tokens * a.q_heads + at) * 4) = float4{sub, l, norm, 0.0f};
-        return;
+        if (facts) *reinterpret_cast<float4 *>(a.part_ml + to * 4) = float4{sub, l, norm, 0.0f};
+    } else if (in) {
+        const float inv = sub == kNegInf && l == 0.0f ? 0.0f : 1.0f / norm;
+        uint16_t *dst = a.out + token * a.out_stride + qhead * D + first;
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+#pragma unroll
+                for (int d = 0; d < kDims; d += 2) {
+                    const int e = 4 * x + y;
+                    *reinterpret_cast<u32x2 *>(dst + (8 * x + 4 * h + y) * kRowDims + 2 * d) =
+                        u32x2{pack_bf16(o[d][e] * inv, o[d][8 + e] * inv), pack_bf16(o[d + 1][e] * inv, o[d + 1][8 + e] * inv)};
+                }
+        if (a.lse && facts) a.lse[int64_t(token) * a.q_heads + qhead] = lse_of(sub, l);
     }
-    const float inv = sub == kNegInf && l == 0.0f ? 0.0f : 1.0f / norm;
-    uint16_t *dst = a.out + token * a.out_stride + qhead * D + first;
-#pragma unroll
-    for (int x = 0; x < 2; ++x)
-#pragma unroll
-        for (int y = 0; y < 4; ++y)
-#pragma unroll
-            for (int d = 0; d < kDims; d += 2) {
-                const int e = 4 * x + y;
-                *reinterpret_cast<u32x2 *>(dst + (8 * x + 4 * h + y) * kRowDims + 2 * d) =
-                    u32x2{pack_bf16(o[d][e] * inv, o[d][8 + e] * inv), pack_bf16(o[d + 1][e] * inv, o[d + 1][8 + e] * inv)};
-            }
-    if (a.lse && h == 0 && half == 0) a.lse[at] = lse_of(sub, l);
 }
 
 // The kernels' shared memory passes the default limit; it is raised once per
@@ -554,16 +555,16 @@ static bool wide_lds_ok() {
 
 int wide_rows(int dim) { return kv_dim(dim, [](auto d) { return WideShape<decltype(d)::value>::kRows; }); }
 
-int launch_attn_wide(const AttnArgs &a, int dim, int k_format, int v_format, hipStream_t stream) {
+int launch_attn_wide(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream) {
     return kv_dim(dim, [&](auto d) {
         return kv_bits(k_format, [&](auto k) {
             return kv_bits(v_format, [&](auto v) {
                 constexpr int D = decltype(d)::value, K = decltype(k)::value, V = decltype(v)::value;
                 typedef WideShape<D> W;
-                const int64_t groups = tile_items(a.kv.tokens, a.group, a.kv.seqs, W::kRows) * a.kv.heads;
+                const int64_t groups = tiles * a.kv.heads;
                 if (groups >= kMaxGrid / W::kThreads) return NVFP4_ESHAPE;
                 if (!wide_lds_ok<D, K, V>()) return NVFP4_EHIP;
-                attn_wide_kernel<D, K, V><<<dim3(unsigned(groups), unsigned(a.split[1].splits)), W::kThreads, W::kLds,
+                attn_wide_kernel<D, K, V><<<dim3(unsigned(groups), unsigned(a.cut[1].splits)), W::kThreads, W::kLds,
                                             stream>>>(a);
                 return launch_status();
             });

@@ -104,12 +104,13 @@ def test_nothing_to_do_is_no_error(lib):
     assert attention(lib, cache(), batch(tokens=0)) == OK
 
 
-def test_workspace_covers_its_use(lib):
+def test_workspace_grows_with_the_batch_and_not_past_need(lib):
     size = lambda **kw: lib.nvfp4_kv_attention_workspace_bytes(ctypes.byref(cache()), ctypes.byref(batch(**kw)), 8)
-    assert size(max_context=1) == 0
-    need = size(max_context=100000, table_width=2000)
-    assert need > 0 and need % (6 * 8 * (128 + 4) * 4) == 0          # whole splits of every row
-    assert need // (6 * 8 * (128 + 4) * 4) <= 256
+    long = dict(max_context=100000, table_width=2000)
+    assert size(max_context=1) == 0                                  # whole tiles, nothing to join
+    assert size(**long) > 0
+    assert size(tokens=600, max_new=300, **long) > size(**long)
+    assert size(tokens=6, max_new=300, **long) > size(**long)        # both kernels' parts
 
 
 def test_binding_refuses_before_the_library():
