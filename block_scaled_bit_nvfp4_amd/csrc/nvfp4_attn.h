@@ -11,20 +11,22 @@
 // match, and the cache's value layout with it).
 #pragma once
 
+#include <mutex>
+
 #include "nvfp4_kv.h"
 
 namespace nvfp4 {
 
 constexpr int kMaxSplits = 256;     // splits of the key axis (the join's threads)
+constexpr int kNarrowRows = 16;     // rows of the narrow kernel's tile
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNegInf = -__builtin_inff();
 
-// A running maximum is moved only when a score passes it by more than this (in
-// powers of two): the weights then reach 2^8 at most, far inside fp32 and with
-// bf16's relative rounding unchanged, and most tiles rescale nothing.
-constexpr float kMaxSlack = 8.0f;
-constexpr float kMaxSum = 1024.0f;      // the same on the sum of a lane's weights of a tile
+// The weights' reference is moved only when a lane's weights of a tile sum to more
+// than this: they stay far inside fp32 with bf16's relative rounding unchanged, and
+// most tiles neither look for their maximum nor rescale.
+constexpr float kMaxSum = 1024.0f;
 
 // How a kernel cuts the work: rows of a tile, keys of a split (a multiple of 128),
 // how many splits at most, how tiles are found (0: by the offsets; else so many tile
@@ -188,9 +190,26 @@ __device__ __forceinline__ uint32_t value_pair(const uint32_t *w, int i, int jp,
     }
 }
 
+// Clears token i's codes of a lane's quad.
+template <int D, int BITS>
+__device__ __forceinline__ void clear_token(uint32_t *w, int i) {
+    constexpr int kBits = D / 16 * BITS;             // of a token
+#pragma unroll
+    for (int k = 0; k < 4 * kBits / 32; ++k) {
+        const int from = i * kBits - 32 * k, to = from + kBits;
+        if (to <= 0 || from >= 32) continue;
+        w[k] &= ~((to >= 32 ? ~0u : (1u << to) - 1u) & (from <= 0 ? ~0u : ~0u << from));
+    }
+}
+
 // Low and high halves of a pair of words side by side.
 __device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x05040100u); }
 __device__ __forceinline__ uint32_t high_halves(uint32_t a, uint32_t b) { return __builtin_amdgcn_perm(b, a, 0x07060302u); }
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+
+// s_waitcnt operands: for all loads from memory, for all of shared memory's.
+constexpr int kWaitLoads = 0x0F70, kWaitLds = 0xC07F;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 
@@ -201,9 +220,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {
     return as_u32(v);
 }
 
-// sum + the two halves of a packed bf16 pair.
-__device__ __forceinline__ float add_pair(uint32_t pair, float sum) {
-    return __builtin_amdgcn_fdot2_f32_bf16(as_bf16x2(pair), as_bf16x2(0x3F803F80u), sum, false);
+__device__ __forceinline__ float piece_weight(float mz, float m) {
+    return mz == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mz - m);
 }
 
 // log(sum of exponentials) from a base-2 maximum and the sum relative to it.
@@ -211,11 +229,25 @@ __device__ __forceinline__ float lse_of(float m, float l) {
     return m == kNegInf && l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
-constexpr int kNarrowRows = 16;    // rows of the narrow kernel's tile
-int wide_rows(int dim);            // rows of the wide kernel's
+int wide_rows(int dim);            // rows of the wide kernel's tile
+
+// Raises a kernel's limit of dynamic shared memory, once per device.
+template <auto KERNEL>
+bool raise_lds(int bytes) {
+    constexpr int kDevices = 64;
+    static std::once_flag once[kDevices];
+    static bool ok[kDevices];
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices) return false;
+    std::call_once(once[dev], [&] {
+        ok[dev] = hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                                      bytes) == hipSuccess;
+    });
+    return ok[dev];
+}
 
 // `tiles`: tile indexes.
-int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream);
+int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int waves, int dim, int k_format, int v_format, hipStream_t stream);
 int launch_attn_wide(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream);
 // Joins the splits; `many`: a workgroup per row, for rows in many splits.
 int launch_attn_join(const AttnArgs &a, bool many, int dim, hipStream_t stream);

@@ -18,6 +18,7 @@ struct AttnPlan {
     int64_t tiles[2];      // tile indexes; 0: the kernel is not needed
     int64_t part_rows;     // of the workspace; 0: no tile is split
     bool many;             // how the splits are joined
+    int waves;             // of the narrow kernel's workgroups
     int narrow_rows;
 };
 
@@ -50,6 +51,7 @@ static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int 
         return window > 0 ? std::min<int64_t>(context, int64_t(window) + rows / group + 1) : context;
     };
     p.cut[0] = AttnCut{kNarrowRows, 128, 1, 0, 0};
+    p.waves = 4;
     if (narrow) {
         // Workgroups to aim at: two for each CU where one sequence is split (more
         // cost the join more than they gain: 131008 keys 53 us, with twice as many 58),
@@ -168,7 +170,7 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
     a.part_o = cut ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + info_bytes(batch, q_heads)) : nullptr;
     a.part_ml = cut ? a.part_o + size_t(plan.part_rows) * dim : nullptr;
     if (plan.tiles[0] > 0)
-        if (int st = launch_attn_narrow(a, plan.tiles[0], dim, cache->k_format, cache->v_format, stream)) return st;
+        if (int st = launch_attn_narrow(a, plan.tiles[0], plan.waves, dim, cache->k_format, cache->v_format, stream)) return st;
     if (plan.tiles[1] > 0)
         if (int st = launch_attn_wide(a, plan.tiles[1], dim, cache->k_format, cache->v_format, stream)) return st;
     return cut ? launch_attn_join(a, plan.many, dim, stream) : NVFP4_OK;

@@ -1,59 +1,96 @@
 // nvfp4_attn_narrow.hip -- attention of few query rows over the paged cache
-// (decode, speculative verify) on gfx950.
+// (decode, speculative verify) on gfx950, and the join of split rows.
+//
+// A workgroup owns 16 rows and a range of keys; its waves take 32-key tiles in turn,
+// each with its own softmax state, and meet at the end.  The work is bound by the
+// cache's bytes, so the codes of a wave's next tile go to shared memory by
+// direct loads while it works on one: they take no registers, and three workgroups
+// of a CU keep 100 KB in flight.  A tile's codes are then read once, decoded in
+// registers straight to operands of v_mfma_f32_16x16x32_bf16.
 #include "nvfp4_attn.h"
 
 namespace nvfp4 {
 
-constexpr int kNarrowWaves = 4;
 constexpr int kTileKeys = 32;      // keys of a wave's tile: two units
 
-// The table's entries of a tile's two units, wave-uniform; made pages when the tile
-// is loaded, so that nothing waits for them before.
-struct TileEntries {
-    int entry[2];
-    __device__ __forceinline__ void load(const KvView &kv, int s, int key) {
-#pragma unroll
-        for (int u = 0; u < 2; ++u) entry[u] = kv.entry_at(s, key + u * kKvUnit);
-    }
+template <int D, int KB, int VB, int WAVES>
+struct NarrowShape {
+    typedef KvSide<D, KB> KS;
+    typedef KvSide<D, VB> VS;
+    static constexpr int kThreads = WAVES * kLanes;
+    static constexpr int kPerSimd = D == 256 ? 1 : WAVES == 8 ? 2 : D == 128 ? 3 : 4;   // waves, by registers
+    static constexpr int kKeyBytes = 2 * KS::kUnitCodes, kTileBytes = kKeyBytes + 2 * VS::kUnitCodes;
+    // the waves' outputs meet in parts of at most 8 elements of each value row
+    static constexpr int kRowDims = D / 16, kPart = kRowDims < 8 ? kRowDims : 8;
+    static constexpr int kCols = 16 * kPart + 4;       // floats of one row's part, padded against bank conflicts
+    static constexpr int kMeet = WAVES * kNarrowRows * kCols * 4;
+    static constexpr int kStatesAt = WAVES * kTileBytes > kMeet ? WAVES * kTileBytes : kMeet;
+    static constexpr int kLds = kStatesAt + 3 * WAVES * kNarrowRows * 4;
 };
 
-// The operands of one 32-key tile as loaded.
+typedef __attribute__((address_space(1))) const void GlobalBytes;
+typedef __attribute__((address_space(3))) void LdsBytes;
+
+// The operands of one 32-key tile: codes from shared memory, scales as loaded.
 template <int D, int KB, int VB>
 struct NarrowTile {
     typedef KvSide<D, KB> KS;
     typedef KvSide<D, VB> VS;
     static constexpr int kLoads = KS::kPieces / 4;
     uint32_t k[2][kLoads][KS::kPiece / 4];
-    uint32_t ks[2][(KS::kBlocks + 3) / 4];
     uint32_t v[2][VS::kSlots * VS::kSlot / 4];
-    uint32_t vs[2];
-    bool some[2];                  // the unit has a page (wave-uniform)
 
-    __device__ __forceinline__ void load(const KvView &kv, const TileEntries &entries, int head, int key, int end) {
+    __device__ __forceinline__ void load(const uint8_t *tile) {
+        const int lane = threadIdx.x & 63;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const uint8_t *kc = tile + u * KS::kUnitCodes + lane * KS::kPiece;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) load_words<KS::kPiece>(kc + j * kLanes * KS::kPiece, k[u][j]);
+            const uint8_t *vc = tile + 2 * KS::kUnitCodes + u * VS::kUnitCodes + lane * VS::kSlot;
+#pragma unroll
+            for (int j = 0; j < VS::kSlots; ++j) load_words<VS::kSlot>(vc + j * kLanes * VS::kSlot, &v[u][j * (VS::kSlot / 4)]);
+        }
+    }
+};
+template <int D, int KB, int VB>
+struct NarrowScales {
+    typedef KvSide<D, KB> KS;
+    typedef KvSide<D, VB> VS;
+    uint32_t k[2][(KS::kBlocks + 3) / 4], v[2];
+    __device__ __forceinline__ void load(const KvView &kv, const int64_t (&unit)[2]) {
         const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int pos = key + u * kKvUnit;
-            const int page = pos < end ? kv.page_in(__builtin_amdgcn_readfirstlane(entries.entry[u]), pos) : -1;
-            some[u] = page >= 0;
-            const int64_t unit = kv.unit_of(max(page, 0), head, pos);
-            const uint8_t *kc = kv.codes[0] + unit * KS::kUnitCodes + lane * KS::kPiece;
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) load_words<KS::kPiece, true>(kc + j * kLanes * KS::kPiece, k[u][j]);
-            load_words<KS::kBlocks>(kv.scales[0] + unit * KS::kUnitScales + r * KS::kBlocks, ks[u]);
-            const uint8_t *vc = kv.codes[1] + unit * VS::kUnitCodes + lane * VS::kSlot;
-#pragma unroll
-            for (int j = 0; j < VS::kSlots; ++j) load_words<VS::kSlot, true>(vc + j * kLanes * VS::kSlot, &v[u][j * (VS::kSlot / 4)]);
-            load_words<4>(kv.scales[1] + unit * VS::kUnitScales + (g * VS::kBlocks + r * VS::kBlocks / 16) * 4, &vs[u]);
+            load_words<KS::kBlocks>(kv.scales[0] + unit[u] * KS::kUnitScales + r * KS::kBlocks, k[u]);
+            load_words<4>(kv.scales[1] + unit[u] * VS::kUnitScales + (g * VS::kBlocks + r * VS::kBlocks / 16) * 4, &v[u]);
         }
     }
 };
 
-template <int D, int KB, int VB>
-__global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_narrow_kernel(AttnArgs a) {
+// One side's codes of two units to shared memory, 16 bytes a lane.
+template <int UNIT>
+__device__ __forceinline__ void send_units(const uint8_t *codes, int64_t unit0, int64_t unit1, uint8_t *to) {
+    const int lane = threadIdx.x & 63;
+#pragma unroll
+    for (int n = 0; n < 2 * UNIT; n += kLanes * 16) {
+        const int u = UNIT >= kLanes * 16 ? n / UNIT : lane * 16 / UNIT;
+        const int at = UNIT >= kLanes * 16 ? n % UNIT + lane * 16 : lane * 16 % UNIT;
+        const uint8_t *from = codes + (u == 0 ? unit0 : unit1) * UNIT + at;
+        __builtin_amdgcn_global_load_lds((GlobalBytes *)from, (LdsBytes *)(to + n), 16, 0, kStream);
+    }
+}
+
+template <int D, int KB, int VB, int WAVES>
+__global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>::kPerSimd))
+    attn_narrow_kernel(AttnArgs a) {
+    typedef NarrowShape<D, KB, VB, WAVES> W;
     typedef KvSide<D, KB> KS;
+    typedef KvSide<D, VB> VS;
     constexpr int kSlices = D / 32;            // MFMAs of one unit's scores
-    constexpr int kRowDims = D / 16;           // elements of a value row
+    constexpr int kRowDims = W::kRowDims;      // elements of a value row
+    constexpr int kStep = WAVES * kTileKeys;
+    extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = blockIdx.y, z = blockIdx.z;
@@ -61,6 +98,37 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
     if (!tile.some) return;
     const KeyRange keys = key_range(a, 0, tile, blockIdx.x, head, z);
     if (!keys.some) return;
+
+    // The tile at `key` on its way: its codes to the wave's shared memory, its scales
+    // to registers, and which of its units have pages.
+    const KvView &kv = a.kv;
+    uint8_t *const mine = lds + wave * W::kTileBytes;
+    NarrowScales<D, KB, VB> scales;
+    bool some[2];
+    int entry[2];
+    const auto look_up = [&](int key) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) entry[u] = kv.entry_at(tile.s, key + u * kKvUnit);
+    };
+    const auto send = [&](int key) {
+        int64_t unit[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int pos = key + u * kKvUnit;
+            const int page = pos < keys.hi ? kv.page_in(__builtin_amdgcn_readfirstlane(entry[u]), pos) : -1;
+            some[u] = page >= 0;
+            unit[u] = kv.unit_of(max(page, 0), head, pos);
+        }
+        send_units<KS::kUnitCodes>(kv.codes[0], unit[0], unit[1], mine);
+        send_units<VS::kUnitCodes>(kv.codes[1], unit[0], unit[1], mine + W::kKeyBytes);
+        scales.load(kv, unit);
+    };
+    int key = keys.lo + wave * kTileKeys;
+    look_up(key);
+    if (key < keys.hi) {
+        send(key);
+        look_up(key + kStep);
+    }
 
     // The row of this lane's column, and its query operands.
     bf16x8 q[kSlices];
@@ -82,18 +150,33 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
         if (in) w = *reinterpret_cast<const u32x4 *>(src + d);
         q[m] = __builtin_bit_cast(bf16x8, w);
     }
-
     if (a.info && z == 0 && threadIdx.x < kNarrowRows && in)
         a.info[int64_t(token) * a.q_heads + qhead] = RowInfo{keys.part + c, kNarrowRows, keys.splits, 0};
 
-    floatx4 o[kRowDims];
-    // lr: the sum of the weights as rounded, which normalises the outputs
-    float mx = kNegInf, sub = 0.0f, l = 0.0f, lr = 0.0f;
+    // Weights are 2^(score - sub); l is their sum, lr the sum of the weights as
+    // rounded to bf16, which normalises the output and comes from the smallest
+    // matrix instruction (each lane's own four weights by ones).
+    floatx4 o[kRowDims], lr = {0, 0, 0, 0};
+    float sub = in ? kNegInf : 0.0f, l = 0.0f;       // rows that see nothing need no maximum
+    const s16x4 ones = {0x3F80, 0x3F80, 0x3F80, 0x3F80};
 #pragma unroll
     for (int j = 0; j < kRowDims; ++j) o[j] = floatx4{0, 0, 0, 0};
 
-    const auto step = [&](const NarrowTile<D, KB, VB> &x, int key, auto edge_tag) {
-        constexpr bool EDGE = decltype(edge_tag)::value != 0;
+    for (; key < keys.hi; key += kStep) {
+        __builtin_amdgcn_s_waitcnt(kWaitLoads);
+        NarrowTile<D, KB, VB> x;
+        x.load(mine);
+        const NarrowScales<D, KB, VB> xs = scales;
+        const bool some0 = some[0], some1 = some[1];
+        // the codes are in registers: the next tile may overwrite them
+        __builtin_amdgcn_s_waitcnt(kWaitLds);
+        __builtin_amdgcn_sched_barrier(0);
+        if (key + kStep < keys.hi) {
+            send(key + kStep);
+            look_up(key + 2 * kStep);
+        }
+        const bool edge = (key < tile.inner_lo) | (key + kTileKeys > min(tile.inner_hi, keys.hi)) | !some0 | !some1;
+
         // scores of two units: lane (g, c) has keys 4 g + i of each, row c
         floatx4 s[2];
 #pragma unroll
@@ -105,198 +188,179 @@ __global__ void __launch_bounds__(kNarrowWaves * kLanes, D <= 128 ? 3 : 1) attn_
                 const int j = m / per, e = m % per;
                 // the block of piece 4 j + g; the four lanes' blocks of a piece never cross a word
                 const int block = ((4 * j + g) * KS::kPieceDims) / kMxBlock;
-                const float unit = unit_of_byte(x.ks[u][4 * j * KS::kPieceDims / kMxBlock / 4], block & 3);
+                const float unit = unit_of_byte(xs.k[u][4 * j * KS::kPieceDims / kMxBlock / 4], block & 3);
                 bf16x8 k;
                 if constexpr (KB == 8) k = codes8(x.k[u][j][2 * e], x.k[u][j][2 * e + 1], unit);
                 else k = codes4(x.k[u][j][e], unit);
                 s[u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, q[m], s[u], 0, 0, 0);
             }
         }
-        uint32_t ones[4];                  // EDGE: the allowed keys as a bf16 operand of ones
-        uint32_t p[4];
-        float f[8];
-        float top = kNegInf;
+        unsigned seen = 0xFFu;                  // bit i: score i is of an allowed key
+        if (edge) {
+            const int first = key + 4 * g, last = min(khi, tile.hi);
+            seen = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            f[i] = s[i >> 2][i & 3] * a.scale_log2;
-            if constexpr (EDGE) {
-                const int pos = key + (i >> 2) * kKvUnit + 4 * g + (i & 3);
-                bool ok = pos >= klo && pos < khi;
-                if (a.tree) {
-                    const int b = pos - tile.past;
-                    ok = ok || (b >= 0 && b < tile.n && b < 64 && ((tree >> (b & 63)) & 1));
-                }
-                ok = ok && x.some[i >> 2] && pos < tile.hi;
-                if (!ok) f[i] = kNegInf;
-                const uint32_t one = ok ? 0x3F80u : 0u;
-                if (i & 1) ones[i >> 1] |= one << 16;
-                else ones[i >> 1] = one;
+            for (int e = 0; e < 8; ++e) {
+                const int at = first + (e >> 2) * kKvUnit + (e & 3);
+                seen |= unsigned((at >= klo) & (at < last)) << e;
             }
-            top = fmaxf(top, f[i]);
+            if (a.tree) {
+                const int drafted = min(min(tile.n, 64), tile.hi - tile.past);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int t = first + (e >> 2) * kKvUnit + (e & 3) - tile.past;
+                    seen |= (unsigned((t >= 0) & (t < drafted)) & unsigned(tree >> (t & 63))) << e;
+                }
+            }
+            seen &= (some0 ? 0x0Fu : 0u) | (some1 ? 0xF0u : 0u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[e >> 2][e & 3] = (seen >> e) & 1u ? s[e >> 2][e & 3] : kNegInf;
         }
-        if (__any(top > mx + kMaxSlack)) {
+        // The weights, against the reference that earlier tiles left.  It moves up
+        // only where their sum shows a weight too large (or none was set).
+        uint32_t p[4];
+        const auto weigh = [&](float ref) {
+            float w[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = exp2_fast(__builtin_fmaf(s[e >> 2][e & 3], a.scale_log2, -ref));
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = pack_bf16(w[2 * e], w[2 * e + 1]);
+            return ((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7]));
+        };
+        float total = weigh(sub == kNegInf ? 0.0f : sub);
+        if (__any(sub == kNegInf || total > kMaxSum)) {
+            float top = kNegInf;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, s[e >> 2][e & 3]);
+            top *= a.scale_log2;
             top = fmaxf(top, __shfl_xor(top, 16));
             top = fmaxf(top, __shfl_xor(top, 32));
-            const float m = fmaxf(mx, top);
-            const float by = m == mx ? 1.0f : exp2_fast(mx - m);
-            mx = m;
-            sub = m == kNegInf ? 0.0f : m;
+            const float m = fmaxf(sub, top);
+            const float by = m == sub ? 1.0f : exp2_fast(sub - m);
+            sub = m;
             l *= by;
             lr *= by;
 #pragma unroll
             for (int j = 0; j < kRowDims; ++j) o[j] *= by;
+            total = weigh(sub == kNegInf ? 0.0f : sub);
         }
-        float e[8];
+        l += total;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            e[i] = exp2_fast(f[i] - sub);
-            l += e[i];
-        }
+        for (int e = 0; e < 4; e += 2)
+            lr = __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(ones, __builtin_bit_cast(s16x4, u32x2{p[e], p[e + 1]}), lr, 0, 0, 0);
+
+        // In an edge tile, values of keys that no row of the tile sees, or without a
+        // page, become zeros, and NaN blocks too: zero weights times NaN would reach
+        // every row.  The product of the NaN marks with the allowed keys says which rows
+        // and elements are NaN.
+        uint32_t vs[2] = {xs.v[0], xs.v[1]};
+        if (edge) {
+            uint32_t bad = 0;                   // bit i where key slot i's block is NaN
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            p[i] = pack_bf16(e[2 * i], e[2 * i + 1]);
-            lr = add_pair(p[i], lr);
+            for (int e = 0; e < 8; ++e) {
+                const int u = e >> 2, at = key + u * kKvUnit + 4 * g + (e & 3);
+                const bool held = (u ? some1 : some0) && at >= tile.lo && at < tile.hi;
+                const bool nan = ((vs[u] >> (8 * (e & 3))) & 0xFFu) == 0xFFu;
+                bad |= unsigned(held && nan) << e;
+                if (held && !nan) continue;
+                vs[u] &= ~(0xFFu << (8 * (e & 3)));
+                clear_token<D, VB>(x.v[u], e & 3);
+            }
+            if (__any(bad != 0)) {
+                u32x4 mark, on;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mark[e] = ((bad >> (2 * e)) & 1 ? 0x3F80u : 0u) | ((bad >> (2 * e + 1)) & 1 ? 0x3F800000u : 0u);
+                    on[e] = ((seen >> (2 * e)) & 1 ? 0x3F80u : 0u) | ((seen >> (2 * e + 1)) & 1 ? 0x3F800000u : 0u);
+                }
+                const floatx4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, mark), __builtin_bit_cast(bf16x8, on), floatx4{0, 0, 0, 0}, 0, 0, 0);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int j = 0; j < kRowDims; ++j) o[j][e] = n[e] > 0.0f ? __builtin_nanf("") : o[j][e];
+            }
         }
         // values: the lane's row holds D / 16 elements of eight keys; two
         // elements of a key come at a time and are paired over keys
-        uint32_t keep[2] = {~0u, ~0u};         // EDGE: per token a byte of ones where its values count
-        uint32_t bad = 0;                      // EDGE: bit i where key slot i's block is NaN
-        if constexpr (EDGE) {
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int pos = key + u * kKvUnit + 4 * g + i;
-                    const bool held = x.some[u] && pos >= tile.lo && pos < tile.hi;
-                    const bool nan = ((x.vs[u] >> (8 * i)) & 0xFFu) == 0xFFu;
-                    if (!held || nan) keep[u] &= ~(0xFFu << (8 * i));
-                    if (held && nan) bad |= 1u << (4 * u + i);
-                }
-        }
+        const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]});
 #pragma unroll
         for (int jp = 0; jp < kRowDims / 2; ++jp) {
             uint32_t w[2][4];
 #pragma unroll
             for (int u = 0; u < 2; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    w[u][i] = value_pair<D, VB>(x.v[u], i, jp, unit_of_byte(x.vs[u], i));
-                    if constexpr (EDGE) w[u][i] = (keep[u] >> (8 * i)) & 1u ? w[u][i] : 0u;
-                }
+                for (int e = 0; e < 4; ++e) w[u][e] = value_pair<D, VB>(x.v[u], e, jp, unit_of_byte(vs[u], e));
             const u32x4 even = {low_halves(w[0][0], w[0][1]), low_halves(w[0][2], w[0][3]),
                                 low_halves(w[1][0], w[1][1]), low_halves(w[1][2], w[1][3])};
             const u32x4 odd = {high_halves(w[0][0], w[0][1]), high_halves(w[0][2], w[0][3]),
                                high_halves(w[1][0], w[1][1]), high_halves(w[1][2], w[1][3])};
-            const bf16x8 pb = __builtin_bit_cast(bf16x8, u32x4{p[0], p[1], p[2], p[3]});
             o[2 * jp] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, even), pb, o[2 * jp], 0, 0, 0);
             o[2 * jp + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, odd), pb, o[2 * jp + 1], 0, 0, 0);
         }
-        if constexpr (EDGE) {
-            // A NaN block counts only for the rows that see its key: its values
-            // were left out above (zero weights times NaN would reach every
-            // row), and a product of the NaN marks with the allowed keys says
-            // which rows and elements are NaN.
-            if (__any(bad != 0)) {
-                u32x4 mark;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mark[i] = ((bad >> (2 * i)) & 1 ? 0x3F80u : 0u) | ((bad >> (2 * i + 1)) & 1 ? 0x3F800000u : 0u);
-                const bf16x8 on = __builtin_bit_cast(bf16x8, u32x4{ones[0], ones[1], ones[2], ones[3]});
-                const floatx4 n = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, mark), on, floatx4{0, 0, 0, 0}, 0, 0, 0);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (n[i] > 0.0f)
-#pragma unroll
-                        for (int j = 0; j < kRowDims; ++j) o[j][i] = __builtin_nanf("");
-            }
-        }
-    };
-
-    // A wave takes every fourth tile; the page numbers of its next one are
-    // fetched while one is worked on.  Codes are not: three waves of a SIMD cover
-    // each other's loads, and a ring of two or three tiles in registers (two
-    // waves of a SIMD) measured 82 -> 92 us on 64 sequences of 4096 keys.
-    constexpr int kStep = kNarrowWaves * kTileKeys;
-    int key = keys.lo + wave * kTileKeys;
-    TileEntries entries;
-    entries.load(a.kv, tile.s, key);
-    for (; key < keys.hi; key += kStep) {
-        NarrowTile<D, KB, VB> x;
-        x.load(a.kv, entries, head, key, keys.hi);
-        entries.load(a.kv, tile.s, key + kStep);
-        const bool inner = key >= tile.inner_lo && key + kTileKeys <= min(tile.inner_hi, keys.hi) && x.some[0] && x.some[1];
-        if (inner) step(x, key, IntC<0>());
-        else step(x, key, IntC<1>());
     }
 
-    // Join the four waves: their maxima and sums, then their outputs, kRowDims in
-    // parts of at most 8 to bound the shared memory.
-    constexpr int kPart = kRowDims < 8 ? kRowDims : 8;
-    constexpr int kCols = 16 * kPart + 4;              // floats of one row's part, padded against bank conflicts
-    __shared__ float sm[kNarrowWaves][kNarrowRows], sl[kNarrowWaves][kNarrowRows], sr[kNarrowWaves][kNarrowRows];
-    __shared__ float so[kNarrowWaves][16][kCols];
+    // The waves meet: their references and sums, then their outputs, in parts.
+    float *const states = reinterpret_cast<float *>(lds + W::kStatesAt);      // [sub, l, lr][wave][row]
+    float *const outs = reinterpret_cast<float *>(lds);                       // [wave][row][kCols]
+    const auto state = [&](int what, int w, int r) -> float & { return states[(what * WAVES + w) * kNarrowRows + r]; };
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
-    lr += __shfl_xor(lr, 16);
-    lr += __shfl_xor(lr, 32);
+    float norm = lr[0] + __shfl_xor(lr[0], 16);
+    norm += __shfl_xor(norm, 32);
     if (g == 0) {
-        sr[wave][c] = lr;
-        sm[wave][c] = mx;
-        sl[wave][c] = l;
+        state(0, wave, c) = sub;
+        state(1, wave, c) = l;
+        state(2, wave, c) = norm;
     }
     __syncthreads();
     float m = kNegInf;
 #pragma unroll
-    for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, sm[w][c]);
-    const float by = mx == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mx - m);
+    for (int w = 0; w < WAVES; ++w) m = fmaxf(m, state(0, w, c));
+    const float by = piece_weight(sub, m);
+    constexpr int kShare = WAVES / 4, kEach = W::kPart / kShare;    // threads for a row's 16 value rows, and their elements
+    const int row16 = (threadIdx.x >> 4) & 15, piece = threadIdx.x & 15, from = threadIdx.x / 256 * kEach;
+    const int mine_row = tile.row0 + row16;
 #pragma unroll
-    for (int part = 0; part < kRowDims / kPart; ++part) {
+    for (int part = 0; part < kRowDims / W::kPart; ++part) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int e = 0; e < 4; ++e)
 #pragma unroll
-            for (int j = 0; j < kPart; ++j) so[wave][c][(4 * g + i) * kPart + j] = o[part * kPart + j][i] * by;
+            for (int j = 0; j < W::kPart; ++j)
+                outs[(wave * kNarrowRows + c) * W::kCols + (4 * g + e) * W::kPart + j] = o[part * W::kPart + j][e] * by;
         __syncthreads();
-        // thread (row, piece): kPart / ... elements of one row
-        constexpr int kEach = 16 * kPart / 16;
-        const int row16 = threadIdx.x >> 4, piece = threadIdx.x & 15;
-        const int row = tile.row0 + row16;
-        if (row < tile.rows) {
+        if (mine_row < tile.rows) {
             float mm = kNegInf, ll = 0.0f, rr = 0.0f;
 #pragma unroll
-            for (int w = 0; w < kNarrowWaves; ++w) mm = fmaxf(mm, sm[w][row16]);
+            for (int w = 0; w < WAVES; ++w) mm = fmaxf(mm, state(0, w, row16));
 #pragma unroll
-            for (int w = 0; w < kNarrowWaves; ++w) {
-                const float mw = sm[w][row16];
-                const float by = mw == kNegInf ? (mm == kNegInf ? 1.0f : 0.0f) : exp2_fast(mw - mm);
-                ll += sl[w][row16] * by;
-                rr += sr[w][row16] * by;
+            for (int w = 0; w < WAVES; ++w) {
+                const float b = piece_weight(state(0, w, row16), mm);
+                ll += state(1, w, row16) * b;
+                rr += state(2, w, row16) * b;
             }
             float y[kEach];
 #pragma unroll
             for (int j = 0; j < kEach; ++j) {
                 y[j] = 0.0f;
 #pragma unroll
-                for (int w = 0; w < kNarrowWaves; ++w) y[j] += so[w][row16][piece * kEach + j];
+                for (int w = 0; w < WAVES; ++w) y[j] += outs[(w * kNarrowRows + row16) * W::kCols + piece * W::kPart + from + j];
             }
-            const int i = row / a.group;
-            const int64_t at = int64_t(tile.begin + i) * a.q_heads + head * a.group + (row - i * a.group);
-            const int d = piece * kRowDims + part * kPart;
+            const int t = mine_row / a.group, at_head = head * a.group + (mine_row - t * a.group);
+            const int d = piece * kRowDims + part * W::kPart + from;
+            const bool facts = piece == 0 && part == 0 && from == 0;
             if (keys.splits > 1) {
                 const int64_t to = keys.part + row16;
                 float *dst = a.part_o + to * D + d;
 #pragma unroll
                 for (int j = 0; j < kEach; ++j) dst[j] = y[j];
-                if (piece == 0 && part == 0) {
-                    float *ml = a.part_ml + to * 4;
-                    *reinterpret_cast<float4 *>(ml) = float4{mm, ll, rr, 0.0f};
-                }
+                if (facts) *reinterpret_cast<float4 *>(a.part_ml + to * 4) = float4{mm, ll, rr, 0.0f};
             } else {
                 const float inv = mm == kNegInf && ll == 0.0f ? 0.0f : 1.0f / rr;
-                uint16_t *dst = a.out + int64_t(tile.begin + i) * a.out_stride + (head * a.group + (row - i * a.group)) * D + d;
+                uint16_t *dst = a.out + int64_t(tile.begin + t) * a.out_stride + at_head * D + d;
 #pragma unroll
                 for (int j = 0; j < kEach; j += 2)
                     *reinterpret_cast<uint32_t *>(dst + j) = pack_bf16(y[j] * inv, y[j + 1] * inv);
-                if (a.lse && piece == 0 && part == 0) a.lse[at] = lse_of(mm, ll);
+                if (a.lse && facts) a.lse[int64_t(tile.begin + t) * a.q_heads + at_head] = lse_of(mm, ll);
             }
         }
         __syncthreads();
@@ -319,10 +383,6 @@ __device__ __forceinline__ RowInfo row_info(const AttnArgs &a, int64_t u) {
         r.first + int64_t(r.pieces - 1) * r.stride >= a.part_rows)
         r.pieces = 0;
     return r;
-}
-
-__device__ __forceinline__ float piece_weight(float mz, float m) {
-    return mz == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mz - m);
 }
 
 __device__ __forceinline__ void store_row4(const AttnArgs &a, int D, int64_t u, int d, float m, float l, float lr,
@@ -452,16 +512,23 @@ int launch_attn_join(const AttnArgs &a, bool many, int dim, hipStream_t stream) 
     });
 }
 
-int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream) {
+template <int D, int K, int V, int WAVES>
+static int launch_narrow(const AttnArgs &a, int64_t tiles, hipStream_t stream) {
+    typedef NarrowShape<D, K, V, WAVES> W;
+    if (tiles >= kMaxGrid / W::kThreads) return NVFP4_ESHAPE;
+    if (!raise_lds<attn_narrow_kernel<D, K, V, WAVES>>(W::kLds)) return NVFP4_EHIP;
+    attn_narrow_kernel<D, K, V, WAVES><<<dim3(unsigned(tiles), unsigned(a.kv.heads), unsigned(a.cut[0].splits)),
+                                         W::kThreads, W::kLds, stream>>>(a);
+    return launch_status();
+}
+
+int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int waves, int dim, int k_format, int v_format,
+                       hipStream_t stream) {
     return kv_dim(dim, [&](auto d) {
         return kv_bits(k_format, [&](auto k) {
             return kv_bits(v_format, [&](auto v) {
                 constexpr int D = decltype(d)::value, K = decltype(k)::value, V = decltype(v)::value;
-                constexpr int kThreads = kNarrowWaves * kLanes;
-                if (tiles >= kMaxGrid / kThreads) return NVFP4_ESHAPE;
-                attn_narrow_kernel<D, K, V><<<dim3(unsigned(tiles), unsigned(a.kv.heads), unsigned(a.cut[0].splits)),
-                                              kThreads, 0, stream>>>(a);
-                return launch_status();
+                return waves == 8 ? launch_narrow<D, K, V, 8>(a, tiles, stream) : launch_narrow<D, K, V, 4>(a, tiles, stream);
             });
         });
     });

@@ -17,13 +17,10 @@
 // At D <= 128 a wave owns 32 rows.  At D = 256 two waves own 32 rows together,
 // each half the elements: they add their halves of the scores through shared
 // memory, take the same softmax, and each keeps half of the output.
-#include <mutex>
-
 #include "nvfp4_attn.h"
 
 namespace nvfp4 {
 
-typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
 template <int D>
@@ -537,22 +534,6 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
     }
 }
 
-// The kernels' shared memory passes the default limit; it is raised once per
-// device and kernel.
-template <int D, int K, int V>
-static bool wide_lds_ok() {
-    constexpr int kDevices = 64;
-    static std::once_flag once[kDevices];
-    static bool ok[kDevices];
-    int dev = 0;
-    if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices) return false;
-    std::call_once(once[dev], [&] {
-        ok[dev] = hipFuncSetAttribute(reinterpret_cast<const void *>(attn_wide_kernel<D, K, V>),
-                                      hipFuncAttributeMaxDynamicSharedMemorySize, WideShape<D>::kLds) == hipSuccess;
-    });
-    return ok[dev];
-}
-
 int wide_rows(int dim) { return kv_dim(dim, [](auto d) { return WideShape<decltype(d)::value>::kRows; }); }
 
 int launch_attn_wide(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream) {
@@ -563,7 +544,7 @@ int launch_attn_wide(const AttnArgs &a, int64_t tiles, int dim, int k_format, in
                 typedef WideShape<D> W;
                 const int64_t groups = tiles * a.kv.heads;
                 if (groups >= kMaxGrid / W::kThreads) return NVFP4_ESHAPE;
-                if (!wide_lds_ok<D, K, V>()) return NVFP4_EHIP;
+                if (!raise_lds<attn_wide_kernel<D, K, V>>(W::kLds)) return NVFP4_EHIP;
                 attn_wide_kernel<D, K, V><<<dim3(unsigned(groups), unsigned(a.cut[1].splits)), W::kThreads, W::kLds,
                                             stream>>>(a);
                 return launch_status();
