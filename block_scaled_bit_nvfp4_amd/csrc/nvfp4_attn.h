@@ -247,7 +247,7 @@ bool raise_lds(int bytes) {
 }
 
 // `tiles`: tile indexes.
-int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int waves, int dim, int k_format, int v_format, hipStream_t stream);
+int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream);
 int launch_attn_wide(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream);
 // Joins the splits; `many`: a workgroup per row, for rows in many splits.
 int launch_attn_join(const AttnArgs &a, bool many, int dim, hipStream_t stream);

@@ -18,7 +18,6 @@ struct AttnPlan {
     int64_t tiles[2];      // tile indexes; 0: the kernel is not needed
     int64_t part_rows;     // of the workspace; 0: no tile is split
     bool many;             // how the splits are joined
-    int waves;             // of the narrow kernel's workgroups
     int narrow_rows;
 };
 
@@ -51,17 +50,23 @@ static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int 
         return window > 0 ? std::min<int64_t>(context, int64_t(window) + rows / group + 1) : context;
     };
     p.cut[0] = AttnCut{kNarrowRows, 128, 1, 0, 0};
-    p.waves = 4;
     if (narrow) {
         // Workgroups to aim at: two for each CU where one sequence is split (more
-        // cost the join more than they gain: 131008 keys 53 us, with twice as many 58),
+        // cost the join more than they gain: 131008 keys 51 us, with twice as many 56),
         // up to twelve where several sequences of unknown lengths balance each
-        // other (64 ragged sequences: 92 us at three for each CU, 86 at twelve).
+        // other (64 ragged sequences: 85.5 us at six for each CU, 84.3 at twelve).
         p.cut[0].tiles_per_seq = wide ? kNarrowMost / kNarrowRows : 0;
         p.tiles[0] = wide ? int64_t(b->seqs) * p.cut[0].tiles_per_seq : b->tokens * group / kNarrowRows + b->seqs;
-        const int64_t target = 2 * kCus * std::min(b->seqs, 6);
+        const int64_t items = p.tiles[0] * c->heads, target = 2 * kCus * std::min(b->seqs, 6);
         const int64_t keys = span(kNarrowRows);
-        cut_keys(p.cut[0], keys, std::max<int64_t>(ceil_div(keys, ceil_div(target, p.tiles[0] * c->heads)), 256), window > 0, most_splits[0]);
+        // No split of fewer keys than a workgroup's start and the join are worth, which
+        // grows with the items that fill the card by themselves (900 keys: one
+        // sequence 10.0 us in splits of 256, 11.7 whole; 8 sequences 12.6, 12.0 in splits
+        // of 512; 64 sequences 33.5, 26.8 whole); up to 512 keys (8.4 us whole, 9.4
+        // split) nothing is split.
+        int64_t least = items >= 256 ? 1024 : items >= 64 ? 512 : 256;
+        if (keys <= 512) least = std::max(least, keys + 63);
+        cut_keys(p.cut[0], keys, std::max(ceil_div(keys, ceil_div(target, items)), least), window > 0, most_splits[0]);
     }
     p.cut[1] = AttnCut{wide_rows(dim), 128, 1, 0, 0};
     if (wide) {
@@ -170,7 +175,7 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
     a.part_o = cut ? reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + info_bytes(batch, q_heads)) : nullptr;
     a.part_ml = cut ? a.part_o + size_t(plan.part_rows) * dim : nullptr;
     if (plan.tiles[0] > 0)
-        if (int st = launch_attn_narrow(a, plan.tiles[0], plan.waves, dim, cache->k_format, cache->v_format, stream)) return st;
+        if (int st = launch_attn_narrow(a, plan.tiles[0], dim, cache->k_format, cache->v_format, stream)) return st;
     if (plan.tiles[1] > 0)
         if (int st = launch_attn_wide(a, plan.tiles[1], dim, cache->k_format, cache->v_format, stream)) return st;
     return cut ? launch_attn_join(a, plan.many, dim, stream) : NVFP4_OK;

@@ -12,26 +12,30 @@
 namespace nvfp4 {
 
 constexpr int kTileKeys = 32;      // keys of a wave's tile: two units
+constexpr int kNarrowWaves = 4, kNarrowThreads = kNarrowWaves * kLanes;
 
-template <int D, int KB, int VB, int WAVES>
+template <int D, int KB, int VB>
 struct NarrowShape {
     typedef KvSide<D, KB> KS;
     typedef KvSide<D, VB> VS;
-    static constexpr int kThreads = WAVES * kLanes;
-    static constexpr int kPerSimd = D == 256 ? 1 : WAVES == 8 ? 2 : D == 128 ? 3 : 4;   // waves, by registers
-    static constexpr int kKeyBytes = 2 * KS::kUnitCodes, kTileBytes = kKeyBytes + 2 * VS::kUnitCodes;
+    static constexpr int kPerSimd = D == 256 ? 2 : D == 128 ? 3 : 4;                 // waves, by registers
+    // a tile in shared memory: [key codes][value codes][scales]
+    static constexpr int kValuesAt = 2 * KS::kUnitCodes, kScalesAt = kValuesAt + 2 * VS::kUnitCodes;
+    static constexpr int kScaleBytes = 16 * D / 32, kScaleLoads = D == 256 ? 2 : 1;      // of a unit and side; of all four
+    static constexpr int kTileBytes = kScalesAt + kScaleLoads * kLanes * 4;
     // the waves' outputs meet in parts of at most 8 elements of each value row
     static constexpr int kRowDims = D / 16, kPart = kRowDims < 8 ? kRowDims : 8;
     static constexpr int kCols = 16 * kPart + 4;       // floats of one row's part, padded against bank conflicts
-    static constexpr int kMeet = WAVES * kNarrowRows * kCols * 4;
-    static constexpr int kStatesAt = WAVES * kTileBytes > kMeet ? WAVES * kTileBytes : kMeet;
-    static constexpr int kLds = kStatesAt + 3 * WAVES * kNarrowRows * 4;
+    static constexpr int kMeet = kNarrowWaves * kNarrowRows * kCols * 4;
+    static constexpr int kTiles = kNarrowWaves * kTileBytes;
+    static constexpr int kStatesAt = kTiles > kMeet ? kTiles : kMeet;
+    static constexpr int kLds = kStatesAt + 3 * kNarrowWaves * kNarrowRows * 4;
 };
 
 typedef __attribute__((address_space(1))) const void GlobalBytes;
 typedef __attribute__((address_space(3))) void LdsBytes;
 
-// The operands of one 32-key tile: codes from shared memory, scales as loaded.
+// The operands of one 32-key tile.
 template <int D, int KB, int VB>
 struct NarrowTile {
     typedef KvSide<D, KB> KS;
@@ -39,31 +43,20 @@ struct NarrowTile {
     static constexpr int kLoads = KS::kPieces / 4;
     uint32_t k[2][kLoads][KS::kPiece / 4];
     uint32_t v[2][VS::kSlots * VS::kSlot / 4];
+    uint32_t ks[2][(KS::kBlocks + 3) / 4], vs[2];
 
-    __device__ __forceinline__ void load(const uint8_t *tile) {
-        const int lane = threadIdx.x & 63;
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-            const uint8_t *kc = tile + u * KS::kUnitCodes + lane * KS::kPiece;
-#pragma unroll
-            for (int j = 0; j < kLoads; ++j) load_words<KS::kPiece>(kc + j * kLanes * KS::kPiece, k[u][j]);
-            const uint8_t *vc = tile + 2 * KS::kUnitCodes + u * VS::kUnitCodes + lane * VS::kSlot;
-#pragma unroll
-            for (int j = 0; j < VS::kSlots; ++j) load_words<VS::kSlot>(vc + j * kLanes * VS::kSlot, &v[u][j * (VS::kSlot / 4)]);
-        }
-    }
-};
-template <int D, int KB, int VB>
-struct NarrowScales {
-    typedef KvSide<D, KB> KS;
-    typedef KvSide<D, VB> VS;
-    uint32_t k[2][(KS::kBlocks + 3) / 4], v[2];
-    __device__ __forceinline__ void load(const KvView &kv, const int64_t (&unit)[2]) {
+    __device__ __forceinline__ void load(const uint8_t *keys, const uint8_t *values, const uint8_t *scales) {
         const int lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            load_words<KS::kBlocks>(kv.scales[0] + unit[u] * KS::kUnitScales + r * KS::kBlocks, k[u]);
-            load_words<4>(kv.scales[1] + unit[u] * VS::kUnitScales + (g * VS::kBlocks + r * VS::kBlocks / 16) * 4, &v[u]);
+            const uint8_t *kc = keys + u * KS::kUnitCodes + lane * KS::kPiece;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) load_words<KS::kPiece>(kc + j * kLanes * KS::kPiece, k[u][j]);
+            load_words<KS::kBlocks>(scales + u * KS::kUnitScales + r * KS::kBlocks, ks[u]);
+            const uint8_t *vc = values + u * VS::kUnitCodes + lane * VS::kSlot;
+#pragma unroll
+            for (int j = 0; j < VS::kSlots; ++j) load_words<VS::kSlot>(vc + j * kLanes * VS::kSlot, &v[u][j * (VS::kSlot / 4)]);
+            load_words<4>(scales + (2 + u) * VS::kUnitScales + (g * VS::kBlocks + r * VS::kBlocks / 16) * 4, &vs[u]);
         }
     }
 };
@@ -81,15 +74,15 @@ __device__ __forceinline__ void send_units(const uint8_t *codes, int64_t unit0, 
     }
 }
 
-template <int D, int KB, int VB, int WAVES>
-__global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>::kPerSimd))
+template <int D, int KB, int VB>
+__global__ void __launch_bounds__(kNarrowThreads, (NarrowShape<D, KB, VB>::kPerSimd))
     attn_narrow_kernel(AttnArgs a) {
-    typedef NarrowShape<D, KB, VB, WAVES> W;
+    typedef NarrowShape<D, KB, VB> W;
     typedef KvSide<D, KB> KS;
     typedef KvSide<D, VB> VS;
     constexpr int kSlices = D / 32;            // MFMAs of one unit's scores
     constexpr int kRowDims = W::kRowDims;      // elements of a value row
-    constexpr int kStep = WAVES * kTileKeys;
+    constexpr int kStep = kNarrowWaves * kTileKeys;
     extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, g = lane >> 4, c = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -99,29 +92,40 @@ __global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>
     const KeyRange keys = key_range(a, 0, tile, blockIdx.x, head, z);
     if (!keys.some) return;
 
-    // The tile at `key` on its way: its codes to the wave's shared memory, its scales
-    // to registers, and which of its units have pages.
+    // The tile at `key` on its way to the wave's shared memory, and which of its units
+    // have pages (a bit each).  The table's entries come a tile earlier.
     const KvView &kv = a.kv;
     uint8_t *const mine = lds + wave * W::kTileBytes;
-    NarrowScales<D, KB, VB> scales;
-    bool some[2];
-    int entry[2];
+    int has = 0, entry[2];
+    // the lane's four bytes of scales: of a side's unit `second` (of two), in as many loads as it takes
+    const uint8_t *scale_of[W::kScaleLoads];
+    bool second[W::kScaleLoads];
+#pragma unroll
+    for (int n = 0; n < W::kScaleLoads; ++n) {
+        const int at = n * kLanes * 4 + lane * 4, region = at / W::kScaleBytes & 3;
+        scale_of[n] = kv.scales[region >> 1] + at % W::kScaleBytes;
+        second[n] = region & 1;
+    }
     const auto look_up = [&](int key) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) entry[u] = kv.entry_at(tile.s, key + u * kKvUnit);
+        for (int u = 0; u < 2; ++u) entry[u] = kv.entry_at_scalar(tile.s, key + u * kKvUnit);
     };
     const auto send = [&](int key) {
         int64_t unit[2];
+        has = 0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int pos = key + u * kKvUnit;
-            const int page = pos < keys.hi ? kv.page_in(__builtin_amdgcn_readfirstlane(entry[u]), pos) : -1;
-            some[u] = page >= 0;
+            const int page = pos < keys.hi ? kv.page_in(entry[u], pos) : -1;
+            has |= (page >= 0) << u;
             unit[u] = kv.unit_of(max(page, 0), head, pos);
         }
         send_units<KS::kUnitCodes>(kv.codes[0], unit[0], unit[1], mine);
-        send_units<VS::kUnitCodes>(kv.codes[1], unit[0], unit[1], mine + W::kKeyBytes);
-        scales.load(kv, unit);
+        send_units<VS::kUnitCodes>(kv.codes[1], unit[0], unit[1], mine + W::kValuesAt);
+#pragma unroll
+        for (int n = 0; n < W::kScaleLoads; ++n)
+            __builtin_amdgcn_global_load_lds((GlobalBytes *)(scale_of[n] + (second[n] ? unit[1] : unit[0]) * W::kScaleBytes),
+                                             (LdsBytes *)(mine + W::kScalesAt + n * kLanes * 4), 4, 0, 0);
     };
     int key = keys.lo + wave * kTileKeys;
     look_up(key);
@@ -165,10 +169,9 @@ __global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>
     for (; key < keys.hi; key += kStep) {
         __builtin_amdgcn_s_waitcnt(kWaitLoads);
         NarrowTile<D, KB, VB> x;
-        x.load(mine);
-        const NarrowScales<D, KB, VB> xs = scales;
-        const bool some0 = some[0], some1 = some[1];
-        // the codes are in registers: the next tile may overwrite them
+        x.load(mine, mine + W::kValuesAt, mine + W::kScalesAt);
+        const bool some0 = has & 1, some1 = has & 2;
+        // the tile is in registers: the next one may overwrite it
         __builtin_amdgcn_s_waitcnt(kWaitLds);
         __builtin_amdgcn_sched_barrier(0);
         if (key + kStep < keys.hi) {
@@ -188,7 +191,7 @@ __global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>
                 const int j = m / per, e = m % per;
                 // the block of piece 4 j + g; the four lanes' blocks of a piece never cross a word
                 const int block = ((4 * j + g) * KS::kPieceDims) / kMxBlock;
-                const float unit = unit_of_byte(xs.k[u][4 * j * KS::kPieceDims / kMxBlock / 4], block & 3);
+                const float unit = unit_of_byte(x.ks[u][4 * j * KS::kPieceDims / kMxBlock / 4], block & 3);
                 bf16x8 k;
                 if constexpr (KB == 8) k = codes8(x.k[u][j][2 * e], x.k[u][j][2 * e + 1], unit);
                 else k = codes4(x.k[u][j][e], unit);
@@ -253,7 +256,7 @@ __global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>
         // page, become zeros, and NaN blocks too: zero weights times NaN would reach
         // every row.  The product of the NaN marks with the allowed keys says which rows
         // and elements are NaN.
-        uint32_t vs[2] = {xs.v[0], xs.v[1]};
+        uint32_t vs[2] = {x.vs[0], x.vs[1]};
         if (edge) {
             uint32_t bad = 0;                   // bit i where key slot i's block is NaN
 #pragma unroll
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>
     // The waves meet: their references and sums, then their outputs, in parts.
     float *const states = reinterpret_cast<float *>(lds + W::kStatesAt);      // [sub, l, lr][wave][row]
     float *const outs = reinterpret_cast<float *>(lds);                       // [wave][row][kCols]
-    const auto state = [&](int what, int w, int r) -> float & { return states[(what * WAVES + w) * kNarrowRows + r]; };
+    const auto state = [&](int what, int w, int r) -> float & { return states[(what * kNarrowWaves + w) * kNarrowRows + r]; };
     l += __shfl_xor(l, 16);
     l += __shfl_xor(l, 32);
     float norm = lr[0] + __shfl_xor(lr[0], 16);
@@ -315,10 +318,9 @@ __global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>
     __syncthreads();
     float m = kNegInf;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) m = fmaxf(m, state(0, w, c));
+    for (int w = 0; w < kNarrowWaves; ++w) m = fmaxf(m, state(0, w, c));
     const float by = piece_weight(sub, m);
-    constexpr int kShare = WAVES / 4, kEach = W::kPart / kShare;    // threads for a row's 16 value rows, and their elements
-    const int row16 = (threadIdx.x >> 4) & 15, piece = threadIdx.x & 15, from = threadIdx.x / 256 * kEach;
+    const int row16 = threadIdx.x >> 4, piece = threadIdx.x & 15;
     const int mine_row = tile.row0 + row16;
 #pragma unroll
     for (int part = 0; part < kRowDims / W::kPart; ++part) {
@@ -331,34 +333,34 @@ __global__ void __launch_bounds__(WAVES * kLanes, (NarrowShape<D, KB, VB, WAVES>
         if (mine_row < tile.rows) {
             float mm = kNegInf, ll = 0.0f, rr = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) mm = fmaxf(mm, state(0, w, row16));
+            for (int w = 0; w < kNarrowWaves; ++w) mm = fmaxf(mm, state(0, w, row16));
 #pragma unroll
-            for (int w = 0; w < WAVES; ++w) {
+            for (int w = 0; w < kNarrowWaves; ++w) {
                 const float b = piece_weight(state(0, w, row16), mm);
                 ll += state(1, w, row16) * b;
                 rr += state(2, w, row16) * b;
             }
-            float y[kEach];
+            float y[W::kPart];
 #pragma unroll
-            for (int j = 0; j < kEach; ++j) {
+            for (int j = 0; j < W::kPart; ++j) {
                 y[j] = 0.0f;
 #pragma unroll
-                for (int w = 0; w < WAVES; ++w) y[j] += outs[(w * kNarrowRows + row16) * W::kCols + piece * W::kPart + from + j];
+                for (int w = 0; w < kNarrowWaves; ++w) y[j] += outs[(w * kNarrowRows + row16) * W::kCols + piece * W::kPart + j];
             }
             const int t = mine_row / a.group, at_head = head * a.group + (mine_row - t * a.group);
-            const int d = piece * kRowDims + part * W::kPart + from;
-            const bool facts = piece == 0 && part == 0 && from == 0;
+            const int d = piece * kRowDims + part * W::kPart;
+            const bool facts = piece == 0 && part == 0;
             if (keys.splits > 1) {
                 const int64_t to = keys.part + row16;
                 float *dst = a.part_o + to * D + d;
 #pragma unroll
-                for (int j = 0; j < kEach; ++j) dst[j] = y[j];
+                for (int j = 0; j < W::kPart; ++j) dst[j] = y[j];
                 if (facts) *reinterpret_cast<float4 *>(a.part_ml + to * 4) = float4{mm, ll, rr, 0.0f};
             } else {
                 const float inv = mm == kNegInf && ll == 0.0f ? 0.0f : 1.0f / rr;
                 uint16_t *dst = a.out + int64_t(tile.begin + t) * a.out_stride + at_head * D + d;
 #pragma unroll
-                for (int j = 0; j < kEach; j += 2)
+                for (int j = 0; j < W::kPart; j += 2)
                     *reinterpret_cast<uint32_t *>(dst + j) = pack_bf16(y[j] * inv, y[j + 1] * inv);
                 if (a.lse && facts) a.lse[int64_t(tile.begin + t) * a.q_heads + at_head] = lse_of(mm, ll);
             }
@@ -512,23 +514,21 @@ int launch_attn_join(const AttnArgs &a, bool many, int dim, hipStream_t stream) 
     });
 }
 
-template <int D, int K, int V, int WAVES>
+template <int D, int K, int V>
 static int launch_narrow(const AttnArgs &a, int64_t tiles, hipStream_t stream) {
-    typedef NarrowShape<D, K, V, WAVES> W;
-    if (tiles >= kMaxGrid / W::kThreads) return NVFP4_ESHAPE;
-    if (!raise_lds<attn_narrow_kernel<D, K, V, WAVES>>(W::kLds)) return NVFP4_EHIP;
-    attn_narrow_kernel<D, K, V, WAVES><<<dim3(unsigned(tiles), unsigned(a.kv.heads), unsigned(a.cut[0].splits)),
-                                         W::kThreads, W::kLds, stream>>>(a);
+    typedef NarrowShape<D, K, V> W;
+    if (tiles >= kMaxGrid / kNarrowThreads) return NVFP4_ESHAPE;
+    if (!raise_lds<attn_narrow_kernel<D, K, V>>(W::kLds)) return NVFP4_EHIP;
+    attn_narrow_kernel<D, K, V><<<dim3(unsigned(tiles), unsigned(a.kv.heads), unsigned(a.cut[0].splits)),
+                                         kNarrowThreads, W::kLds, stream>>>(a);
     return launch_status();
 }
 
-int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int waves, int dim, int k_format, int v_format,
-                       hipStream_t stream) {
+int launch_attn_narrow(const AttnArgs &a, int64_t tiles, int dim, int k_format, int v_format, hipStream_t stream) {
     return kv_dim(dim, [&](auto d) {
         return kv_bits(k_format, [&](auto k) {
             return kv_bits(v_format, [&](auto v) {
-                constexpr int D = decltype(d)::value, K = decltype(k)::value, V = decltype(v)::value;
-                return waves == 8 ? launch_narrow<D, K, V, 8>(a, tiles, stream) : launch_narrow<D, K, V, 4>(a, tiles, stream);
+                return launch_narrow<decltype(d)::value, decltype(k)::value, decltype(v)::value>(a, tiles, stream);
             });
         });
     });

@@ -69,6 +69,12 @@ struct KvView {
     __device__ __forceinline__ int entry_at(int s, int pos) const {
         return table[int64_t(s) * width + (min(max(pos, 0), capacity - 1) >> page_shift)];
     }
+    // The same as a scalar load, for `s` and `pos` that are the same in the whole wave.
+    __device__ __forceinline__ int entry_at_scalar(int s, int pos) const {
+        const int at = __builtin_amdgcn_readfirstlane(min(max(pos, 0), capacity - 1) >> page_shift);
+        typedef __attribute__((address_space(4))) const int32_t Constant;
+        return ((Constant *)(table + int64_t(__builtin_amdgcn_readfirstlane(s)) * width))[at];
+    }
     __device__ __forceinline__ int page_in(int entry, int pos) const {
         return pos >= 0 && pos < capacity && entry >= 0 && entry < pages ? entry : -1;
     }
