@@ -433,14 +433,26 @@ def _rows(name, t, cache, batch, heads, dtypes):
     if t.dtype not in dtypes:
         raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
     dim = cache.head_dim
-    if t.shape != (batch.tokens, heads, dim):
-        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (batch.tokens, heads, dim)))
-    stride = t.stride()
-    if batch.tokens and (stride[2] != 1 or (heads > 1 and stride[1] != dim)):
+    tokens = batch.tokens
+    if t.shape != (tokens, heads, dim):
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (tokens, heads, dim)))
+    token, head, element = t.stride()
+    if tokens and (element != 1 or (heads > 1 and head != dim)):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
     if t.device != cache.device:
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, cache.device))
-    return stride[0] if batch.tokens > 1 else heads * dim
+    return token if tokens > 1 else heads * dim
+
+
+# torch's getter of the current stream's handle; its public one builds an object
+# around it, 2 us of a call that takes 10.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _kv_stream(stream, t):
+    if stream is None and _raw_stream is not None and t.is_cuda:
+        return _raw_stream(t.get_device())
+    return _stream(stream, t)
 
 
 def _kv_pair(cache, batch):
@@ -455,7 +467,7 @@ def nvfp4_kv_append(cache, batch, K, V, stream=None):
     ks = _rows("K", K, cache, batch, cache.heads, _KV_DTYPE)
     vs = _rows("V", V, cache, batch, cache.heads, (K.dtype,))
     _check(load().nvfp4_kv_append(cache._ref, batch._ref, _KV_DTYPE[K.dtype], K.data_ptr(), ks, V.data_ptr(), vs,
-                                  _stream(stream, K)), "nvfp4_kv_append")
+                                  _kv_stream(stream, K)), "nvfp4_kv_append")
 
 
 def nvfp4_kv_read(cache, batch, K=None, V=None, stream=None):
@@ -468,7 +480,7 @@ def nvfp4_kv_read(cache, batch, K=None, V=None, stream=None):
         raise ValueError("K is %s, V %s" % (K.dtype, V.dtype))
     _check(load().nvfp4_kv_read(cache._ref, batch._ref, _KV_DTYPE[given[0].dtype],
                                 None if K is None else K.data_ptr(), ks, None if V is None else V.data_ptr(), vs,
-                                _stream(stream, given[0])), "nvfp4_kv_read")
+                                _kv_stream(stream, given[0])), "nvfp4_kv_read")
 
 
 def nvfp4_kv_attention_workspace_bytes(cache, batch, q_heads) -> int:
@@ -496,5 +508,5 @@ def nvfp4_kv_attention(cache, batch, Q, scale, out, lse=None, window=0, tree=Non
     _check(load().nvfp4_kv_attention(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale), int(window),
                                      None if tree is None else tree.data_ptr(), out.data_ptr(), os_,
                                      None if lse is None else lse.data_ptr(),
-                                     workspace.data_ptr() if nbytes else None, nbytes, _stream(stream, Q)),
+                                     workspace.data_ptr() if nbytes else None, nbytes, _kv_stream(stream, Q)),
            "nvfp4_kv_attention")

@@ -64,26 +64,52 @@ __device__ __forceinline__ void load16(const uint16_t *p, float (&x)[16]) {
         }
     }
 }
-__device__ __forceinline__ void store16(float *p, const float (&x)[16]) {
+// Stores of 16 elements a lane, four lanes in a row.  The lanes of a four exchange
+// their words, so that each store instruction writes whole 64-byte runs.
+template <int CTRL>
+__device__ __forceinline__ uint32_t of_four(uint32_t w) {
+    return uint32_t(__builtin_amdgcn_update_dpp(0, int(w), CTRL, 0xF, 0xF, false));
+}
+template <int FROM>
+__device__ __forceinline__ void store_run(float *p, const float (&x)[16], int q) {
+    u32x4 w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4 *>(p)[i] = float4{x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]};
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = of_four<FROM * 0x55>(__float_as_uint(x[j])), b = of_four<FROM * 0x55>(__float_as_uint(x[4 + j]));
+        const uint32_t c = of_four<FROM * 0x55>(__float_as_uint(x[8 + j])), d = of_four<FROM * 0x55>(__float_as_uint(x[12 + j]));
+        w[j] = q & 2 ? (q & 1 ? d : c) : (q & 1 ? b : a);
+    }
+    reinterpret_cast<u32x4 *>(p)[4 * FROM] = w;
+}
+__device__ __forceinline__ void store16(float *p, const float (&x)[16], int q) {
+    p += 4 * q - 16 * q;
+    store_run<0>(p, x, q);
+    store_run<1>(p, x, q);
+    store_run<2>(p, x, q);
+    store_run<3>(p, x, q);
 }
 // The values are bf16 values (or lose bits below bf16's smallest subnormal
 // only), so the conversion does not round.
-__device__ __forceinline__ void store16(uint16_t *p, const float (&x)[16]) {
+__device__ __forceinline__ void store16(uint16_t *p, const float (&x)[16], int q) {
+    uint32_t w[8];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        u32x4 w;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            bf16x2 v;
-            v[0] = static_cast<__bf16>(x[8 * i + 2 * j]);
-            v[1] = static_cast<__bf16>(x[8 * i + 2 * j + 1]);
-            w[j] = as_u32(v);
-        }
-        reinterpret_cast<u32x4 *>(p)[i] = w;
+    for (int j = 0; j < 8; ++j) {
+        bf16x2 v;
+        v[0] = static_cast<__bf16>(x[2 * j]);
+        v[1] = static_cast<__bf16>(x[2 * j + 1]);
+        w[j] = as_u32(v);
     }
+    u32x4 lo, hi;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t a = of_four<0x50>(w[j]), b = of_four<0x50>(w[4 + j]);     // lanes 0 0 1 1
+        const uint32_t c = of_four<0xFA>(w[j]), d = of_four<0xFA>(w[4 + j]);     // lanes 2 2 3 3
+        lo[j] = q & 1 ? b : a;
+        hi[j] = q & 1 ? d : c;
+    }
+    p += 8 * q - 16 * q;
+    reinterpret_cast<u32x4 *>(p)[0] = lo;
+    reinterpret_cast<u32x4 *>(p)[4] = hi;
 }
 
 // Exponent E of a block's scale from the bits of its largest magnitude.
@@ -176,125 +202,162 @@ __device__ __forceinline__ void move_codes(uint8_t *unit, int r, int part, uint3
     }
 }
 
-// A thread's place in the batch: token row `t`, its unit and place there.
-struct KvPlace {
-    int64_t unit;
-    int r;
-    bool ok;
+// The places in the cache of a thread's N token rows t0, t0 + 1, ...
+template <int N>
+struct KvPlaces {
+    int64_t unit[N];
+    int r[N];              // the token of the unit
+    bool in[N], ok[N];     // whether the row is one of the batch's, and has a page
 };
-__device__ __forceinline__ KvPlace kv_place(const KvView &v, int t, int head) {
+template <int N>
+__device__ __forceinline__ KvPlaces<N> kv_places(const KvView &v, int t0, int head) {
     // the wave's first token finds its sequence together; a later lane's is a
     // few sequences on at most
-    const int t0 = __builtin_amdgcn_readfirstlane(t);
-    int s = wave_count_le(v.seqs, t0, [&](int i) { return v.offsets[i]; }) - 1;
+    int s = wave_count_le(v.seqs, __builtin_amdgcn_readfirstlane(t0), [&](int i) { return v.offsets[i]; }) - 1;
     s = max(s, 0);
-    while (s + 1 < v.seqs && v.offsets[s + 1] <= t) ++s;
-    int begin, end, before;
-    v.sequence(s, begin, end, before);
-    const int pos = before + (t - begin);
-    const int page = t >= begin && t < end ? v.page_of(s, pos) : -1;
-    KvPlace p;
-    p.ok = page >= 0;
-    p.unit = v.unit_of(max(page, 0), head, max(pos, 0));
-    p.r = pos & (kKvUnit - 1);
+    int begin = 0, end = 0, before = 0, seq[N], pos[N], entry[N];
+    KvPlaces<N> p;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int t = t0 + i;
+        if (i == 0 || t >= end) {
+            while (s + 1 < v.seqs && v.offsets[s + 1] <= t) ++s;
+            v.sequence(s, begin, end, before);
+        }
+        seq[i] = s;
+        pos[i] = before + (t - begin);
+        p.in[i] = t >= begin && t < end;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) entry[i] = v.entry_at(seq[i], pos[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const int page = p.in[i] ? v.page_in(entry[i], pos[i]) : -1;
+        p.ok[i] = page >= 0;
+        p.unit[i] = v.unit_of(max(page, 0), head, max(pos[i], 0));
+        p.r[i] = pos[i] & (kKvUnit - 1);
+    }
     return p;
 }
 
-// One thread takes 16 elements of one token's head; two neighbours share a
+// What a thread of append and read takes: 16 elements of a head of N tokens in a row.
+template <int N, int D>
+struct KvThread {
+    int t0, head, part;
+    bool in;
+    __device__ __forceinline__ KvThread(const KvView &v) {
+        constexpr int kParts = D / 16;
+        const int64_t u = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
+        const int64_t rows = int64_t((v.tokens + N - 1) / N) * v.heads;
+        in = u < rows * kParts;
+        const int row = int(in ? u / kParts : rows - 1);
+        part = int(u % kParts);
+        const int group = row / v.heads;
+        head = row - group * v.heads;
+        t0 = group * N;
+    }
+};
+
+// One thread takes 16 elements of a head of N tokens; two neighbours share a
 // block.  Bound by bytes (2 or 4 read and 1 or 1/2 written per element) for a
-// chunk of tokens and by the launch for one token.
-template <int D, int BITS, int SIDE, class T>
-__device__ __forceinline__ void append16(const KvView &v, const KvPlace &p, const T *src, int part) {
+// chunk of tokens (where several tokens a thread share the search for their place and
+// have their loads in flight together), and by the launch for a few tokens.
+template <int N, int D, int BITS, int SIDE, class T>
+__device__ __forceinline__ void append16(const KvView &v, const KvPlaces<N> &p, const T *src, int64_t stride, int part) {
     typedef KvSide<D, BITS> S;
-    float x[16];
-    load16(src, x);
-    uint32_t amax = 0;
+    float x[N][16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) amax = max(amax, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    amax = max(amax, uint32_t(__builtin_amdgcn_update_dpp(0, int(amax), 0xB1, 0xF, 0xF, false)));   // the neighbour's
-    if (!p.ok) return;
-    const bool bad = amax >= 0x7F800000u;
-    const int E = block_exponent<BITS>(bad ? 0u : amax);
-    uint32_t w[BITS / 2];
-    quantise16<BITS>(x, E, bad, w);
-    move_codes<D, BITS, SIDE, false>(v.codes[SIDE] + p.unit * S::kUnitCodes, p.r, part, w);
-    if ((part & 1) == 0) {
-        const int b = part / 2;
-        v.scales[SIDE][p.unit * S::kUnitScales + (SIDE == 0 ? S::key_scale(p.r, b) : S::value_scale(p.r, b))] =
-            uint8_t(bad ? 0xFF : E + 127);
+    for (int i = 0; i < N; ++i)
+        if (p.in[i]) load16(src + i * stride, x[i]);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        uint32_t amax = 0;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) amax = max(amax, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
+        amax = max(amax, uint32_t(__builtin_amdgcn_update_dpp(0, int(amax), 0xB1, 0xF, 0xF, false)));   // the neighbour's
+        if (!p.ok[i]) continue;
+        const bool bad = amax >= 0x7F800000u;
+        const int E = block_exponent<BITS>(bad ? 0u : amax);
+        uint32_t w[BITS / 2];
+        quantise16<BITS>(x[i], E, bad, w);
+        move_codes<D, BITS, SIDE, false>(v.codes[SIDE] + p.unit[i] * S::kUnitCodes, p.r[i], part, w);
+        if ((part & 1) == 0) {
+            const int b = part / 2;
+            v.scales[SIDE][p.unit[i] * S::kUnitScales + (SIDE == 0 ? S::key_scale(p.r[i], b) : S::value_scale(p.r[i], b))] =
+                uint8_t(bad ? 0xFF : E + 127);
+        }
     }
 }
 
-template <int D, class T>
+template <int N, int D, class T>
 __global__ void __launch_bounds__(256) kv_append_kernel(KvView v, int k_bits, int v_bits, const T *__restrict__ k,
                                                         int64_t k_stride, const T *__restrict__ x, int64_t v_stride) {
-    constexpr int kParts = D / 16;
-    const int64_t u = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int64_t rows = int64_t(v.tokens) * v.heads;
-    const bool in = u < rows * kParts;
-    const int row = int(in ? u / kParts : rows - 1), part = int(u % kParts);
-    const int t = row / v.heads, head = row - t * v.heads;
-    KvPlace p = kv_place(v, t, head);
-    p.ok = p.ok && in;
+    const KvThread<N, D> a(v);
+    KvPlaces<N> p = kv_places<N>(v, a.t0, a.head);
+    if (!a.in) return;                                   // neighbours return together
     const int side = blockIdx.y;
-    const T *src = (side == 0 ? k + t * k_stride : x + t * v_stride) + head * D + part * 16;
+    const int64_t stride = side == 0 ? k_stride : v_stride;
+    const T *src = (side == 0 ? k : x) + a.t0 * stride + a.head * D + a.part * 16;
     if (side == 0) {
-        if (k_bits == 8) append16<D, 8, 0>(v, p, src, part);
-        else append16<D, 4, 0>(v, p, src, part);
+        if (k_bits == 8) append16<N, D, 8, 0>(v, p, src, stride, a.part);
+        else append16<N, D, 4, 0>(v, p, src, stride, a.part);
     } else {
-        if (v_bits == 8) append16<D, 8, 1>(v, p, src, part);
-        else append16<D, 4, 1>(v, p, src, part);
+        if (v_bits == 8) append16<N, D, 8, 1>(v, p, src, stride, a.part);
+        else append16<N, D, 4, 1>(v, p, src, stride, a.part);
     }
 }
 
 // --------------------------------------------------------------------- read
 
-template <int D, int BITS, int SIDE, class T>
-__device__ __forceinline__ void read16(const KvView &v, const KvPlace &p, T *dst, int part) {
+template <int N, int D, int BITS, int SIDE, class T>
+__device__ __forceinline__ void read16(const KvView &v, const KvPlaces<N> &p, T *dst, int64_t stride, int part) {
     typedef KvSide<D, BITS> S;
-    float x[16] = {};
-    if (p.ok) {
-        uint32_t w[BITS / 2] = {};
-        move_codes<D, BITS, SIDE, true>(v.codes[SIDE] + p.unit * S::kUnitCodes, p.r, part, w);
+    uint32_t w[N][BITS / 2] = {};
+    uint8_t scale[N] = {};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        if (!p.ok[i]) continue;
         const int b = part / 2;
-        const float unit =
-            e8m0_f32(v.scales[SIDE][p.unit * S::kUnitScales + (SIDE == 0 ? S::key_scale(p.r, b) : S::value_scale(p.r, b))]);
+        move_codes<D, BITS, SIDE, true>(v.codes[SIDE] + p.unit[i] * S::kUnitCodes, p.r[i], part, w[i]);
+        scale[i] = v.scales[SIDE][p.unit[i] * S::kUnitScales + (SIDE == 0 ? S::key_scale(p.r[i], b) : S::value_scale(p.r[i], b))];
+    }
 #pragma unroll
-        for (int i = 0; i < BITS / 2; ++i) {
+    for (int i = 0; i < N; ++i) {
+        if (!p.in[i]) continue;
+        float x[16];
+        const float unit = e8m0_f32(scale[i]);           // tokens without a page: zeros by their codes
+#pragma unroll
+        for (int k = 0; k < BITS / 2; ++k) {
             if constexpr (BITS == 8) {
-                const float2 lo = e4m3x2_f32(w[i], 0), hi = e4m3x2_f32(w[i], 1);
-                x[4 * i] = lo.x * unit; x[4 * i + 1] = lo.y * unit;
-                x[4 * i + 2] = hi.x * unit; x[4 * i + 3] = hi.y * unit;
+                const float2 lo = e4m3x2_f32(w[i][k], 0), hi = e4m3x2_f32(w[i][k], 1);
+                x[4 * k] = lo.x * unit; x[4 * k + 1] = lo.y * unit;
+                x[4 * k + 2] = hi.x * unit; x[4 * k + 3] = hi.y * unit;
             } else {
-                const bf16x8 c = e2m1x8_bf16(w[i]);
+                const bf16x8 c = e2m1x8_bf16(w[i][k]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[8 * i + j] = float(c[j]) * unit;
+                for (int j = 0; j < 8; ++j) x[8 * k + j] = float(c[j]) * unit;
             }
         }
+        store16(dst + i * stride, x, part & 3);
     }
-    store16(dst, x);
 }
 
-template <int D, class T>
+template <int N, int D, class T>
 __global__ void __launch_bounds__(256) kv_read_kernel(KvView v, int k_bits, int v_bits, T *__restrict__ k,
                                                       int64_t k_stride, T *__restrict__ x, int64_t v_stride) {
-    constexpr int kParts = D / 16;
     const int side = blockIdx.y;
     if ((side == 0 ? k : x) == nullptr) return;
-    const int64_t u = int64_t(blockIdx.x) * blockDim.x + threadIdx.x;
-    const int64_t rows = int64_t(v.tokens) * v.heads;
-    const bool in = u < rows * kParts;
-    const int row = int(in ? u / kParts : rows - 1), part = int(u % kParts);
-    const int t = row / v.heads, head = row - t * v.heads;
-    const KvPlace p = kv_place(v, t, head);
-    if (!in || t >= v.offsets[v.seqs]) return;
-    T *dst = (side == 0 ? k + t * k_stride : x + t * v_stride) + head * D + part * 16;
+    const KvThread<N, D> a(v);
+    KvPlaces<N> p = kv_places<N>(v, a.t0, a.head);
+    if (!a.in) return;
+    const int64_t stride = side == 0 ? k_stride : v_stride;
+    T *dst = (side == 0 ? k : x) + a.t0 * stride + a.head * D + a.part * 16;
     if (side == 0) {
-        if (k_bits == 8) read16<D, 8, 0>(v, p, dst, part);
-        else read16<D, 4, 0>(v, p, dst, part);
+        if (k_bits == 8) read16<N, D, 8, 0>(v, p, dst, stride, a.part);
+        else read16<N, D, 4, 0>(v, p, dst, stride, a.part);
     } else {
-        if (v_bits == 8) read16<D, 8, 1>(v, p, dst, part);
-        else read16<D, 4, 1>(v, p, dst, part);
+        if (v_bits == 8) read16<N, D, 8, 1>(v, p, dst, stride, a.part);
+        else read16<N, D, 4, 1>(v, p, dst, stride, a.part);
     }
 }
 
@@ -307,20 +370,32 @@ static int kv_rows_check(const nvfp4_kv_cache *c, int dtype, const void *p, int6
     return aligned(p, 16) && stride * size % 16 == 0 ? NVFP4_OK : NVFP4_EALIGN;
 }
 
-template <bool APPEND, int D, class T>
-static int kv_launch(const nvfp4_kv_cache *c, const KvView &v, void *k, int64_t k_stride, void *x, int64_t v_stride,
-                     hipStream_t stream) {
-    const int64_t groups = ceil_div(int64_t(v.tokens) * c->heads * (D / 16), 256);
+template <bool APPEND, int N, int D, class T>
+static int kv_launch_rows(const nvfp4_kv_cache *c, const KvView &v, void *k, int64_t k_stride, void *x, int64_t v_stride,
+                          hipStream_t stream) {
+    const int64_t groups = ceil_div(ceil_div(v.tokens, N) * c->heads * (D / 16), 256);
     if (groups >= kMaxGrid / 256) return NVFP4_ESHAPE;
     const unsigned g = unsigned(groups);
     const int kb = c->k_format == NVFP4_KV_MXFP8 ? 8 : 4, vb = c->v_format == NVFP4_KV_MXFP8 ? 8 : 4;
     if (APPEND)
-        kv_append_kernel<D, T><<<dim3(g, 2), 256, 0, stream>>>(v, kb, vb, static_cast<const T *>(k), k_stride,
-                                                               static_cast<const T *>(x), v_stride);
+        kv_append_kernel<N, D, T><<<dim3(g, 2), 256, 0, stream>>>(v, kb, vb, static_cast<const T *>(k), k_stride,
+                                                                  static_cast<const T *>(x), v_stride);
     else
-        kv_read_kernel<D, T><<<dim3(g, 2), 256, 0, stream>>>(v, kb, vb, static_cast<T *>(k), k_stride,
-                                                             static_cast<T *>(x), v_stride);
+        kv_read_kernel<N, D, T><<<dim3(g, 2), 256, 0, stream>>>(v, kb, vb, static_cast<T *>(k), k_stride,
+                                                                static_cast<T *>(x), v_stride);
     return launch_status();
+}
+
+template <bool APPEND, int D, class T>
+static int kv_launch(const nvfp4_kv_cache *c, const KvView &v, void *k, int64_t k_stride, void *x, int64_t v_stride,
+                     hipStream_t stream) {
+    // A thread reads two token rows where the card is full all the same (65521 tokens:
+    // 91.7 us, one row 95.2, four 91.5; 1500 tokens of 4 heads of 256: 9.3, 9.9, 10.0);
+    // for append one is as good (16384 tokens 64.6 us, two 62.8; 2048 tokens 12.6, 13.2).
+    constexpr int64_t kFill = 1 << 17;
+    if (!APPEND && int64_t(v.tokens) * c->heads * (D / 16) >= kFill)
+        return kv_launch_rows<APPEND, APPEND ? 1 : 2, D, T>(c, v, k, k_stride, x, v_stride, stream);
+    return kv_launch_rows<APPEND, 1, D, T>(c, v, k, k_stride, x, v_stride, stream);
 }
 
 template <bool APPEND>
