@@ -11,8 +11,8 @@
 // one multiplies (the values of tile i - 1 by its weights, then the keys of tile i by
 // its queries), the other takes tile i's softmax and decodes its share of the tiles
 // to come, so that the matrix and the vector pipe of a SIMD both stay busy.  Keys are
-// decoded two tiles ahead, values one, into rings of three, codes loaded one
-// tile before that.
+// decoded two tiles ahead, values one, into rings of two, between the matrix
+// instructions; codes are loaded one tile before that.
 //
 // At D <= 128 a wave owns 32 rows.  At D = 256 two waves own 32 rows together,
 // each half the elements: they add their halves of the scores through shared
