@@ -76,7 +76,10 @@ static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int 
         // the parts' way out and back at 4 TB/s and the join's launch.
         const int rows = p.cut[1].rows;
         p.tiles[1] = b->tokens * group / rows + b->seqs;
-        const int64_t keys = span(rows), tiles = ceil_div(b->tokens * group, rows) * c->heads;
+        // tiles of the sequences, each with a last one that is half full on average
+        const bool even = b->tokens == int64_t(b->seqs) * b->max_new;
+        const int64_t keys = span(rows);
+        const int64_t tiles = c->heads * (even ? b->seqs * ceil_div(most, rows) : ceil_div(b->tokens * group, rows) + b->seqs / 2);
         double best = 0;
         int64_t each = keys;
         for (int n = 1; n <= 16; ++n) {
