@@ -51,6 +51,7 @@ struct AttnArgs {
     int window;
     float scale_log2;      // scale * log2(e)
     int narrow_rows;       // sequences of at most so many rows (new tokens x group) are the narrow kernel's
+    bool reused;           // whether several tiles read a sequence's keys
     AttnCut cut[2];        // the narrow kernel's, the wide kernel's
     RowInfo *info;         // [tokens * q_heads]; NULL where no tile is split
     int part_rows;

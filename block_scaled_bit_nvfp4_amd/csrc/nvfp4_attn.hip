@@ -8,7 +8,8 @@
 
 namespace nvfp4 {
 
-// Sequences of at most so many rows (new tokens x group) go to the narrow kernel.
+// Sequences of at most so many rows (new tokens x group) go to the narrow kernel,
+// whatever the others need.
 constexpr int kNarrowMost = 64;
 constexpr int kCus = 256;
 
@@ -30,69 +31,100 @@ static void cut_keys(AttnCut &c, int64_t span, int64_t keys, bool window, int mo
     c.splits = int(ceil_div(span, keys));
 }
 
-static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads, int window) {
+// us that the parts of n splits take on their way out and back (at 4 TB/s), and
+// the join's launch.
+static double parts_us(const nvfp4_kv_batch *b, int q_heads, int dim, int64_t n) {
+    return n == 1 ? 0 : 4 + double(b->tokens) * q_heads * dim * 4 * 2 * n / 4e6;
+}
+
+// The narrow kernel's cut for `tiles` tile indexes; returns the us that it should take.
+static double cut_narrow(AttnCut &c, const nvfp4_kv_batch *b, int q_heads, int heads, int dim, int64_t tiles, int64_t keys,
+                         bool window, int most_splits) {
+    // Workgroups to aim at: two for each CU where one sequence is split (more
+    // cost the join more than they gain: 131008 keys 51 us, with twice as many 56),
+    // up to twelve where several sequences of unknown lengths balance each
+    // other (64 ragged sequences: 85.5 us at six for each CU, 84.3 at twelve).
+    const int64_t items = tiles * heads, target = 2 * kCus * std::min(b->seqs, 6);
+    // No split of fewer keys than a workgroup's start and the join are worth, which
+    // grows with the items that fill the card by themselves (900 keys: one
+    // sequence 10.0 us in splits of 256, 11.7 whole; 8 sequences 12.6, 12.0 in splits
+    // of 512; 64 sequences 33.5, 26.8 whole); up to 512 keys (8.4 us whole, 9.4
+    // split) nothing is split.
+    int64_t least = items >= 256 ? 1024 : items >= 64 ? 512 : 256;
+    if (keys <= 512) least = std::max(least, keys + 63);
+    cut_keys(c, keys, std::max(ceil_div(keys, ceil_div(target, items)), least), window, most_splits);
+    // Launch 6 us; then whichever is longer: all SIMDs' tiles of 16 rows and 32 keys
+    // with the workgroups' starts, or one workgroup's walk (measured at 64, 128, 256).
+    const double per_tile = 0.15 + 0.0035 * dim, per_step = 0.6 + 0.005 * dim;
+    const int64_t groups = items * c.splits, at_once = kCus * (dim == 256 ? 2 : dim == 128 ? 3 : 4);
+    const double all = 4.0 * double(groups) / double(at_once) + per_tile * double(items) * double(keys) / 32 / (4 * kCus);
+    const double one = 4 + per_step * double(std::min<int64_t>(c.keys, keys)) / 128;
+    return 6 + std::max(all, one) + parts_us(b, q_heads, dim, c.splits);
+}
+
+// The wide kernel's cut, the same way: the number of splits that should take the
+// least time, a CU taking one workgroup at a time.
+static double cut_wide(AttnCut &c, const nvfp4_kv_batch *b, int q_heads, int dim, int64_t tiles, int64_t keys, bool window,
+                       int most_splits) {
+    const double per_tile = dim == 64 ? 2.5 : dim == 128 ? 1.75 : 1.25;       // us of 8192 / dim keys
+    double best = 0;
+    int64_t each = keys;
+    for (int n = 1; n <= kMaxSplits / 2; n += std::max(1, n / 4)) {
+        const int64_t of = ceil_div(ceil_div(keys, n), 128) * 128;
+        if (n > 1 && of < 32768 / dim) break;
+        const double cost = double(ceil_div(tiles * n, kCus)) * (double(of) * dim / 8192 * per_tile + 5) + parts_us(b, q_heads, dim, n);
+        if (n == 1 || cost < best) {
+            best = cost;
+            each = of;
+        }
+    }
+    cut_keys(c, keys, each, window, most_splits);
+    return 5 + best;
+}
+
+static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int q_heads, int window, int64_t most_parts) {
     const int group = q_heads / c->heads, dim = c->head_dim;
     // A caller asks for the workspace without saying the window: with one, no more
-    // splits than without.
+    // splits, and no more parts, than without.
     int most_splits[2] = {kMaxSplits, kMaxSplits};
     if (window > 0) {
-        const AttnPlan without = attn_plan(c, b, q_heads, 0);
-        for (int cls = 0; cls < 2; ++cls) most_splits[cls] = without.cut[cls].splits;
+        const AttnPlan without = attn_plan(c, b, q_heads, 0, INT_MAX);
+        for (int cls = 0; cls < 2; ++cls)
+            if (without.tiles[cls] > 0) most_splits[cls] = without.cut[cls].splits;
+        most_parts = without.part_rows;
     }
     const int64_t most = int64_t(std::max(b->max_new, 1)) * group;
     AttnPlan p = {};
-    const bool wide = most > kNarrowMost;
-    const bool narrow = !wide || b->tokens < int64_t(b->seqs) * b->max_new;     // all the same length otherwise
-    p.narrow_rows = !wide ? INT_MAX : narrow ? kNarrowMost : -1;
     // a tile sees its window and its own tokens
     const auto span = [&](int rows) {
         const int64_t context = std::max(b->max_context, 1);
         return window > 0 ? std::min<int64_t>(context, int64_t(window) + rows / group + 1) : context;
     };
+    const bool even = b->tokens == int64_t(b->seqs) * b->max_new;         // all of the same length
     p.cut[0] = AttnCut{kNarrowRows, 128, 1, 0, 0};
-    if (narrow) {
-        // Workgroups to aim at: two for each CU where one sequence is split (more
-        // cost the join more than they gain: 131008 keys 51 us, with twice as many 56),
-        // up to twelve where several sequences of unknown lengths balance each
-        // other (64 ragged sequences: 85.5 us at six for each CU, 84.3 at twelve).
-        p.cut[0].tiles_per_seq = wide ? kNarrowMost / kNarrowRows : 0;
-        p.tiles[0] = wide ? int64_t(b->seqs) * p.cut[0].tiles_per_seq : b->tokens * group / kNarrowRows + b->seqs;
-        const int64_t items = p.tiles[0] * c->heads, target = 2 * kCus * std::min(b->seqs, 6);
-        const int64_t keys = span(kNarrowRows);
-        // No split of fewer keys than a workgroup's start and the join are worth, which
-        // grows with the items that fill the card by themselves (900 keys: one
-        // sequence 10.0 us in splits of 256, 11.7 whole; 8 sequences 12.6, 12.0 in splits
-        // of 512; 64 sequences 33.5, 26.8 whole); up to 512 keys (8.4 us whole, 9.4
-        // split) nothing is split.
-        int64_t least = items >= 256 ? 1024 : items >= 64 ? 512 : 256;
-        if (keys <= 512) least = std::max(least, keys + 63);
-        cut_keys(p.cut[0], keys, std::max(ceil_div(keys, ceil_div(target, items)), least), window > 0, most_splits[0]);
-    }
     p.cut[1] = AttnCut{wide_rows(dim), 128, 1, 0, 0};
+    // All by the narrow kernel, or the long sequences by the wide one.
+    const int64_t all_narrow = b->tokens * group / kNarrowRows + b->seqs;
+    const double narrow_us = cut_narrow(p.cut[0], b, q_heads, c->heads, dim, all_narrow, span(kNarrowRows), window > 0, most_splits[0]);
+    bool wide = most > kNarrowMost;
     if (wide) {
-        // The number of splits that should take the least time, a CU taking one
-        // workgroup at a time: about 1.8 us for each tile of 8192 / dim keys
-        // (2.5 at 64), 5 us for a workgroup's start and end, and for split tiles
-        // the parts' way out and back at 4 TB/s and the join's launch.
-        const int rows = p.cut[1].rows;
-        p.tiles[1] = b->tokens * group / rows + b->seqs;
         // tiles of the sequences, each with a last one that is half full on average
-        const bool even = b->tokens == int64_t(b->seqs) * b->max_new;
-        const int64_t keys = span(rows);
+        const int rows = p.cut[1].rows;
         const int64_t tiles = c->heads * (even ? b->seqs * ceil_div(most, rows) : ceil_div(b->tokens * group, rows) + b->seqs / 2);
-        double best = 0;
-        int64_t each = keys;
-        for (int n = 1; n <= 16; ++n) {
-            const int64_t of = ceil_div(ceil_div(keys, n), 128) * 128;
-            if (n > 1 && of < 32768 / dim) break;
-            const double parts = n == 1 ? 0 : 4 + double(b->tokens) * q_heads * dim * 4 * 2 * n / 4e6;
-            const double cost = double(ceil_div(tiles * n, kCus)) * (double(of) * dim / 8192 * (dim == 64 ? 2.5 : 1.8) + 5) + parts;
-            if (n == 1 || cost < best) {
-                best = cost;
-                each = of;
-            }
+        wide = cut_wide(p.cut[1], b, q_heads, dim, tiles, span(rows), window > 0, most_splits[1]) < narrow_us;
+    }
+    p.narrow_rows = !wide ? INT_MAX : even ? -1 : kNarrowMost;
+    if (!wide) {
+        p.tiles[0] = all_narrow;
+        p.cut[1].splits = 1;
+    } else {
+        p.tiles[1] = b->tokens * group / p.cut[1].rows + b->seqs;
+        p.cut[0].splits = 1;
+        if (!even) {
+            p.cut[0].tiles_per_seq = kNarrowMost / kNarrowRows;
+            p.tiles[0] = int64_t(b->seqs) * p.cut[0].tiles_per_seq;
+            cut_narrow(p.cut[0], b, q_heads, c->heads, dim, p.tiles[0], span(kNarrowRows), window > 0, most_splits[0]);
         }
-        cut_keys(p.cut[1], keys, each, window > 0, most_splits[1]);
     }
     int64_t rows = 0;
     for (int cls = 0; cls < 2; ++cls) {
@@ -100,7 +132,7 @@ static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int 
         k.first_row = int(rows);
         if (p.tiles[cls] == 0 || k.splits == 1) continue;
         const int64_t more = p.tiles[cls] * c->heads * k.splits * k.rows;
-        if (rows + more > INT_MAX) {           // part rows are 32-bit: whole tiles then
+        if (rows + more > most_parts) {        // part rows are 32-bit: whole tiles then
             k.splits = 1;
             continue;
         }
@@ -134,7 +166,7 @@ NVFP4_API size_t nvfp4_kv_attention_workspace_bytes(const nvfp4_kv_cache *cache,
                                                     int q_heads) {
     KvView v;
     if (attn_check(cache, batch, q_heads, v) != NVFP4_OK) return 0;
-    return plan_bytes(attn_plan(cache, batch, q_heads, 0), batch, q_heads, cache->head_dim);
+    return plan_bytes(attn_plan(cache, batch, q_heads, 0, INT_MAX), batch, q_heads, cache->head_dim);
 }
 
 NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, const uint16_t *q,
@@ -152,7 +184,7 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
         (tree && !aligned(tree, 8)))
         return NVFP4_EALIGN;
     if (batch->tokens == 0) return NVFP4_OK;
-    const AttnPlan plan = attn_plan(cache, batch, q_heads, window);
+    const AttnPlan plan = attn_plan(cache, batch, q_heads, window, INT_MAX);
     const size_t need = plan_bytes(plan, batch, q_heads, cache->head_dim);
     if (need > 0) {
         if (!workspace || workspace_bytes < need) return NVFP4_EWORKSPACE;
@@ -169,6 +201,7 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
     a.window = window;
     a.scale_log2 = scale * kLog2e;
     a.narrow_rows = plan.narrow_rows;
+    a.reused = batch->max_new > kNarrowRows / a.group;
     a.cut[0] = plan.cut[0];
     a.cut[1] = plan.cut[1];
     const int dim = cache->head_dim;

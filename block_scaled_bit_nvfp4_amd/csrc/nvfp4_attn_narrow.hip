@@ -61,8 +61,9 @@ struct NarrowTile {
     }
 };
 
-// One side's codes of two units to shared memory, 16 bytes a lane.
-template <int UNIT>
+// One side's codes of two units to shared memory, 16 bytes a lane.  STREAM: for codes
+// that nobody reads again.
+template <int UNIT, int STREAM>
 __device__ __forceinline__ void send_units(const uint8_t *codes, int64_t unit0, int64_t unit1, uint8_t *to) {
     const int lane = threadIdx.x & 63;
 #pragma unroll
@@ -70,7 +71,7 @@ __device__ __forceinline__ void send_units(const uint8_t *codes, int64_t unit0, 
         const int u = UNIT >= kLanes * 16 ? n / UNIT : lane * 16 / UNIT;
         const int at = UNIT >= kLanes * 16 ? n % UNIT + lane * 16 : lane * 16 % UNIT;
         const uint8_t *from = codes + (u == 0 ? unit0 : unit1) * UNIT + at;
-        __builtin_amdgcn_global_load_lds((GlobalBytes *)from, (LdsBytes *)(to + n), 16, 0, kStream);
+        __builtin_amdgcn_global_load_lds((GlobalBytes *)from, (LdsBytes *)(to + n), 16, 0, STREAM);
     }
 }
 
@@ -120,8 +121,16 @@ __global__ void __launch_bounds__(kNarrowThreads, (NarrowShape<D, KB, VB>::kPerS
             has |= (page >= 0) << u;
             unit[u] = kv.unit_of(max(page, 0), head, pos);
         }
-        send_units<KS::kUnitCodes>(kv.codes[0], unit[0], unit[1], mine);
-        send_units<VS::kUnitCodes>(kv.codes[1], unit[0], unit[1], mine + W::kValuesAt);
+        // Codes that one tile reads go past the caches (64 sequences of 8192 keys 146 us,
+        // through them 168); those that the tiles of a chunk share do not (64 tokens
+        // over 4064 keys, heads of 256: 42 us, past them 52).
+        if (a.reused) {
+            send_units<KS::kUnitCodes, 0>(kv.codes[0], unit[0], unit[1], mine);
+            send_units<VS::kUnitCodes, 0>(kv.codes[1], unit[0], unit[1], mine + W::kValuesAt);
+        } else {
+            send_units<KS::kUnitCodes, kStream>(kv.codes[0], unit[0], unit[1], mine);
+            send_units<VS::kUnitCodes, kStream>(kv.codes[1], unit[0], unit[1], mine + W::kValuesAt);
+        }
 #pragma unroll
         for (int n = 0; n < W::kScaleLoads; ++n)
             __builtin_amdgcn_global_load_lds((GlobalBytes *)(scale_of[n] + (second[n] ? unit[1] : unit[0]) * W::kScaleBytes),

@@ -9,6 +9,7 @@ import block_scaled_bit_nvfp4_amd as nv
 from oracle import kv as okv
 
 DEV = "cuda:0"
+shape = "exact"              # of a batch's host numbers, see test_gpu_kv_attention.py
 
 
 def lengths(new, past):

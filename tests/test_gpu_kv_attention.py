@@ -21,6 +21,14 @@ def _device():
     torch.cuda.synchronize()
 
 
+# The batch's host numbers only shape the launch: the same cases run with bounds that
+# are exact, with a context bound far above (the long splits of many rows), and among
+# many rows that no sequence has (whole tiles of the kernel for many rows).
+@pytest.fixture(params=["exact", "far", "spare"], autouse=True)
+def _shape(request, monkeypatch):
+    monkeypatch.setattr(K, "shape", request.param)
+
+
 def _run(rng, new, past, heads, group, dim, k_fmt=8, v_fmt=8, page=16, window=0, tree=None, pad=0, q_scale=1.5,
          edit=None, **bounds):
     table, keys, values = K.filled(rng, new, past, heads, dim, k_fmt, v_fmt, page)
@@ -29,19 +37,27 @@ def _run(rng, new, past, heads, group, dim, k_fmt=8, v_fmt=8, page=16, window=0,
     offsets, past = K.lengths(new, past)
     tokens, q_heads = int(offsets[-1]), heads * group
     wide = K.to_gpu(q_scale * rng.standard_normal((tokens, q_heads * dim + pad)), torch.bfloat16)
+    if K.shape == "far":
+        bounds = {"max_context": 100000, **bounds}
+    if K.shape == "spare":
+        wide = torch.cat([wide, wide.new_zeros(400000 // q_heads, wide.shape[1])])
+        bounds = {"tokens": wide.shape[0], **bounds}
     q = wide[:, :q_heads * dim].unflatten(1, (q_heads, dim))
     scale = dim ** -0.5
     cache, batch = K.cache_gpu(keys, values, page), K.batch_gpu(table, offsets, past, **bounds)
     kw = {"window": window}
     if tree is not None:
         words = [int(w) - (1 << 64) if int(w) >> 63 else int(w) for w in tree]
-        kw["tree"] = torch.tensor(words, dtype=torch.int64, device=K.DEV)
+        kw["tree"] = torch.tensor(words + [0] * (len(q) - tokens), dtype=torch.int64, device=K.DEV)
     out, lse = K.attend(cache, batch, q, scale, q_heads, **kw)
+    assert out[tokens:].isnan().all() and lse[tokens:].isnan().all()     # rows of no sequence are left alone
+    q, out, lse = q[:tokens], out[:tokens], lse[:tokens]
     ref = okv.attention(keys, values, table, offsets, past, q.double().cpu().numpy(), scale, window, tree)
     what = "new %s past %s heads %dx%d D %d formats %d/%d page %d window %d" % (
         list(new)[:6], list(past)[:6], heads, group, dim, k_fmt, v_fmt, page, window)
     K.check(out, lse, ref, dim, what)
-    again, lse2 = K.attend(cache, batch, q, scale, q_heads, **kw)
+    q = wide[:, :q_heads * dim].unflatten(1, (q_heads, dim))
+    again, lse2 = (t[:tokens] for t in K.attend(cache, batch, q, scale, q_heads, **kw))
     assert torch.equal(out.view(torch.int16), again.view(torch.int16)), what + ": another run, other bits"
     assert torch.equal(lse.view(torch.int32), lse2.view(torch.int32))
     return out, lse, ref
@@ -112,6 +128,15 @@ def test_long_context_is_split():
     _run(rng, new, past, 1, 5, 64, 8, 8, page=64, max_context=100000, max_new=64)
     rng = np.random.default_rng(12)
     _run(rng, new, past, 1, 5, 64, 8, 8, page=64, max_context=1, max_new=1)
+
+
+@pytest.mark.parametrize("dim,k_fmt,v_fmt", [(64, 8, 8), (128, 8, 4), (256, 4, 8)])
+def test_many_rows_in_splits(dim, k_fmt, v_fmt):
+    """A chunk whose keys several workgroups share, beside a short sequence and one
+    whose last split has a single key."""
+    G.note("attention of a chunk, split keys, D=%d" % dim)
+    rng = np.random.default_rng(dim)
+    _run(rng, [100, 3, 60], [2600, 900, 837], 1, 5, dim, k_fmt, v_fmt, page=64)
 
 
 @pytest.mark.parametrize("n", [1, 8, 40, 64])
