@@ -11,7 +11,7 @@
 // match, and the cache's value layout with it).
 #pragma once
 
-#include <mutex>
+#include <atomic>
 
 #include "nvfp4_kv.h"
 
@@ -232,19 +232,20 @@ __device__ __forceinline__ float lse_of(float m, float l) {
 
 int wide_rows(int dim);            // rows of the wide kernel's tile
 
-// Raises a kernel's limit of dynamic shared memory, once per device.
+// Raises a kernel's limit of dynamic shared memory, once per device (by several
+// threads at once, it may be twice).
 template <auto KERNEL>
 bool raise_lds(int bytes) {
     constexpr int kDevices = 64;
-    static std::once_flag once[kDevices];
-    static bool ok[kDevices];
+    static std::atomic<bool> done[kDevices];
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= kDevices) return false;
-    std::call_once(once[dev], [&] {
-        ok[dev] = hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
-                                      bytes) == hipSuccess;
-    });
-    return ok[dev];
+    if (done[dev].load(std::memory_order_acquire)) return true;
+    if (hipFuncSetAttribute(reinterpret_cast<const void *>(KERNEL), hipFuncAttributeMaxDynamicSharedMemorySize,
+                            bytes) != hipSuccess)
+        return false;
+    done[dev].store(true, std::memory_order_release);
+    return true;
 }
 
 // `tiles`: tile indexes.

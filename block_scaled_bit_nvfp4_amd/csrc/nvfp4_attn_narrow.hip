@@ -3,10 +3,19 @@
 //
 // A workgroup owns 16 rows and a range of keys; its waves take 32-key tiles in turn,
 // each with its own softmax state, and meet at the end.  The work is bound by the
-// cache's bytes, so the codes of a wave's next tile go to shared memory by
+// cache's bytes, so the codes and scales of a wave's next tile go to shared memory by
 // direct loads while it works on one: they take no registers, and three workgroups
 // of a CU keep 100 KB in flight.  A tile's codes are then read once, decoded in
-// registers straight to operands of v_mfma_f32_16x16x32_bf16.
+// registers straight to operands of v_mfma_f32_16x16x32_bf16; sixteen rows are
+// the least that instruction takes, so a group of one to sixteen query heads costs the
+// same.  A tile's 180 vector instructions take about 0.6 us of a SIMD, a third of the
+// time that its bytes take, so that the masks of edge tiles, the search for the
+// maximum and NaN have branches of their own.
+//
+// Measured: one token over 131008 keys of 8 heads of 128 (277 MB) 45 us, 6.2 TB/s,
+// and 5 us for the join; 64 tokens over 8192 keys each 146 us (5.8 TB/s), over 1 to
+// 8192 keys 84 us (4.4 TB/s: the last workgroups run alone); over 1037 keys of one
+// sequence 10 us, of which 7 are the two launches.
 #include "nvfp4_attn.h"
 
 namespace nvfp4 {

@@ -399,8 +399,9 @@ int nvfp4_kv_append(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, in
                     int64_t k_stride, const void *v, int64_t v_stride, hipStream_t stream);
 
 /* The values that the cache holds for the batch's tokens (positions past[s] ..),
- * to k and v laid out as nvfp4_kv_append's inputs; exact in either type.  Either
- * may be NULL, not both. */
+ * to k and v laid out as nvfp4_kv_append's inputs; exact in either type (in bf16
+ * down to its smallest subnormal).  Rows of no sequence are left alone.  Either may be
+ * NULL, not both. */
 int nvfp4_kv_read(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int dtype, void *k, int64_t k_stride,
                   void *v, int64_t v_stride, hipStream_t stream);
 
@@ -414,7 +415,8 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int 
  * positions before past[s] and past[s] + b for each set bit b of the token's
  * word -- the ancestors of a drafted token in a speculative verify.  A token with
  * nothing allowed gets zeros and lse = -infinity.  What stands in masked or
- * unwritten places, NaN too, does not reach the outputs.
+ * unwritten places, NaN too, does not reach the outputs.  Rows of no sequence are
+ * left alone.
  *   q   bf16 bits [tokens][q_heads][head_dim], q_stride elements between tokens;
  *   out bf16 bits, the same with out_stride;  lse fp32 [tokens][q_heads] or NULL.
  * q_heads is a multiple of heads, scale finite and > 0; q and out 16-byte
