@@ -46,11 +46,12 @@ static double cut_narrow(AttnCut &c, const nvfp4_kv_batch *b, int q_heads, int h
     // other (64 ragged sequences: 85.5 us at six for each CU, 84.3 at twelve).
     const int64_t items = tiles * heads, target = 2 * kCus * std::min(b->seqs, 6);
     // No split of fewer keys than a workgroup's start and the join are worth, which
-    // grows with the items that fill the card by themselves (900 keys: one
-    // sequence 10.0 us in splits of 256, 11.7 whole; 8 sequences 12.6, 12.0 in splits
-    // of 512; 64 sequences 33.5, 26.8 whole); up to 512 keys (8.4 us whole, 9.4
-    // split) nothing is split.
-    int64_t least = items >= 256 ? 1024 : items >= 64 ? 512 : 256;
+    // grows with the items that fill the card by themselves (one sequence of 1037
+    // keys: 9.6 us in splits of 128, 10.3 of 256, 11.9 whole; 900 keys: 8 sequences 12.0
+    // in splits of 512, 12.6 of 256; 64 sequences 33.5 of 256, 26.8 whole; past 4096
+    // keys splits of 128 would be too many: 8001 keys 13.6, of 256 11.8); up to 512
+    // keys (8.4 us whole, 9.4 split) nothing is split.
+    int64_t least = items >= 256 ? 1024 : items >= 64 ? 512 : keys <= 4096 ? 128 : 256;
     if (keys <= 512) least = std::max(least, keys + 63);
     cut_keys(c, keys, std::max(ceil_div(keys, ceil_div(target, items)), least), window, most_splits);
     // Launch 6 us; then whichever is longer: all SIMDs' tiles of 16 rows and 32 keys
@@ -139,7 +140,9 @@ static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int 
         rows += more;
     }
     p.part_rows = rows;
-    p.many = !wide && p.cut[0].splits > 12;    // among many rows few are in many splits
+    // a workgroup for a row from seven splits on (12 splits: 10.3 us, a thread for four
+    // elements 12.7; 5 splits: the same); among many rows few are in many splits
+    p.many = !wide && p.cut[0].splits > 6;
     return p;
 }
 

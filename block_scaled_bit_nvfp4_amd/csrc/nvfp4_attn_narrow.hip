@@ -15,7 +15,7 @@
 // Measured: one token over 131008 keys of 8 heads of 128 (277 MB) 45 us, 6.2 TB/s,
 // and 5 us for the join; 64 tokens over 8192 keys each 146 us (5.8 TB/s), over 1 to
 // 8192 keys 84 us (4.4 TB/s: the last workgroups run alone); over 1037 keys of one
-// sequence 10 us, of which 7 are the two launches.
+// sequence 9.6 us, of which 7 are the two launches.
 #include "nvfp4_attn.h"
 
 namespace nvfp4 {
