@@ -155,12 +155,11 @@ __device__ __forceinline__ float unit_of_byte(uint32_t w, int i) {
     return __uint_as_float(__builtin_amdgcn_ubfe(w, 8 * i, 8) << 23);
 }
 
-// A load of BYTES per lane into words; STREAM: of bytes that nobody reads again.
-template <int BYTES, bool STREAM = false>
+// A load of BYTES per lane into words.
+template <int BYTES>
 __device__ __forceinline__ void load_words(const uint8_t *p, uint32_t *w) {
     if constexpr (BYTES == 16) {
-        const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
-        const u32x4 t = STREAM ? __builtin_nontemporal_load(q) : *q;
+        const u32x4 t = *reinterpret_cast<const u32x4 *>(p);
         w[0] = t[0]; w[1] = t[1]; w[2] = t[2]; w[3] = t[3];
     } else if constexpr (BYTES == 8) {
         const u32x2 t = *reinterpret_cast<const u32x2 *>(p);

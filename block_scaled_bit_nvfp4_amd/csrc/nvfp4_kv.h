@@ -60,16 +60,13 @@ struct KvView {
         end = min(max(offsets[s + 1], begin), tokens);
         before = min(max(past[s], 0), capacity);
     }
-    // The page of sequence s's position `pos`, or -1 where the table has none.
-    __device__ __forceinline__ int page_of(int s, int pos) const {
-        return page_in(entry_at(s, pos), pos);
-    }
-    // The same in two steps, for loads ahead of their use: the table's entry (any
-    // one where `pos` is past the table), then the page.
+    // The page of sequence s's position `pos` in two steps, for loads ahead of their
+    // use: the table's entry (any one where `pos` is past the table), then the page, or
+    // -1 where there is none.
     __device__ __forceinline__ int entry_at(int s, int pos) const {
         return table[int64_t(s) * width + (min(max(pos, 0), capacity - 1) >> page_shift)];
     }
-    // The same as a scalar load, for `s` and `pos` that are the same in the whole wave.
+    // The entry as a scalar load, for `s` and `pos` that are the same in the whole wave.
     __device__ __forceinline__ int entry_at_scalar(int s, int pos) const {
         const int at = __builtin_amdgcn_readfirstlane(min(max(pos, 0), capacity - 1) >> page_shift);
         typedef __attribute__((address_space(4))) const int32_t Constant;
