@@ -386,7 +386,7 @@ class KvCache:
                  ("v_codes", v_codes, _U8, nvfp4_kv_code_bytes(v_format, *shape), False),
                  ("v_scales", v_scales, _U8, nvfp4_kv_scale_bytes(v_format, *shape), False))
         self.planes = (k_codes, k_scales, v_codes, v_scales)
-        self.device = k_codes.device
+        self.device, self._index = k_codes.device, k_codes.get_device()
         self.pages, self.page_tokens, self.heads, self.head_dim = shape
         self.k_format, self.v_format = int(k_format), int(v_format)
         self._c = _KvCache(*[t.data_ptr() for t in self.planes], self.k_format, self.v_format, *shape)
@@ -406,7 +406,7 @@ class KvBatch:
         _checked(("page_table", page_table, _I32, 4, False), ("offsets", offsets, _I32, 4 * (seqs + 1), False),
                  ("past", past, _I32, 4 * seqs, False))
         self.arrays = (page_table, offsets, past)
-        self.device = page_table.device
+        self.device, self._index = page_table.device, page_table.get_device()
         self.tokens, self.max_new, self.max_context = int(tokens), int(max_new), int(max_context)
         self._c = _KvBatch(*[t.data_ptr() for t in self.arrays], self.tokens, seqs, width, self.max_new,
                            self.max_context)
@@ -432,16 +432,21 @@ def _rows(name, t, cache, batch, heads, dtypes):
         raise TypeError("%s: expected a torch.Tensor, got %r" % (name, type(t)))
     if t.dtype not in dtypes:
         raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
-    dim = cache.head_dim
-    tokens = batch.tokens
+    dim, tokens = cache.head_dim, batch.tokens
     if t.shape != (tokens, heads, dim):
         raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), (tokens, heads, dim)))
     token, head, element = t.stride()
     if tokens and (element != 1 or (heads > 1 and head != dim)):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    if t.device != cache.device:
+    if t.get_device() != cache._index:
         raise ValueError("%s is on %s, the cache on %s" % (name, t.device, cache.device))
     return token if tokens > 1 else heads * dim
+
+
+def _flat(name, t, cache, dtype, n):
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_contiguous() and t.numel() >= n and
+            t.get_device() == cache._index):
+        raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (name, dtype, n, cache.device))
 
 
 # torch's getter of the current stream's handle; its public one builds an object
@@ -449,16 +454,16 @@ def _rows(name, t, cache, batch, heads, dtypes):
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _kv_stream(stream, t):
-    if stream is None and _raw_stream is not None and t.is_cuda:
-        return _raw_stream(t.get_device())
-    return _stream(stream, t)
+def _kv_stream(stream, cache):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(cache._index)
+    return _stream(stream, *cache.planes)
 
 
 def _kv_pair(cache, batch):
     if not isinstance(cache, KvCache) or not isinstance(batch, KvBatch):
         raise TypeError("expected a KvCache and a KvBatch")
-    if cache.device != batch.device:
+    if cache._index != batch._index:
         raise ValueError("the batch is on %s, the cache on %s" % (batch.device, cache.device))
 
 
@@ -467,20 +472,21 @@ def nvfp4_kv_append(cache, batch, K, V, stream=None):
     ks = _rows("K", K, cache, batch, cache.heads, _KV_DTYPE)
     vs = _rows("V", V, cache, batch, cache.heads, (K.dtype,))
     _check(load().nvfp4_kv_append(cache._ref, batch._ref, _KV_DTYPE[K.dtype], K.data_ptr(), ks, V.data_ptr(), vs,
-                                  _kv_stream(stream, K)), "nvfp4_kv_append")
+                                  _kv_stream(stream, cache)), "nvfp4_kv_append")
 
 
 def nvfp4_kv_read(cache, batch, K=None, V=None, stream=None):
     _kv_pair(cache, batch)
-    given = [t for t in (K, V) if t is not None]
-    if not given:
+    if K is None and V is None:
         raise ValueError("K or V is required")
-    ks, vs = (0 if t is None else _rows(n, t, cache, batch, cache.heads, _KV_DTYPE) for n, t in (("K", K), ("V", V)))
-    if given[0].dtype != given[-1].dtype:
-        raise ValueError("K is %s, V %s" % (K.dtype, V.dtype))
-    _check(load().nvfp4_kv_read(cache._ref, batch._ref, _KV_DTYPE[given[0].dtype],
+    ks = 0 if K is None else _rows("K", K, cache, batch, cache.heads, _KV_DTYPE)
+    vs = 0 if V is None else _rows("V", V, cache, batch, cache.heads, _KV_DTYPE)
+    dtype = V.dtype if K is None else K.dtype
+    if V is not None and V.dtype != dtype:
+        raise ValueError("K is %s, V %s" % (dtype, V.dtype))
+    _check(load().nvfp4_kv_read(cache._ref, batch._ref, _KV_DTYPE[dtype],
                                 None if K is None else K.data_ptr(), ks, None if V is None else V.data_ptr(), vs,
-                                _kv_stream(stream, given[0])), "nvfp4_kv_read")
+                                _kv_stream(stream, cache)), "nvfp4_kv_read")
 
 
 def nvfp4_kv_attention_workspace_bytes(cache, batch, q_heads) -> int:
@@ -496,17 +502,17 @@ def nvfp4_kv_attention(cache, batch, Q, scale, out, lse=None, window=0, tree=Non
     heads = Q.shape[1] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else 0
     qs = _rows("Q", Q, cache, batch, heads, _BF16[:1])
     os_ = _rows("out", out, cache, batch, heads, _BF16[:1])
-    for name, t, dtype, n in (("lse", lse, torch.float32, batch.tokens * heads), ("tree", tree, torch.int64, batch.tokens)):
-        if t is not None and not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.is_contiguous() and
-                                  t.numel() >= n and t.device == cache.device):
-            raise ValueError("%s must be a contiguous %s tensor of %d elements on %s" % (name, dtype, n, cache.device))
+    if lse is not None:
+        _flat("lse", lse, cache, torch.float32, batch.tokens * heads)
+    if tree is not None:
+        _flat("tree", tree, cache, torch.int64, batch.tokens)
     nbytes = 0
     if workspace is not None:
-        if not workspace.is_contiguous() or workspace.device != cache.device:
+        if not workspace.is_contiguous() or workspace.get_device() != cache._index:
             raise ValueError("workspace must be contiguous, on %s" % cache.device)
         nbytes = workspace.numel() * workspace.element_size()
     _check(load().nvfp4_kv_attention(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale), int(window),
                                      None if tree is None else tree.data_ptr(), out.data_ptr(), os_,
                                      None if lse is None else lse.data_ptr(),
-                                     workspace.data_ptr() if nbytes else None, nbytes, _kv_stream(stream, Q)),
+                                     workspace.data_ptr() if nbytes else None, nbytes, _kv_stream(stream, cache)),
            "nvfp4_kv_attention")
