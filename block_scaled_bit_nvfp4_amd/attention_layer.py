@@ -48,6 +48,7 @@ class AttentionLayer:
         self.q, self.o = buffer(q_heads * head_dim, torch.bfloat16), buffer(q_heads * head_dim, torch.bfloat16)
         self.y = buffer(self.hidden, torch.float32)
         self.workspace = torch.empty(0, dtype=torch.uint8, device=self.device)
+        self.retired = []            # outgrown workspaces, see reserve
 
     def _weights(self, w):
         R, K = w.shape
@@ -59,10 +60,16 @@ class AttentionLayer:
         return wq, ws, 1.0, R, K
 
     def reserve(self, batch):
-        """Room for the split attention of `batch`; before a capture, for its batch."""
+        """Room for the split attention of `batch`; before a capture, for its batch.  A
+        captured step keeps writing to the workspace that it was captured with, so one
+        that is outgrown stays the layer's own; each is at least twice the one
+        before, so that all of them together take less than twice the last."""
         need = nv.nvfp4_kv_attention_workspace_bytes(self.cache, batch, self.q_heads)
-        if need > self.workspace.numel():
-            self.workspace = torch.empty(need, dtype=torch.uint8, device=self.device)
+        have = self.workspace.numel()
+        if need > have:
+            if have:
+                self.retired.append(self.workspace)
+            self.workspace = torch.empty(max(need, 2 * have), dtype=torch.uint8, device=self.device)
 
     def step(self, x, batch, window=0, tree=None):
         """x bfloat16 [tokens, hidden], the batch's new tokens in its order; the
