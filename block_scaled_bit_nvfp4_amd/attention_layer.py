@@ -18,6 +18,8 @@ of seven drafted tokens, and prints what each took.
 """
 from __future__ import annotations
 
+import math
+
 import torch
 
 import block_scaled_bit_nvfp4_amd as nv
@@ -51,13 +53,19 @@ class AttentionLayer:
         self.retired = []            # outgrown workspaces, see reserve
 
     def _weights(self, w):
+        """Planes and tensor scale of a matrix: the scale puts the largest block's at
+        E4M3's largest, 448, so that the others' are normal numbers down to 2^-14 of it."""
         R, K = w.shape
+        largest = float(w.abs().amax())
+        if not math.isfinite(largest):
+            raise ValueError("weights must be finite")
+        tscale = max(largest / (6 * 448), 2.0 ** -126) if largest else 1.0
         codes = torch.empty(R, K // 2, dtype=torch.uint8, device=self.device)
         scales = torch.empty(R, K // 16, dtype=torch.uint8, device=self.device)
-        nv.nvfp4_quantize(w.contiguous(), R, K, 1.0, codes, scales)
+        nv.nvfp4_quantize(w.contiguous(), R, K, tscale, codes, scales)
         wq, ws = nv.alloc_repacked(R, K, self.device)
         nv.nvfp4_repack(codes, scales, R, K, wq, ws)
-        return wq, ws, 1.0, R, K
+        return wq, ws, tscale, R, K
 
     def reserve(self, batch):
         """Room for the split attention of `batch`; before a capture, for its batch.  A

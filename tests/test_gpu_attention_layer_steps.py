@@ -5,7 +5,9 @@ import pytest
 import torch
 
 import block_scaled_bit_nvfp4_amd as nv
+from block_scaled_bit_nvfp4_amd.attention_layer import AttentionLayer
 from tests import _gpu as G
+from tests import _kv as K
 from tests import test_gpu_attention_layer as L
 
 pytestmark = pytest.mark.gpu
@@ -63,3 +65,40 @@ def test_captured_decode_survives_larger_steps():
             assert (b == 0x55).all()
         outs.append(torch.cat(got).cpu())
     assert torch.equal(*outs) and outs[0].isfinite().all()
+
+
+@pytest.mark.parametrize("std", [1e4, 0.06, 0.01, 0.002, 1e-5])
+def test_weights_of_any_size_are_held(std):
+    """Each weight within the E2M1 code's half step of its block: a block's unit is its
+    largest magnitude over 6, rounded to E4M3 (at most 2^-4 of it, while the scales are
+    normal numbers), and the widest gap between codes is two units.  A scale for each
+    matrix keeps the block scales in E4M3's range whatever the weights' size."""
+    G.note("attention layer, weights of %g" % std)
+    gen = torch.Generator(G.DEV).manual_seed(7)
+    weights = [torch.randn(r, c, generator=gen, device=G.DEV) * s
+               for r, c, s in (((L.Q_HEADS + 2 * L.HEADS) * L.DIM, L.HIDDEN, std), (L.HIDDEN, L.Q_HEADS * L.DIM, 0.1 * std))]
+    layer = AttentionLayer(*weights, L.Q_HEADS, L.HEADS, L.DIM, 8, L.PAGES, L.PAGE)
+    for w, planes in zip(weights, (layer.wqkv, layer.wo)):
+        held = torch.empty_like(w)
+        nv.nvfp4_dequant(*planes, out_f32=held)
+        largest = w.double().abs().unflatten(1, (-1, 16)).amax(-1, keepdim=True)
+        off = (w.double() - held.double()).abs().unflatten(1, (-1, 16))
+        bad = int((off > (1 + 2.0 ** -4) / 6 * largest * (1 + 2.0 ** -20)).sum())
+        assert bad == 0, "%d of %d weights are off" % (bad, off.numel())
+
+
+def test_weights_without_a_scale():
+    """Zeros stay zeros, weights at the bottom of float32's range are no error, and
+    what is not finite is refused."""
+    G.note("attention layer, weights without a scale")
+    shape = (L.Q_HEADS + 2 * L.HEADS) * L.DIM, L.HIDDEN
+    wo = torch.zeros(L.HIDDEN, L.Q_HEADS * L.DIM, device=G.DEV)
+    batch = K.batch_gpu(np.arange(L.PAGES).reshape(1, -1), np.array([0, 3]), np.array([0]))
+    for w in (torch.zeros(shape, device=G.DEV), torch.full(shape, 2.0 ** -149, device=G.DEV)):
+        layer = AttentionLayer(w, wo, L.Q_HEADS, L.HEADS, L.DIM, 8, L.PAGES, L.PAGE)
+        assert (layer.step(L._inputs(3, 1), batch) == 0).all()
+    for bad in (float("inf"), float("nan")):
+        w = torch.zeros(shape, device=G.DEV)
+        w[3, 5] = bad
+        with pytest.raises(ValueError):
+            AttentionLayer(w, wo, L.Q_HEADS, L.HEADS, L.DIM, 8, L.PAGES, L.PAGE)
