@@ -224,9 +224,16 @@ __device__ __forceinline__ float piece_weight(float mz, float m) {
     return mz == kNegInf ? (m == kNegInf ? 1.0f : 0.0f) : exp2_fast(mz - m);
 }
 
+// What a row that has no maximum yet adds to its sum in a tile where it sees keys:
+// their scores are all minus infinity (an infinite query) or NaN.  A row that sees
+// nothing keeps a sum of zero, and zeros are its output; such a one divides zeros by a
+// sum of zero weights and is NaN.  A maximum found later clears the mark.
+__device__ __forceinline__ float no_maximum(float m, bool sees) { return m == kNegInf && sees ? 1.0f : 0.0f; }
+
 // log(sum of exponentials) from a base-2 maximum and the sum relative to it.
 __device__ __forceinline__ float lse_of(float m, float l) {
-    return m == kNegInf && l == 0.0f ? kNegInf : (m + __builtin_amdgcn_logf(l)) * kLn2;
+    if (m == kNegInf) return l == 0.0f ? kNegInf : __builtin_nanf("");
+    return (m + __builtin_amdgcn_logf(l)) * kLn2;
 }
 
 int wide_rows(int dim);            // rows of the wide kernel's tile

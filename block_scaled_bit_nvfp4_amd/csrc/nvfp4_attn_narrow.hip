@@ -259,7 +259,7 @@ __global__ void __launch_bounds__(kNarrowThreads, (NarrowShape<D, KB, VB>::kPerS
             const float m = fmaxf(sub, top);
             const float by = m == sub ? 1.0f : exp2_fast(sub - m);
             sub = m;
-            l *= by;
+            l = l * by + no_maximum(m, seen != 0);
             lr *= by;
 #pragma unroll
             for (int j = 0; j < kRowDims; ++j) o[j] *= by;

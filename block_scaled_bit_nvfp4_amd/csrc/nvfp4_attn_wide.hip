@@ -395,7 +395,7 @@ __global__ void __launch_bounds__(WideShape<D>::kThreads) attn_wide_kernel(AttnA
             const float m = fmaxf(sub, top);
             const float by = m == sub ? 1.0f : exp2_fast(sub - m);
             sub = m;
-            l *= by;
+            l = l * by + no_maximum(m, !edge || seen != 0);
             lr *= by;
 #pragma unroll
             for (int d = 0; d < kDims; ++d) o[d] *= by;
