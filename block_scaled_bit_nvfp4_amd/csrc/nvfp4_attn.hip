@@ -178,7 +178,7 @@ NVFP4_API int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_bat
                                  size_t workspace_bytes, hipStream_t stream) {
     AttnArgs a;
     if (int st = attn_check(cache, batch, q_heads, a.kv)) return st;
-    if (!q || !out || !tscale_ok(scale) || window < 0) return NVFP4_EINVAL;
+    if ((batch->tokens > 0 && (!q || !out)) || !tscale_ok(scale) || window < 0) return NVFP4_EINVAL;
     if (tree && (window > 0 || batch->max_new > 64)) return NVFP4_EINVAL;
     const int64_t wide = int64_t(q_heads) * cache->head_dim;
     if (q_stride < wide || out_stride < wide || q_stride > (int64_t(1) << 40) || out_stride > (int64_t(1) << 40))

@@ -408,7 +408,7 @@ static int kv_move(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int
     KvView v;
     if (int st = kv_check(cache, batch, v)) return st;
     if (dtype != NVFP4_KV_BF16 && dtype != NVFP4_KV_F32) return NVFP4_EINVAL;
-    if (APPEND ? !k || !x : !k && !x) return NVFP4_EINVAL;
+    if (batch->tokens > 0 && (APPEND ? !k || !x : !k && !x)) return NVFP4_EINVAL;
     if (int st = kv_rows_check(cache, dtype, k, k_stride)) return st;
     if (int st = kv_rows_check(cache, dtype, x, v_stride)) return st;
     if (batch->tokens == 0) return NVFP4_OK;

@@ -363,7 +363,8 @@ int mxfp4_gemv(const uint8_t *wq, const uint8_t *ws, float tscale, int64_t rows,
  * checked there (offsets are clamped to 0..tokens, past to the table's
  * positions).  max_new and max_context are upper bounds of any sequence's new
  * tokens and of past + new, known to the host: they pick the launch's shape and
- * never the results' correctness. */
+ * never the results' correctness.  A batch of no tokens is no error, and its rows'
+ * pointers may be NULL. */
 #define NVFP4_KV_MXFP4 4
 #define NVFP4_KV_MXFP8 8
 
@@ -414,9 +415,10 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int 
  * word per new token; at most 64 new tokens per sequence, window 0) the
  * positions before past[s] and past[s] + b for each set bit b of the token's
  * word -- the ancestors of a drafted token in a speculative verify.  A token with
- * nothing allowed gets zeros and lse = -infinity.  What stands in masked or
- * unwritten places, NaN too, does not reach the outputs.  Rows of no sequence are
- * left alone.
+ * nothing allowed gets zeros and lse = -infinity; one that sees keys but has no
+ * finite score (an infinity or NaN in its query, NaN keys) gets NaN.  What stands in
+ * masked or unwritten places, NaN too, does not reach the outputs.  Rows of no
+ * sequence are left alone.
  *   q   bf16 bits [tokens][q_heads][head_dim], q_stride elements between tokens;
  *   out bf16 bits, the same with out_stride;  lse fp32 [tokens][q_heads] or NULL.
  * q_heads is a multiple of heads, scale finite and > 0; q and out 16-byte
