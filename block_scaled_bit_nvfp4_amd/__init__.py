@@ -361,12 +361,25 @@ def alloc_mx_repacked(rows: int, cols: int, device="cuda"):
 
 # ------------------------------------------- paged, quantised key/value cache
 
+def _int32(name, value):
+    """value as an int, refused where ctypes would cut it down to another one."""
+    value = int(value)
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError("%s is %d, past 32 bits" % (name, value))
+    return value
+
+
+def _kv_shape(format, pages, page_tokens, heads, head_dim):
+    return (_int32("format", format), _int32("pages", pages), _int32("page_tokens", page_tokens),
+            _int32("heads", heads), _int32("head_dim", head_dim))
+
+
 def nvfp4_kv_code_bytes(format: int, pages: int, page_tokens: int, heads: int, head_dim: int) -> int:
-    return int(load().nvfp4_kv_code_bytes(format, pages, page_tokens, heads, head_dim))
+    return int(load().nvfp4_kv_code_bytes(*_kv_shape(format, pages, page_tokens, heads, head_dim)))
 
 
 def nvfp4_kv_scale_bytes(format: int, pages: int, page_tokens: int, heads: int, head_dim: int) -> int:
-    return int(load().nvfp4_kv_scale_bytes(format, pages, page_tokens, heads, head_dim))
+    return int(load().nvfp4_kv_scale_bytes(*_kv_shape(format, pages, page_tokens, heads, head_dim)))
 
 
 class KvCache:
@@ -407,7 +420,8 @@ class KvBatch:
                  ("past", past, _I32, 4 * seqs, False))
         self.arrays = (page_table, offsets, past)
         self.device, self._index = page_table.device, page_table.get_device()
-        self.tokens, self.max_new, self.max_context = int(tokens), int(max_new), int(max_context)
+        self.tokens = int(tokens)
+        self.max_new, self.max_context = _int32("max_new", max_new), _int32("max_context", max_context)
         self._c = _KvBatch(*[t.data_ptr() for t in self.arrays], self.tokens, seqs, width, self.max_new,
                            self.max_context)
         self._ref = ctypes.addressof(self._c)
@@ -491,7 +505,7 @@ def nvfp4_kv_read(cache, batch, K=None, V=None, stream=None):
 
 def nvfp4_kv_attention_workspace_bytes(cache, batch, q_heads) -> int:
     _kv_pair(cache, batch)
-    return int(load().nvfp4_kv_attention_workspace_bytes(cache._ref, batch._ref, int(q_heads)))
+    return int(load().nvfp4_kv_attention_workspace_bytes(cache._ref, batch._ref, _int32("q_heads", q_heads)))
 
 
 def nvfp4_kv_attention(cache, batch, Q, scale, out, lse=None, window=0, tree=None, workspace=None, stream=None):
@@ -511,7 +525,8 @@ def nvfp4_kv_attention(cache, batch, Q, scale, out, lse=None, window=0, tree=Non
         if not workspace.is_contiguous() or workspace.get_device() != cache._index:
             raise ValueError("workspace must be contiguous, on %s" % cache.device)
         nbytes = workspace.numel() * workspace.element_size()
-    _check(load().nvfp4_kv_attention(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale), int(window),
+    _check(load().nvfp4_kv_attention(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale),
+                                     _int32("window", window),
                                      None if tree is None else tree.data_ptr(), out.data_ptr(), os_,
                                      None if lse is None else lse.data_ptr(),
                                      workspace.data_ptr() if nbytes else None, nbytes, _kv_stream(stream, cache)),

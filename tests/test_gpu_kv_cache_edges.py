@@ -36,3 +36,27 @@ def test_a_step_of_no_tokens():
     nv.nvfp4_kv_attention(cache, batch, q, 0.125, torch.empty_like(q), tree=torch.empty(0, dtype=torch.int64, device=K.DEV))
     torch.cuda.synchronize()
     assert all((p == 0x5A).all() for p in cache.planes)
+
+
+@pytest.mark.parametrize("value", [1 << 31, (1 << 32) + 5, -(1 << 31) - 1, -(1 << 32) + 5])
+def test_numbers_past_32_bits_are_refused(value):
+    """The library's arguments are 32-bit: a larger number must not become another one
+    (a window of 2^32 + 5 keys one of 5)."""
+    G.note("kv calls with %d" % value)
+    table, offsets, past = (torch.zeros(s, dtype=torch.int32, device=K.DEV) for s in ((1, 2), (2,), (1,)))
+    with pytest.raises(ValueError):
+        nv.KvBatch(table, offsets, past, 1, value, 1)
+    with pytest.raises(ValueError):
+        nv.KvBatch(table, offsets, past, 1, 1, value)
+    cache, batch = nv.alloc_kv_cache(2, 16, 1, 64, device=K.DEV), nv.KvBatch(table, offsets, past, 1, 1, 1)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16, device=K.DEV)
+    with pytest.raises(ValueError):
+        nv.nvfp4_kv_attention(cache, batch, q, 0.125, torch.empty_like(q), window=value)
+    with pytest.raises(ValueError):
+        nv.nvfp4_kv_attention_workspace_bytes(cache, batch, value)
+    planes = [torch.zeros(1 << 12, dtype=torch.uint8, device=K.DEV) for _ in range(4)]
+    for at in range(5):
+        numbers = [8, 8, 16, 1, 64]
+        numbers[at] += value & ~0xFFFFFFFF or 1 << 32
+        with pytest.raises((ValueError, nv.NVFP4Error)):
+            nv.KvCache(*planes, *numbers)
