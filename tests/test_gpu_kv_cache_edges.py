@@ -6,6 +6,7 @@ import torch
 import block_scaled_bit_nvfp4_amd as nv
 from tests import _gpu as G
 from tests import _kv as K
+from tests.test_gpu_kv_cache import _want
 
 pytestmark = pytest.mark.gpu
 
@@ -60,3 +61,36 @@ def test_numbers_past_32_bits_are_refused(value):
         numbers[at] += value & ~0xFFFFFFFF or 1 << 32
         with pytest.raises((ValueError, nv.NVFP4Error)):
             nv.KvCache(*planes, *numbers)
+
+
+@pytest.mark.parametrize("dim,heads,k_fmt,v_fmt,new", [
+    (256, 4, 8, 4, [701, 0, 1, 3, 333, 0, 0, 1011, 4]),          # 2053 rows of 64 threads' work
+    (128, 5, 4, 8, [0, 5, 1, 2, 3001, 2, 275]),
+    (64, 3, 8, 8, [10913, 0, 11, 2]),
+])
+def test_read_of_many_rows(dim, heads, k_fmt, v_fmt, new):
+    """Enough rows that a thread of the read takes two of them: pairs whose second row is
+    another sequence's, has another page or none, or is the last, alone; pages left
+    out from an odd row on; rows of no sequence after them."""
+    G.note("kv read, %d rows D=%d" % (sum(new), dim))
+    rng = np.random.default_rng(dim)
+    page, tokens, spare = 16, sum(new), 6
+    past = rng.integers(0, 30, len(new))
+    past[np.argmax(new)] = 3
+    table, keys, values = K.filled(rng, new, past, heads, dim, k_fmt, v_fmt, page)
+    table[np.argmax(new), 5], table[np.argmax(new), 9:11] = -1, len(keys.codes)
+    offsets, past = K.lengths(new, past)
+    assert tokens * heads * (dim // 16) >= 1 << 17 and (offsets[np.argmax(new)] + 5 * page - 3) % 2
+    cache = K.cache_gpu(keys, values, page)
+    batch = K.batch_gpu(table, offsets, past, tokens=tokens + spare)
+    want = [_want(side, table, offsets, past, tokens) for side in (keys, values)]
+    for dtype in (torch.bfloat16, torch.float32):
+        wide = torch.full((tokens + spare, 2 * heads * dim + 16), float("nan"), dtype=dtype, device=K.DEV)
+        k, v = wide[:, :heads * dim].unflatten(1, (heads, dim)), wide[:, heads * dim + 16:].unflatten(1, (heads, dim))
+        nv.nvfp4_kv_read(cache, batch, k, v)
+        for got, ref in zip((k, v), want):
+            assert np.array_equal(got[:tokens].double().cpu().numpy(), ref)
+        assert wide[tokens:].isnan().all() and wide[:, heads * dim:heads * dim + 16].isnan().all()
+        alone = torch.full((tokens + spare, heads, dim), float("nan"), dtype=dtype, device=K.DEV)
+        nv.nvfp4_kv_read(cache, batch, V=alone)
+        assert torch.equal(alone[:tokens], v[:tokens]) and alone[tokens:].isnan().all()
