@@ -60,3 +60,48 @@ def test_infinities_in_queries(dim, k_fmt, new, past, tree, monkeypatch):
         else:
             assert np.isnan(o[t, h]).all()
     assert np.isnan(o).any(-1).sum() == len(at) - tree
+
+
+def _nan(side, table, pos, head, block, page):
+    """One block of one token becomes NaN."""
+    unit, r = divmod(pos % page, 16)
+    side.scales[table[0, pos // page], head, unit, side._scale_bytes(r)[block]] = 0xFF
+
+
+@pytest.mark.parametrize("dim,k_fmt,v_fmt", [(64, 8, 8), (64, 4, 4), (128, 8, 4), (128, 4, 8), (256, 4, 8), (256, 8, 4)])
+@pytest.mark.parametrize("new,group", [(40, 4), (100, 8)])
+def test_nan_blocks_of_new_tokens(new, group, dim, k_fmt, v_fmt):
+    """A NaN block of a value reaches its elements, a NaN block of a key everything, in
+    the rows that see the token and no other."""
+    G.note("attention, NaN among %d new tokens D=%d %d/%d" % (new, dim, k_fmt, v_fmt))
+    past, last = 50, dim // 32 - 1
+
+    def edit(table, keys, values):
+        _nan(values, table, past + new // 2, 0, 1, 32)
+        _nan(values, table, past + new // 2 + 3, 1, 0, 32)
+        _nan(keys, table, past + new - 2, 0, last, 32)
+        _nan(values, table, past + new - 1, 0, last, 32)
+
+    out, lse, ref = _run(np.random.default_rng(dim), [new], [past], 2, group, dim, k_fmt, v_fmt, page=32, edit=edit)
+    o, half = out.float().cpu().numpy(), new // 2
+    assert np.isfinite(o[:half]).all() and np.isnan(o[half:, :group, 32:64]).all() and np.isnan(o[new - 2:, :group]).all()
+    assert np.isfinite(o[half:new - 2, :group, :32]).all() and np.isfinite(o[half:new - 2, :group, 64:]).all()
+    assert np.isnan(o[half + 3:, group:, :32]).all() and np.isfinite(o[:, group:, 32:]).all()
+
+
+@pytest.mark.parametrize("dim,k_fmt,v_fmt", [(64, 8, 4), (128, 4, 8), (256, 8, 8)])
+@pytest.mark.parametrize("new,window", [(3, 0), (100, 0), (100, 60)])
+def test_nan_blocks_of_the_past(new, window, dim, k_fmt, v_fmt):
+    """The same in tiles that every row sees, and where the rows' windows pass them."""
+    G.note("attention, NaN in the past of %d new tokens D=%d window %d" % (new, dim, window))
+    past = 300
+
+    def edit(table, keys, values):
+        _nan(values, table, 140 if window == 0 else past - 20, 0, 1, 32)
+        _nan(keys, table, 170 if window == 0 else past - 10, 1, 0, 32)
+
+    out, lse, ref = _run(np.random.default_rng(dim), [new], [past], 3, 4, dim, k_fmt, v_fmt, page=32, edit=edit, window=window)
+    o = out.float().cpu().numpy()
+    v_rows, k_rows = (new, new) if window == 0 else (window - 20, window - 10)        # the rows that see them
+    assert np.isnan(o[:v_rows, :4, 32:64]).all() and np.isfinite(o[:, :4, :32]).all() and np.isfinite(o[v_rows:, :4]).all()
+    assert np.isnan(o[:k_rows, 4:8]).all() and np.isfinite(o[k_rows:, 4:8]).all() and np.isfinite(o[:, 8:]).all()
