@@ -6,6 +6,7 @@ import torch
 
 import block_scaled_bit_nvfp4_amd as nv
 from block_scaled_bit_nvfp4_amd.attention_layer import AttentionLayer
+from oracle import kv as okv
 from tests import _gpu as G
 from tests import _kv as K
 from tests import test_gpu_attention_layer as L
@@ -102,3 +103,27 @@ def test_weights_without_a_scale():
         w[3, 5] = bad
         with pytest.raises(ValueError):
             AttentionLayer(w, wo, L.Q_HEADS, L.HEADS, L.DIM, 8, L.PAGES, L.PAGE)
+
+
+def test_a_steps_attention_against_the_oracle():
+    """The layer's attention outputs, and the log-sum-exp of the same call on its own
+    queries and cache, against the fp64 oracle."""
+    layer = L._layer()
+    table = np.arange(L.PAGES, dtype=np.int32)[::-1].reshape(2, -1).copy()
+    keys, values = (kind(8, L.PAGES, L.PAGE, L.HEADS, L.DIM, fill=0xFF) for kind in (okv.Keys, okv.Values))
+    past = np.zeros(2, np.int64)
+    for seed, new in enumerate([(70, 3), (1, 1), (9, 30)]):
+        offsets, _ = K.lengths(new, past)
+        batch, n = K.batch_gpu(table, offsets, past), sum(new)
+        G.note("attention layer: %s after %s, log-sum-exp" % (new, past.tolist()))
+        layer.step(L._inputs(n, seed), batch)
+        heads = layer.qkv[:n].view(n, -1, L.DIM).double().cpu().numpy()
+        okv.append(keys, table, offsets, past, heads[:, L.Q_HEADS:L.Q_HEADS + L.HEADS])
+        okv.append(values, table, offsets, past, heads[:, L.Q_HEADS + L.HEADS:])
+        q = layer.q[:n].view(n, L.Q_HEADS, L.DIM)
+        assert np.array_equal(q.double().cpu().numpy(), K.bf16(heads[:, :L.Q_HEADS]))
+        out, lse = K.attend(layer.cache, batch, q, layer.scale, L.Q_HEADS)
+        assert torch.equal(out, layer.o[:n].view_as(out))
+        ref = okv.attention(keys, values, table, offsets, past, q.double().cpu().numpy(), layer.scale)
+        K.check(out, lse, ref, L.DIM, "step %d" % seed)
+        past += np.asarray(new)
