@@ -96,9 +96,10 @@ static AttnPlan attn_plan(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, int 
     }
     const int64_t most = int64_t(std::max(b->max_new, 1)) * group;
     AttnPlan p = {};
-    // a tile sees its window and its own tokens
+    // a tile sees its window and its own tokens; a bound past every position would
+    // pass 32 bits once rounded to whole splits
     const auto span = [&](int rows) {
-        const int64_t context = std::max(b->max_context, 1);
+        const int64_t context = std::min(std::max(b->max_context, 1), kKvMaxPositions);
         return window > 0 ? std::min<int64_t>(context, int64_t(window) + rows / group + 1) : context;
     };
     const bool even = b->tokens == int64_t(b->seqs) * b->max_new;         // all of the same length

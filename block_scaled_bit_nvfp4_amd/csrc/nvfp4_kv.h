@@ -10,6 +10,7 @@ namespace nvfp4 {
 
 constexpr int kKvUnit = 16;            // tokens of a unit
 constexpr int kKvMaxPages = 1 << 30;
+constexpr int kKvMaxPositions = 1 << 30;   // that a sequence's table names
 constexpr int64_t kMaxGrid = int64_t(1) << 32;   // threads along one extent of a grid stay below this
 
 // One side (keys or values) of a unit at head dimension D and BITS per code.

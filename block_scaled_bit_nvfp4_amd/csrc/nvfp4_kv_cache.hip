@@ -21,7 +21,7 @@ int kv_check(const nvfp4_kv_cache *c, const nvfp4_kv_batch *b, KvView &v) {
     if (!b->page_table || !b->offsets || !b->past || b->seqs < 1 || b->table_width < 1) return NVFP4_EINVAL;
     if (b->tokens < 0 || b->max_new < 0 || b->max_context < 0) return NVFP4_EINVAL;
     // positions, and rows of heads, are 32-bit in the kernels
-    if (int64_t(b->table_width) * c->page_tokens > (int64_t(1) << 30)) return NVFP4_ESHAPE;
+    if (int64_t(b->table_width) * c->page_tokens > kKvMaxPositions) return NVFP4_ESHAPE;
     if (b->tokens > (int64_t(1) << 30) / c->heads) return NVFP4_ESHAPE;
     if (!aligned(c->k_codes, 16) || !aligned(c->k_scales, 16) || !aligned(c->v_codes, 16) ||
         !aligned(c->v_scales, 16) || !aligned(b->page_table, 4) || !aligned(b->offsets, 4) || !aligned(b->past, 4))
