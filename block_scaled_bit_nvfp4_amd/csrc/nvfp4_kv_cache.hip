@@ -258,59 +258,53 @@ struct KvThread {
     }
 };
 
-// One thread takes 16 elements of a head of N tokens; two neighbours share a
-// block.  Bound by bytes (2 or 4 read and 1 or 1/2 written per element) for a
-// chunk of tokens (where several tokens a thread share the search for their place and
-// have their loads in flight together), and by the launch for a few tokens.  Measured:
-// 2048 tokens of 8 heads of 128 from float32 to 4 bits 7 us, 64 tokens 3.4 us.
-template <int N, int D, int BITS, int SIDE, class T>
-__device__ __forceinline__ void append16(const KvView &v, const KvPlaces<N> &p, const T *src, int64_t stride, int part) {
+// One thread takes 16 elements of a head of a token; two neighbours share a block.
+// Bound by bytes (2 or 4 read and 1 or 1/2 written per element) for a chunk of tokens,
+// and by the launch for a few.  Measured: 2048 tokens of 8 heads of 128 from float32 to
+// 4 bits 7 us, 64 tokens 3.4 us.
+template <int D, int BITS, int SIDE, class T>
+__device__ __forceinline__ void append16(const KvView &v, const KvPlaces<1> &p, const T *src, int part) {
     typedef KvSide<D, BITS> S;
-    float x[N][16];
+    float x[16];
+    if (p.in[0]) load16(src, x);
+    uint32_t amax = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        if (p.in[i]) load16(src + i * stride, x[i]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-        uint32_t amax = 0;
-#pragma unroll
-        for (int e = 0; e < 16; ++e) amax = max(amax, __float_as_uint(x[i][e]) & 0x7FFFFFFFu);
-        amax = max(amax, uint32_t(__builtin_amdgcn_update_dpp(0, int(amax), 0xB1, 0xF, 0xF, false)));   // the neighbour's
-        if (!p.ok[i]) continue;
-        const bool bad = amax >= 0x7F800000u;
-        const int E = block_exponent<BITS>(bad ? 0u : amax);
-        uint32_t w[BITS / 2];
-        quantise16<BITS>(x[i], E, bad, w);
-        move_codes<D, BITS, SIDE, false>(v.codes[SIDE] + p.unit[i] * S::kUnitCodes, p.r[i], part, w);
-        if ((part & 1) == 0) {
-            const int b = part / 2;
-            v.scales[SIDE][p.unit[i] * S::kUnitScales + (SIDE == 0 ? S::key_scale(p.r[i], b) : S::value_scale(p.r[i], b))] =
-                uint8_t(bad ? 0xFF : E + 127);
-        }
+    for (int e = 0; e < 16; ++e) amax = max(amax, __float_as_uint(x[e]) & 0x7FFFFFFFu);
+    amax = max(amax, uint32_t(__builtin_amdgcn_update_dpp(0, int(amax), 0xB1, 0xF, 0xF, false)));   // the neighbour's
+    if (!p.ok[0]) return;
+    const bool bad = amax >= 0x7F800000u;
+    const int E = block_exponent<BITS>(bad ? 0u : amax);
+    uint32_t w[BITS / 2];
+    quantise16<BITS>(x, E, bad, w);
+    const int64_t unit = p.unit[0];
+    move_codes<D, BITS, SIDE, false>(v.codes[SIDE] + unit * S::kUnitCodes, p.r[0], part, w);
+    if ((part & 1) == 0) {
+        const int at = SIDE == 0 ? S::key_scale(p.r[0], part / 2) : S::value_scale(p.r[0], part / 2);
+        v.scales[SIDE][unit * S::kUnitScales + at] = uint8_t(bad ? 0xFF : E + 127);
     }
 }
 
-template <int N, int D, class T>
+template <int D, class T>
 __global__ void __launch_bounds__(256) kv_append_kernel(KvView v, int k_bits, int v_bits, const T *__restrict__ k,
                                                         int64_t k_stride, const T *__restrict__ x, int64_t v_stride) {
-    const KvThread<N, D> a(v);
-    KvPlaces<N> p = kv_places<N>(v, a.t0, a.head);
+    const KvThread<1, D> a(v);
+    const KvPlaces<1> p = kv_places<1>(v, a.t0, a.head);
     if (!a.in) return;                                   // neighbours return together
     const int side = blockIdx.y;
-    const int64_t stride = side == 0 ? k_stride : v_stride;
-    const T *src = (side == 0 ? k : x) + a.t0 * stride + a.head * D + a.part * 16;
+    const T *src = (side == 0 ? k + a.t0 * k_stride : x + a.t0 * v_stride) + a.head * D + a.part * 16;
     if (side == 0) {
-        if (k_bits == 8) append16<N, D, 8, 0>(v, p, src, stride, a.part);
-        else append16<N, D, 4, 0>(v, p, src, stride, a.part);
+        if (k_bits == 8) append16<D, 8, 0>(v, p, src, a.part);
+        else append16<D, 4, 0>(v, p, src, a.part);
     } else {
-        if (v_bits == 8) append16<N, D, 8, 1>(v, p, src, stride, a.part);
-        else append16<N, D, 4, 1>(v, p, src, stride, a.part);
+        if (v_bits == 8) append16<D, 8, 1>(v, p, src, a.part);
+        else append16<D, 4, 1>(v, p, src, a.part);
     }
 }
 
 // --------------------------------------------------------------------- read
 
-// The same way back: one pass, bound by bytes (65521 tokens of 8 heads of 128 from
+// The same way back, of N tokens that share the search for their places and have their
+// loads in flight together: one pass, bound by bytes (65521 tokens of 8 heads of 128 from
 // 8 bits 92 us, 4.5 TB/s read and written; a large copy reaches 4.8).  The values are
 // exact products of a code and a power of two.
 template <int N, int D, int BITS, int SIDE, class T>
@@ -374,32 +368,50 @@ static int kv_rows_check(const nvfp4_kv_cache *c, int dtype, const void *p, int6
     return aligned(p, 16) && stride * size % 16 == 0 ? NVFP4_OK : NVFP4_EALIGN;
 }
 
-template <bool APPEND, int N, int D, class T>
-static int kv_launch_rows(const nvfp4_kv_cache *c, const KvView &v, void *k, int64_t k_stride, void *x, int64_t v_stride,
-                          hipStream_t stream) {
-    const int64_t groups = ceil_div(ceil_div(v.tokens, N) * c->heads * (D / 16), 256);
-    if (groups >= kMaxGrid / 256) return NVFP4_ESHAPE;
-    const unsigned g = unsigned(groups);
-    const int kb = c->k_format == NVFP4_KV_MXFP8 ? 8 : 4, vb = c->v_format == NVFP4_KV_MXFP8 ? 8 : 4;
-    if (APPEND)
-        kv_append_kernel<N, D, T><<<dim3(g, 2), 256, 0, stream>>>(v, kb, vb, static_cast<const T *>(k), k_stride,
-                                                                  static_cast<const T *>(x), v_stride);
-    else
-        kv_read_kernel<N, D, T><<<dim3(g, 2), 256, 0, stream>>>(v, kb, vb, static_cast<T *>(k), k_stride,
-                                                                static_cast<T *>(x), v_stride);
+// Workgroups along the rows of a launch of N token rows a thread; 0 past the grid's limit.
+static unsigned kv_groups(const KvView &v, int n, int dim) {
+    const int64_t groups = ceil_div(ceil_div(v.tokens, n) * v.heads * (dim / 16), 256);
+    return groups < kMaxGrid / 256 ? unsigned(groups) : 0u;
+}
+
+template <int D, class T>
+static int kv_launch_append(const KvView &v, int k_bits, int v_bits, const T *k, int64_t k_stride, const T *x,
+                            int64_t v_stride, hipStream_t stream) {
+    // One token row a thread: two are as good (16384 tokens 64.6 us, two 62.8; 2048
+    // tokens 12.6, 13.2).
+    const unsigned g = kv_groups(v, 1, D);
+    if (g == 0) return NVFP4_ESHAPE;
+    kv_append_kernel<D, T><<<dim3(g, 2), 256, 0, stream>>>(v, k_bits, v_bits, k, k_stride, x, v_stride);
     return launch_status();
+}
+
+template <int N, int D, class T>
+static int kv_launch_read_rows(const KvView &v, int k_bits, int v_bits, T *k, int64_t k_stride, T *x, int64_t v_stride,
+                               hipStream_t stream) {
+    const unsigned g = kv_groups(v, N, D);
+    if (g == 0) return NVFP4_ESHAPE;
+    kv_read_kernel<N, D, T><<<dim3(g, 2), 256, 0, stream>>>(v, k_bits, v_bits, k, k_stride, x, v_stride);
+    return launch_status();
+}
+
+template <int D, class T>
+static int kv_launch_read(const KvView &v, int k_bits, int v_bits, T *k, int64_t k_stride, T *x, int64_t v_stride,
+                          hipStream_t stream) {
+    // Two token rows a thread where the card is full all the same (65521 tokens: 91.7
+    // us, one row 95.2, four 91.5; 1500 tokens of 4 heads of 256: 9.3, 9.9, 10.0).
+    constexpr int64_t kFill = 1 << 17;
+    if (int64_t(v.tokens) * v.heads * (D / 16) >= kFill)
+        return kv_launch_read_rows<2, D, T>(v, k_bits, v_bits, k, k_stride, x, v_stride, stream);
+    return kv_launch_read_rows<1, D, T>(v, k_bits, v_bits, k, k_stride, x, v_stride, stream);
 }
 
 template <bool APPEND, int D, class T>
 static int kv_launch(const nvfp4_kv_cache *c, const KvView &v, void *k, int64_t k_stride, void *x, int64_t v_stride,
                      hipStream_t stream) {
-    // A thread reads two token rows where the card is full all the same (65521 tokens:
-    // 91.7 us, one row 95.2, four 91.5; 1500 tokens of 4 heads of 256: 9.3, 9.9, 10.0);
-    // for append one is as good (16384 tokens 64.6 us, two 62.8; 2048 tokens 12.6, 13.2).
-    constexpr int64_t kFill = 1 << 17;
-    if (!APPEND && int64_t(v.tokens) * c->heads * (D / 16) >= kFill)
-        return kv_launch_rows<APPEND, APPEND ? 1 : 2, D, T>(c, v, k, k_stride, x, v_stride, stream);
-    return kv_launch_rows<APPEND, 1, D, T>(c, v, k, k_stride, x, v_stride, stream);
+    const int kb = c->k_format == NVFP4_KV_MXFP8 ? 8 : 4, vb = c->v_format == NVFP4_KV_MXFP8 ? 8 : 4;
+    T *const ks = static_cast<T *>(k), *const xs = static_cast<T *>(x);
+    if constexpr (APPEND) return kv_launch_append<D, T>(v, kb, vb, ks, k_stride, xs, v_stride, stream);
+    else return kv_launch_read<D, T>(v, kb, vb, ks, k_stride, xs, v_stride, stream);
 }
 
 template <bool APPEND>
