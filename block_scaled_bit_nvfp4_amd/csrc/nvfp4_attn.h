@@ -9,6 +9,13 @@
 // need no other lane, and the exponentials, rounded to bf16, are the B operand of the
 // second product as they stand (the order of keys in that contraction is chosen to
 // match, and the cache's value layout with it).
+//
+// That rounding, at most 2^-8 of a weight, is chosen for the one matrix instruction that
+// it takes: the remainders as a second operand would double those of the second
+// product, which bound chunks. The outputs are divided by the sum of the weights as
+// rounded, so that it does not shift them. Against 64-bit arithmetic the outputs are 0.0017
+// to 0.0023 off (2-norm), of which 0.0016 is their own rounding to bf16. Everything
+// else, scores, references, sums, parts and the log-sum-exp, is fp32.
 #pragma once
 
 #include <atomic>

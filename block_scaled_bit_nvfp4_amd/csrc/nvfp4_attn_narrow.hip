@@ -8,9 +8,9 @@
 // of a CU keep 100 KB in flight.  A tile's codes are then read once, decoded in
 // registers straight to operands of v_mfma_f32_16x16x32_bf16; sixteen rows are
 // the least that instruction takes, so a group of one to sixteen query heads costs the
-// same.  A tile's 180 vector instructions take about 0.6 us of a SIMD, a third of the
-// time that its bytes take, so that the masks of edge tiles, the search for the
-// maximum and NaN have branches of their own.
+// same.  A tile's 230 vector and 18 matrix instructions take about half a microsecond of
+// a SIMD, a third of the time that its bytes take, so that the masks of edge tiles, the
+// search for the maximum and NaN have branches of their own.
 //
 // Measured: one token over 131008 keys of 8 heads of 128 (277 MB) 45 us, 6.2 TB/s,
 // and 5 us for the join; 64 tokens over 8192 keys each 146 us (5.8 TB/s), over 1 to

@@ -5,7 +5,9 @@
 // values are decoded to bf16 once per workgroup, into shared memory and as whole
 // operands of v_mfma_f32_32x32x16_bf16: the waves read them with conflict-free
 // 16-byte loads, and the cache's byte order makes each thread's share of the decode
-// one load and a few stores.
+// one load and a few stores.  The stores do conflict, those of values by their stride
+// of 16 bytes, those of 4-bit keys by their two pieces a kilobyte apart: 10 % of shared
+// memory's busy cycles, with 4-bit keys at heads of 128 and 256 17 to 18 %.
 //
 // The two waves of a SIMD work in opposite phases, a barrier between phases: while
 // one multiplies (the values of tile i - 1 by its weights, then the keys of tile i by
@@ -18,10 +20,10 @@
 // each half the elements: they add their halves of the scores through shared
 // memory, take the same softmax, and each keeps half of the output.
 //
-// Measured: 2048 tokens of 40 heads of 128 over 32768 keys 1170 us, 1137 TFLOP/s (a
-// large library product of matrices reaches 1270, at a clock that both lower); 512
-// tokens of 32 heads over 8192 keys 77 us, of which the splits' parts and their join
-// take 15.  Per tile and CU 1.75 us at 128, bound by the matrix instructions; 2.5 us at
+// Measured: 2048 tokens of 40 heads of 128 over 32768 keys 1220 us, 1091 TFLOP/s (1190
+// to 1280 us from card to card; a large library product of matrices reaches 1270
+// TFLOP/s, at a clock that both lower); 512 tokens of 32 heads over 8192 keys 79 us,
+// of which the splits' parts and their join take 15.  Per tile and CU 1.75 us at 128, bound by the matrix instructions; 2.5 us at
 // 64, by the exponentials, of which there are twice as many for each product; 1.2 us for
 // half the rows at 256, by the decode and the phases' starts.
 #include "nvfp4_attn.h"

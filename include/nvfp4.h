@@ -326,8 +326,10 @@ int mxfp4_gemv(const uint8_t *wq, const uint8_t *ws, float tscale, int64_t rows,
  * E2M1 codes (NVFP4_KV_MXFP4), chosen for each side, with one E8M0 scale byte
  * b (2^(b - 127), 0xFF NaN) per 32 consecutive elements of a token's head
  * vector.  Power-of-two scales make every value code * 2^(b - 127) a bf16
- * value, which the matrix cores multiply exactly.  A block with largest
- * magnitude a gets b = 127 + E, E clamped to [-127, 127]:
+ * value, which the matrix cores multiply exactly (but for 2^128, to which MXFP8
+ * rounds elements above 248 * 2^120, the top 3 % of bf16's range: it reads as
+ * infinity).  A block with largest magnitude a gets b = 127 + E, E clamped to
+ * [-127, 127]:
  *   MXFP4: E = floor(log2(a)) - 2, codes saturating at 6 (mxfp4_quantize's rule);
  *   MXFP8: the least E with a <= 448 * 2^E (E4M3 has exponents to spare, so the
  *          larger unit costs nothing, while saturating would cost the largest
@@ -425,7 +427,12 @@ int nvfp4_kv_read(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int 
  * aligned with strides of whole 16 bytes, lse 4-byte, tree 8-byte aligned.
  * Products accumulate in fp32 and the softmax is fp32; its weights are rounded to
  * bf16 for the second product.  Sums run in an order fixed by the arguments and the
- * arrays' values: results are the same bits on every run.
+ * arrays' values: results are the same bits on every run.  They need not be for a
+ * token in another batch (a column of a product of up to eight has the bits that it
+ * has alone): the batch's sizes and bounds choose the kernel and the splits, so that
+ * a token verified among others and the same token decoded alone may differ in the
+ * last bits.  max_context cuts the key axis whatever the lengths on the device, so
+ * that short sequences under a bound far above them are shared by fewer workgroups.
  * workspace: nvfp4_kv_attention_workspace_bytes bytes (for the same cache shape,
  * tokens, seqs, max_new, max_context and q_heads; 0 where the key axis is not
  * split), 16-byte aligned, any contents; not shared by calls that may overlap. */
