@@ -27,6 +27,7 @@ __all__ = [
     "NVFP4_KV_MXFP4", "NVFP4_KV_MXFP8", "KvCache", "KvBatch", "alloc_kv_cache", "nvfp4_kv_code_bytes",
     "nvfp4_kv_scale_bytes", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_kv_attention_workspace_bytes",
     "nvfp4_kv_attention",
+    "nvfp4_rope", "NVFP4_MAX_ROPE",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +37,7 @@ _lib = None
 
 NVFP4_MAX_N = 65536
 NVFP4_MAX_BATCH = 4
+NVFP4_MAX_ROPE = 4
 NVFP4_KV_MXFP4 = 4
 NVFP4_KV_MXFP8 = 8
 _KV_DTYPE = {torch.bfloat16: 0, torch.float32: 1}      # NVFP4_KV_BF16, NVFP4_KV_F32
@@ -57,6 +59,12 @@ class _KvBatch(ctypes.Structure):
     """struct nvfp4_kv_batch of nvfp4.h."""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("page_table", "offsets", "past")] + [("tokens", ctypes.c_int64)] +
                 [(n, ctypes.c_int32) for n in ("seqs", "table_width", "max_new", "max_context")])
+
+
+class _RopeRows(ctypes.Structure):
+    """struct nvfp4_rope_rows of nvfp4.h."""
+    _fields_ = ([("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_stride", ctypes.c_int64),
+                 ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32), ("out_type", ctypes.c_int32)])
 
 
 class NVFP4Error(RuntimeError):
@@ -108,6 +116,7 @@ def load():
             "nvfp4_kv_read": (i32, [P, P, i32, P, i64, P, i64, P]),
             "nvfp4_kv_attention_workspace_bytes": (sz, [P, P, i32]),
             "nvfp4_kv_attention": (i32, [P, P, P, i64, i32, f32, i32, P, P, i64, P, P, sz, P]),
+            "nvfp4_rope": (i32, [P, i32, i32, i64, i32, i32, i32, P, i32, P, P, f32, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -531,3 +540,57 @@ def nvfp4_kv_attention(cache, batch, Q, scale, out, lse=None, window=0, tree=Non
                                      None if lse is None else lse.data_ptr(),
                                      workspace.data_ptr() if nbytes else None, nbytes, _kv_stream(stream, cache)),
            "nvfp4_kv_attention")
+
+
+# ------------------------------------------------------------ rotary positions
+
+def _heads_of(name, t, dtypes, shape, index):
+    """Check a [tokens, heads, dim] tensor whose tokens may be strided (the heads of a
+    token are not); its token stride in elements.  shape: what the last call's tensors
+    share, (tokens, dim)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s: expected a torch.Tensor, got %r" % (name, type(t)))
+    if t.dtype not in dtypes:
+        raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
+    if t.dim() != 3 or (t.shape[0], t.shape[2]) != shape:
+        raise ValueError("%s has shape %s, expected (%d, heads, %d)" % (name, tuple(t.shape), *shape))
+    token, head, element = t.stride()
+    tokens, heads, dim = t.shape
+    if tokens and ((dim > 1 and element != 1) or (heads > 1 and head != dim)):
+        raise ValueError("%s: the heads of a token must be contiguous" % name)
+    if not t.is_cuda or t.get_device() != index:
+        raise ValueError("%s is on %s, the positions on cuda:%d" % (name, t.device, index))
+    return token if tokens > 1 else heads * dim
+
+
+def nvfp4_rope(rows, positions, freqs, axis=None, adjacent=False, factor=1.0, stream=None):
+    """Rotate rows by their tokens' positions: rows is a list of (in, out) pairs of
+    [tokens, heads, head_dim] tensors (all inputs of one type, bfloat16 or float32; out of
+    either; a pair of the same tensor is rotated in place), positions int32 [axes, tokens]
+    or [tokens], freqs float64 [pairs] (radians for each position), axis uint8 [pairs] or
+    None (all pairs follow the first axis)."""
+    rows = list(rows)
+    if not rows or not all(isinstance(r, (tuple, list)) and len(r) == 2 and isinstance(r[0], torch.Tensor)
+                           for r in rows) or rows[0][0].dim() != 3:
+        raise ValueError("rows must be a list of (in, out) pairs of [tokens, heads, head_dim] tensors")
+    _checked(("positions", positions, _I32, 0, False), ("freqs", freqs, (torch.float64,), 0, False),
+             ("axis", axis, _U8, 0, True))
+    first = rows[0][0]
+    tokens, dim = shape = (first.shape[0], first.shape[2])
+    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
+        raise ValueError("positions has shape %s, expected ([axes,] %d)" % (tuple(positions.shape), tokens))
+    pairs = freqs.numel()
+    if axis is not None and axis.numel() != pairs:
+        raise ValueError("axis has %d elements, freqs %d" % (axis.numel(), pairs))
+    index = positions.get_device()
+    arr = (_RopeRows * len(rows))()
+    for i, (x, out) in enumerate(rows):
+        xs = _heads_of("rows[%d] in" % i, x, (first.dtype,) if i else _KV_DTYPE, shape, index)
+        os_ = _heads_of("rows[%d] out" % i, out, _KV_DTYPE, shape, index)
+        if x.shape != out.shape:
+            raise ValueError("rows[%d]: in has shape %s, out %s" % (i, tuple(x.shape), tuple(out.shape)))
+        arr[i] = _RopeRows(x.data_ptr(), out.data_ptr(), xs, os_, x.shape[1], _KV_DTYPE[out.dtype])
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    _check(load().nvfp4_rope(arr, len(rows), _KV_DTYPE[first.dtype], tokens, dim, 2 * pairs, int(bool(adjacent)),
+                             positions.data_ptr(), axes, freqs.data_ptr(), None if axis is None else axis.data_ptr(),
+                             float(factor), _stream(stream, positions)), "nvfp4_rope")

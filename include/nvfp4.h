@@ -442,6 +442,42 @@ int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch,
                        uint16_t *out, int64_t out_stride, float *lse, void *workspace, size_t workspace_bytes,
                        hipStream_t stream);
 
+/* ------------------------------------------------------ rotary positions
+ * What stands between a layer's projection and its cache: queries and keys are
+ * rotated by their tokens' positions.  A position has `axes` numbers (one for
+ * text; time, height and width for images and video).  The first rotary_dim
+ * elements of a head are rotary_dim / 2 pairs; pair i is elements i and
+ * i + rotary_dim / 2, with `adjacent` elements 2 i and 2 i + 1, and turns by
+ *   t = positions[axis[i]][token] * freqs[i]  (radians, in 64 bits):
+ *   out_a = factor * (a cos t - b sin t),  out_b = factor * (b cos t + a sin t);
+ * the rest of the head is copied.  Computed in fp32 and rounded once.  Which axis
+ * a pair follows is the caller's (sections of the head, or by turns); a pair whose
+ * axis is not below `axes` turns by 0.  A negative position turns back.
+ * Frequencies, axes and positions are device memory, read when the kernel runs.
+ *
+ * `count` row sets (queries and keys, say) of `tokens` tokens share positions and
+ * take one launch.  A set is [tokens][heads][head_dim] of `dtype` (NVFP4_KV_BF16 or
+ * _F32), in_stride elements between tokens (column ranges of one projection's
+ * output), written as out_type with out_stride.  A set may be rotated in place (out
+ * the same pointer, type and stride as in); otherwise outputs overlap nothing else.
+ * head_dim is a multiple of 8 up to 1024, rotary_dim a multiple of 8 up to
+ * head_dim (else NVFP4_ESHAPE); pointers 16-byte aligned with strides of whole 16
+ * bytes, freqs 8-byte and positions 4-byte aligned (else NVFP4_EALIGN).  axis may
+ * be NULL: all pairs follow axis 0.  factor is finite and > 0.  No tokens is no
+ * error, and the rows' pointers may then be NULL. */
+#define NVFP4_MAX_ROPE 4
+
+typedef struct nvfp4_rope_rows {
+    const void *in;
+    void *out;
+    int64_t in_stride, out_stride;
+    int32_t heads, out_type;
+} nvfp4_rope_rows;
+
+int nvfp4_rope(const nvfp4_rope_rows *rows, int count, int dtype, int64_t tokens, int head_dim, int rotary_dim,
+               int adjacent, const int32_t *positions, int axes, const double *freqs, const uint8_t *axis,
+               float factor, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
