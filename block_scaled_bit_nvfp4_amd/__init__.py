@@ -28,6 +28,7 @@ __all__ = [
     "nvfp4_kv_scale_bytes", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_kv_attention_workspace_bytes",
     "nvfp4_kv_attention",
     "nvfp4_rope", "NVFP4_MAX_ROPE",
+    "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "NVFP4_MAX_TOP",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -38,6 +39,7 @@ _lib = None
 NVFP4_MAX_N = 65536
 NVFP4_MAX_BATCH = 4
 NVFP4_MAX_ROPE = 4
+NVFP4_MAX_TOP = 64
 NVFP4_KV_MXFP4 = 4
 NVFP4_KV_MXFP8 = 8
 _KV_DTYPE = {torch.bfloat16: 0, torch.float32: 1}      # NVFP4_KV_BF16, NVFP4_KV_F32
@@ -117,6 +119,8 @@ def load():
             "nvfp4_kv_attention_workspace_bytes": (sz, [P, P, i32]),
             "nvfp4_kv_attention": (i32, [P, P, P, i64, i32, f32, i32, P, P, i64, P, P, sz, P]),
             "nvfp4_rope": (i32, [P, i32, i32, i64, i32, i32, i32, P, i32, P, P, f32, P]),
+            "nvfp4_logprobs_workspace_bytes": (sz, [i64, i64, i32]),
+            "nvfp4_logprobs": (i32, [i32, P, i64, i64, i64, f32, P, i32, P, P, P, i32, P, P, P, sz, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(lib, name)
@@ -594,3 +598,53 @@ def nvfp4_rope(rows, positions, freqs, axis=None, adjacent=False, factor=1.0, st
     _check(load().nvfp4_rope(arr, len(rows), _KV_DTYPE[first.dtype], tokens, dim, 2 * pairs, int(bool(adjacent)),
                              positions.data_ptr(), axes, freqs.data_ptr(), None if axis is None else axis.data_ptr(),
                              float(factor), _stream(stream, positions)), "nvfp4_rope")
+
+
+# ---------------------------------------------------------- log probabilities
+
+def nvfp4_logprobs_workspace_bytes(n: int, vocab: int, top: int) -> int:
+    return int(load().nvfp4_logprobs_workspace_bytes(int(n), int(vocab), _int32("top", top)))
+
+
+def _second(name, t, n):
+    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != n:
+        raise ValueError("%s must be an int32 tensor [%d, ...]" % (name, n))
+    return t.shape[1]
+
+
+def _like(name, t, shape):
+    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape:
+        raise ValueError("%s must be a float32 tensor of shape %s" % (name, shape))
+
+
+def nvfp4_logprobs(logits, tokens=None, logp=None, lse=None, entropy=None, top_logp=None, top_index=None, scale=1.0,
+                   workspace=None, stream=None):
+    """Log probabilities of logits [n, vocab] (float32 or bfloat16; rows may be strided):
+    logp float32 [n, given] of tokens int32 [n, given], lse and entropy float32 [n], and
+    the likeliest tokens top_index int32 [n, top] with top_logp float32 [n, top].  What is
+    None is not computed."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits: expected a torch.Tensor, got %r" % type(logits))
+    if logits.dtype not in _KV_DTYPE or logits.dim() != 2:
+        raise ValueError("logits must be a float32 or bfloat16 tensor [n, vocab]")
+    n, vocab = logits.shape
+    if vocab > 1 and logits.stride(1) != 1:
+        raise ValueError("the logits of a row must be contiguous")
+    if (tokens is None) != (logp is None) or (top_logp is None) != (top_index is None):
+        raise ValueError("tokens and logp, and top_logp and top_index, come together")
+    given = top = 0
+    if tokens is not None:
+        given = _second("tokens", tokens, n)
+        _like("logp", logp, (n, given))
+    if top_index is not None:
+        top = _second("top_index", top_index, n)
+        _like("top_logp", top_logp, (n, top))
+    _checked(("logits", logits[:, :0], _KV_DTYPE, 0, False), ("tokens", tokens, _I32, 0, True),
+             ("logp", logp, _F32, 0, True), ("lse", lse, _F32, 4 * n, True), ("entropy", entropy, _F32, 4 * n, True),
+             ("top_logp", top_logp, _F32, 0, True), ("top_index", top_index, _I32, 0, True),
+             ("workspace", workspace, _ANY, 0, True))
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(load().nvfp4_logprobs(_KV_DTYPE[logits.dtype], _ptr(logits), n, vocab,
+                                 logits.stride(0) if n > 1 else vocab, float(scale), _ptr(tokens), given, _ptr(logp),
+                                 _ptr(lse), _ptr(entropy), top, _ptr(top_logp), _ptr(top_index), _ptr(workspace),
+                                 nbytes, _stream(stream, logits)), "nvfp4_logprobs")

@@ -478,6 +478,34 @@ int nvfp4_rope(const nvfp4_rope_rows *rows, int count, int dtype, int64_t tokens
                int adjacent, const int32_t *positions, int axes, const double *freqs, const uint8_t *axis,
                float factor, hipStream_t stream);
 
+/* --------------------------------------------------------- log probabilities
+ * What is asked of a vocabulary projection's logits beside their argmax.  Row r of
+ * logits [n][vocab] (NVFP4_KV_F32, as the products write them, or _BF16; `stride`
+ * elements between rows), with z = scale * logit (scale: one over the
+ * temperature), gives
+ *   lse[r]       = log sum exp(z),
+ *   logp[r][i]   = z[tokens[r][i]] - lse[r]  for i < given; NaN for a token that is
+ *                  not in 0 .. vocab - 1,
+ *   entropy[r]   = -sum p log p in nats, p = exp(z - lse[r]); p = 0 adds nothing,
+ *   top_index[r] = the `top` tokens of the largest logits in falling order (ties: the
+ *                  lowest token first; -0 and +0 tie, NaN counts least), and
+ *   top_logp[r]  = their log probabilities.
+ * Logits of minus infinity are tokens that are masked out.  A row of nothing else
+ * has lse and all log probabilities -infinity and entropy 0; one with a z of +infinity
+ * or NaN has lse, log probabilities and entropy NaN.  Outputs may each be NULL
+ * (tokens and logp together, with given = 0; top_logp and top_index both, with top =
+ * 0), but not all.  Sums are fp32 in a fixed order.  0 <= n, 1 <= vocab <= 2^30,
+ * 0 <= top <= min(vocab, NVFP4_MAX_TOP), stride >= vocab (else NVFP4_ESHAPE),
+ * 0 <= given <= 2^20; logits need only their element's alignment, outputs 4 bytes.
+ * workspace: nvfp4_logprobs_workspace_bytes(n, vocab, top) bytes, 16-byte aligned,
+ * any contents; not shared by calls that may overlap.  n = 0 is no error. */
+#define NVFP4_MAX_TOP 64
+size_t nvfp4_logprobs_workspace_bytes(int64_t n, int64_t vocab, int top);
+int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t vocab, int64_t stride, float scale,
+                   const int32_t *tokens, int given, float *logp, float *lse, float *entropy, int top,
+                   float *top_logp, int32_t *top_index, void *workspace, size_t workspace_bytes,
+                   hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
