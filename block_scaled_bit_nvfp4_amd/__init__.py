@@ -28,6 +28,7 @@ __all__ = [
     "nvfp4_kv_scale_bytes", "nvfp4_kv_append", "nvfp4_kv_read", "nvfp4_kv_attention_workspace_bytes",
     "nvfp4_kv_attention",
     "nvfp4_rope", "NVFP4_MAX_ROPE",
+    "nvfp4_kv_weights", "nvfp4_kv_evict",
     "nvfp4_logprobs_workspace_bytes", "nvfp4_logprobs", "NVFP4_MAX_TOP",
 ]
 
@@ -119,6 +120,8 @@ def load():
             "nvfp4_kv_attention_workspace_bytes": (sz, [P, P, i32]),
             "nvfp4_kv_attention": (i32, [P, P, P, i64, i32, f32, i32, P, P, i64, P, P, sz, P]),
             "nvfp4_rope": (i32, [P, i32, i32, i64, i32, i32, i32, P, i32, P, P, f32, P]),
+            "nvfp4_kv_weights": (i32, [P, P, P, i64, i32, f32, i32, P, P, f32, P, i64, P]),
+            "nvfp4_kv_evict": (i32, [P, P, i32, i32, i32, P, P, i64, P, P, P]),
             "nvfp4_logprobs_workspace_bytes": (sz, [i64, i64, i32]),
             "nvfp4_logprobs": (i32, [i32, P, i64, i64, i64, f32, P, i32, P, P, P, i32, P, P, P, sz, P]),
         }
@@ -598,6 +601,53 @@ def nvfp4_rope(rows, positions, freqs, axis=None, adjacent=False, factor=1.0, st
     _check(load().nvfp4_rope(arr, len(rows), _KV_DTYPE[first.dtype], tokens, dim, 2 * pairs, int(bool(adjacent)),
                              positions.data_ptr(), axes, freqs.data_ptr(), None if axis is None else axis.data_ptr(),
                              float(factor), _stream(stream, positions)), "nvfp4_rope")
+
+
+# ------------------------------------- eviction by gathered attention weight
+
+def _weights(name, t, cache, batch):
+    """Check a [seqs, heads, width] tensor of weights; its width."""
+    seqs = batch.arrays[0].shape[0]
+    if not (isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.dim() == 3 and t.is_contiguous() and
+            t.shape[0] == seqs and t.shape[1] == cache.heads and t.get_device() == cache._index):
+        raise ValueError("%s must be a contiguous float32 tensor [%d, %d, width] on %s" % (
+            name, seqs, cache.heads, cache.device))
+    return t.shape[2]
+
+
+def nvfp4_kv_weights(cache, batch, Q, scale, lse, weights, decay=1.0, window=0, tree=None, stream=None):
+    """Gather the attention that the cache's keys receive from the batch's new tokens: Q,
+    scale, window and tree as nvfp4_kv_attention took them, lse as it gave it; weights
+    float32 [seqs, heads, width], width at least the tokens that the page table can name."""
+    _kv_pair(cache, batch)
+    heads = Q.shape[1] if isinstance(Q, torch.Tensor) and Q.dim() == 3 else 0
+    qs = _rows("Q", Q, cache, batch, heads, _BF16[:1])
+    _flat("lse", lse, cache, torch.float32, batch.tokens * heads)
+    width = _weights("weights", weights, cache, batch)
+    if tree is not None:
+        _flat("tree", tree, cache, torch.int64, batch.tokens)
+    _check(load().nvfp4_kv_weights(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale),
+                                   _int32("window", window), None if tree is None else tree.data_ptr(),
+                                   lse.data_ptr(), float(decay), weights.data_ptr(), width,
+                                   _kv_stream(stream, cache)), "nvfp4_kv_weights")
+
+
+def nvfp4_kv_evict(cache, batch, weights, budget, kept, left, weights_out=None, first=0, recent=0, stream=None):
+    """Cut sequences that hold more than `budget` tokens (the batch's `past`) down to it:
+    of each head the first `first`, the last `recent` and the keys of the largest weights
+    stay, and move to the front.  kept int32 [seqs, heads, budget], left int32 [seqs] (may
+    be the batch's past), weights_out as weights, or None: in place."""
+    _kv_pair(cache, batch)
+    seqs, budget = batch.arrays[0].shape[0], _int32("budget", budget)
+    width = _weights("weights", weights, cache, batch)
+    if weights_out is not None and _weights("weights_out", weights_out, cache, batch) != width:
+        raise ValueError("weights_out is %d wide, weights %d" % (weights_out.shape[2], width))
+    _flat("kept", kept, cache, torch.int32, seqs * cache.heads * max(budget, 0))
+    _flat("left", left, cache, torch.int32, seqs)
+    _check(load().nvfp4_kv_evict(cache._ref, batch._ref, budget, _int32("first", first), _int32("recent", recent),
+                                 weights.data_ptr(), (weights if weights_out is None else weights_out).data_ptr(),
+                                 width, kept.data_ptr(), left.data_ptr(), _kv_stream(stream, cache)),
+           "nvfp4_kv_evict")
 
 
 # ---------------------------------------------------------- log probabilities

@@ -506,6 +506,57 @@ int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t vocab, int6
                    float *top_logp, int32_t *top_index, void *workspace, size_t workspace_bytes,
                    hipStream_t stream);
 
+/* ------------------------------------- eviction by gathered attention weight
+ * A cache that is kept within a budget: the attention that each cached key has
+ * received is gathered step by step (nvfp4_kv_weights), and the keys that gathered
+ * least leave the cache (nvfp4_kv_evict).  Both work on one key/value head by
+ * itself, so after an eviction the heads of a sequence hold tokens of different
+ * positions in the same slots; keys that are rotated by position carry it with
+ * them (nvfp4_rope), and attention over the slots stands as it is, but for windows,
+ * which then count slots.
+ *
+ * nvfp4_kv_weights: weights fp32 [seqs][heads][width], width at least
+ * table_width * page_tokens.  With the scores z and the allowed keys of
+ * nvfp4_kv_attention for the same batch, q, scale, window and tree, and lse as that
+ * call gave it,
+ *   weights[s][h][j] = decay * weights[s][h][j] (0 for j >= past[s])
+ *                      + sum over new tokens and query heads of head h of exp(z_j - lse)
+ * for every position j < past[s] + new; the rest is left alone, and so are sequences
+ * without new tokens.  decay is in 0..1; 1 gathers, 0 does not read what was there.
+ * Rows whose lse is not finite add
+ * nothing, nor do keys that hold a NaN or an infinity or have no page.  Scores
+ * accumulate in fp32, sums in fp32 in an order fixed by the arguments and the
+ * arrays' values: the same bits on every run.  Requirements and errors as
+ * nvfp4_kv_attention; weights and lse 4-byte aligned, a decay out of range
+ * NVFP4_EINVAL, a width too small NVFP4_ESHAPE. */
+int nvfp4_kv_weights(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, const uint16_t *q, int64_t q_stride,
+                     int q_heads, float scale, int window, const uint64_t *tree, const float *lse, float decay,
+                     float *weights, int64_t width, hipStream_t stream);
+
+/* Cut the sequences that hold more than `budget` tokens down to it.  The batch's
+ * past[s] tokens are what sequence s holds (its offsets and tokens are not read).
+ * Where past[s] > budget, each head keeps the first `first` positions, the last
+ * `recent` ones, and of those between the budget - first - recent with the largest
+ * weights (ties: the lowest position; NaN counts least), in their order:
+ *   kept int32 [seqs][heads][budget]  the kept positions, ascending; a sequence
+ *                                     within the budget has 0 .. past[s] - 1, then -1;
+ *   weights_out                       laid out as weights: those of the kept, moved
+ *                                     to slots 0 .. budget - 1 (may be weights itself,
+ *                                     else they do not overlap); the rest left alone;
+ *   left int32 [seqs]                 the tokens held now, min(past[s], budget) (may
+ *                                     be batch->past itself);
+ * and the codes and scales of the kept move to slots 0 .. budget - 1 of the same
+ * pages, byte for byte.  What stands behind them is left as it was, and the pages
+ * that hold no slot below the budget are free for other use.  A sequence some of
+ * whose past[s] positions have no page is left as it is: kept -1, weights moved
+ * nowhere, left[s] = past[s].  A page named by two sequences (a shared prefix)
+ * must not be in one that is cut.  budget >= 1, first, recent >= 0, first + recent <= budget (else
+ * NVFP4_EINVAL); budget at most 2^30 / (seqs * heads), and width at least
+ * table_width * page_tokens (else NVFP4_ESHAPE); arrays 4-byte aligned. */
+int nvfp4_kv_evict(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int budget, int first, int recent,
+                   const float *weights, float *weights_out, int64_t width, int32_t *kept, int32_t *left,
+                   hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif
