@@ -1,11 +1,6 @@
 // nvfp4_kv_weights.hip -- the attention that each cached key receives, gathered over
-// steps (gfx950).
-//
-// A wave holds 32 keys of a head as the A operand of v_mfma_f32_32x32x16_bf16 and walks
-// the query rows, 32 at a time, as B: a lane of the accumulator then has 16 keys' scores
-// of one row, whose log-sum-exp it holds too, and adds its weights to 16 running sums.
-// Only at the end are the sums of the 32 rows' lanes added.  Waves of a workgroup share
-// keys (each takes its part of the rows; their sums meet in shared memory) or rows.
+// steps (gfx950).  Two kernels: one streams keys past a few query rows (decode steps,
+// verifies), one streams the query rows of a chunk past keys that stay in registers.
 //
 // A weight is 2^(s * c - r) with c = scale * log2(e) and r = lse * log2(e), each rounded
 // to fp32; what that loses of the weights that count, those whose score is near lse, is
@@ -16,7 +11,7 @@
 namespace nvfp4 {
 
 constexpr int kWeighWaves = 4, kWeighThreads = kWeighWaves * kLanes;
-constexpr int kWeighTile = 32;             // keys of a wave's operand, rows of a step
+constexpr int kFewRows = 64;               // the most rows (new tokens x group) of a sequence for the first kernel
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
@@ -28,19 +23,229 @@ struct WeighArgs {
     float *weights;
     int64_t q_stride, width;
     int q_heads, group, window;
-    int row_waves;         // waves of a workgroup that share keys
+    uint32_t group_magic;  // (2^32 - 1) / group
+    int few_rows;          // sequences of at most so many rows are the first kernel's
+    int keys;              // of a workgroup of the first kernel
     float scale_log2;      // c as rounded
     float lost;            // (scale * log2(e) - c) / scale
     float decay;
 };
 
-// One 32-key operand of head `head` from position `key` on.
+// A row of a sequence's (new token, head of the group).
+struct WeighRow {
+    int i, g;
+    __device__ __forceinline__ WeighRow(const WeighArgs &a, int row) {
+        i = int(__umulhi(uint32_t(row), a.group_magic));     // the quotient, or one less
+        g = row - i * a.group;
+        const bool less = g >= a.group;
+        i += less;
+        g -= less ? a.group : 0;
+    }
+};
+
+// What turns a row's scores into weights.
+struct RowFacts {
+    float r, factor;
+};
+__device__ __forceinline__ bool counts(float lse) { return fabsf(lse) < __builtin_inff(); }
+__device__ __forceinline__ RowFacts row_facts(const WeighArgs &a, float lse) {
+    constexpr float kLog2eRest = 1.92596299e-8f;             // log2(e) - kLog2e
+    const bool in = counts(lse);
+    lse = in ? lse : 0.0f;
+    const float r = lse * kLog2e;
+    const float rest = __builtin_fmaf(lse, kLog2e, -r) + lse * kLog2eRest;
+    return RowFacts{r, in ? exp2_fast(__builtin_fmaf(lse, a.lost, -rest)) : 0.0f};
+}
+
+// The new weight of a key from what its rows add and what it had (0 for none); a key with
+// a NaN or an infinity, or without a page, adds nothing.
+__device__ __forceinline__ float gathered(float total, bool page, float old, float keep) {
+    if (!(total < __builtin_inff()) || !page) total = 0.0f;
+    return keep != 0.0f ? __builtin_fmaf(old, keep, total) : total;
+}
+
+// -------------------------------------------------------- keys past a few rows
+//
+// Q as the A operand of v_mfma_f32_16x16x32_bf16, RT tiles of 16 rows that stay in
+// registers, and keys, 32 of a wave's step, as B: a lane of the accumulator has four
+// rows' scores of one key, whose sum it takes with two exchanges between lanes for the
+// other rows.  Codes of the step to come are loaded ahead, the table's entries a step
+// before that.
+
+template <int D, int BITS>
+struct KeyTile {
+    typedef KvSide<D, BITS> S;
+    static constexpr int kLoads = S::kPieces / 4, kSlices = D / 32, kPer = S::kPieceDims / 8;
+    uint32_t w[2][kLoads][S::kPiece / 4], scale[2][(S::kBlocks + 3) / 4];
+    float old;
+    int has;               // which units have a page
+
+    // `weights`: read below position `held`.
+    __device__ __forceinline__ void load(const WeighArgs &a, int head, int key, int end, const int (&entry)[2],
+                                         const float *weights, int held) {
+        const int lane = threadIdx.x & 63, r = lane & 15;
+        has = 0;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int pos = key + u * kKvUnit;
+            const int page = pos < end ? a.kv.page_in(entry[u], pos) : -1;
+            has |= (page >= 0) << u;
+            const int64_t unit = a.kv.unit_of(max(page, 0), head, pos);
+            const uint8_t *codes = a.kv.codes[0] + unit * S::kUnitCodes + lane * S::kPiece;
+#pragma unroll
+            for (int j = 0; j < kLoads; ++j) load_words<S::kPiece>(codes + j * kLanes * S::kPiece, w[u][j]);
+            load_words<S::kBlocks>(a.kv.scales[0] + unit * S::kUnitScales + r * S::kBlocks, scale[u]);
+        }
+        old = 0.0f;
+        if (lane < 32 && key + lane < held) old = weights[key + lane];
+    }
+    __device__ __forceinline__ bf16x8 operand(int u, int m) const {
+        const int g = (threadIdx.x & 63) >> 4, j = m / kPer, e = m % kPer;
+        // the block of piece 4 j + g; the four lanes' blocks of a piece never cross a word
+        const int block = (4 * j + g) * S::kPieceDims / kMxBlock;
+        const float unit = unit_of_byte(scale[u][4 * j * S::kPieceDims / kMxBlock / 4], block & 3);
+        if constexpr (BITS == 8) return codes8(w[u][j][2 * e], w[u][j][2 * e + 1], unit);
+        else return codes4(w[u][j][e], unit);
+    }
+};
+
+// Sum over the lanes of the same column (lane % 16).
+__device__ __forceinline__ float column_sum(float v) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+template <int D, int BITS, int RT>
+__global__ void __launch_bounds__(kWeighThreads) weigh_few_kernel(WeighArgs a) {
+    typedef KeyTile<D, BITS> K;
+    constexpr int kStep = kWeighWaves * 32;
+    const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int head = blockIdx.y;
+    for (int s = blockIdx.z; s < a.kv.seqs; s += gridDim.z) {
+        int begin, stop, past;
+        a.kv.sequence(s, begin, stop, past);
+        const int n = stop - begin, rows = n * a.group, end = int(min(unsigned(past) + unsigned(n), unsigned(a.kv.capacity)));
+        if (n == 0 || rows > a.few_rows) continue;
+        float *const weights = a.weights + (int64_t(s) * a.kv.heads + head) * a.width;
+        const auto look_up = [&](int key, int (&entry)[2]) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) entry[u] = a.kv.entry_at_scalar(s, key + u * kKvUnit);
+        };
+        for (unsigned first = blockIdx.x * a.keys; first < unsigned(end); first += gridDim.x * a.keys) {
+            const int last = int(min(first + a.keys, unsigned(end)));
+            const int start = int(first) + wave * 32;
+            if (start >= last) break;
+            // more rows than the bounds said take more passes
+            for (int base = 0; base < rows; base += 16 * RT) {
+                const float keep = base == 0 ? a.decay : 1.0f;
+                const int held = base == 0 ? (a.decay != 0.0f ? past : 0) : end;
+                int key = start, entry[2];
+                K next;
+                look_up(key, entry);
+                next.load(a, head, key, end, entry, weights, held);
+                look_up(key + kStep, entry);
+                // the rows' operands and facts
+                bf16x8 q[RT][K::kSlices];
+                RowFacts fact[RT][4];
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const int row = base + 16 * t + c;
+                    const WeighRow w(a, min(row, rows - 1));
+                    const int64_t token = begin + w.i, qhead = head * a.group + w.g;
+                    const bool in = row < rows && counts(a.lse[token * a.q_heads + qhead]);
+                    const uint16_t *src = a.q + token * a.q_stride + qhead * D;
+#pragma unroll
+                    for (int m = 0; m < K::kSlices; ++m) {
+                        const int d = (4 * (m / K::kPer) + g) * K::S::kPieceDims + 8 * (m % K::kPer);
+                        u32x4 x = {0, 0, 0, 0};
+                        if (in) x = *reinterpret_cast<const u32x4 *>(src + d);
+                        q[t][m] = __builtin_bit_cast(bf16x8, x);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const int at = base + 16 * t + 4 * g + e;
+                        const WeighRow v(a, min(at, rows - 1));
+                        const float lse = a.lse[int64_t(begin + v.i) * a.q_heads + head * a.group + v.g];
+                        fact[t][e] = row_facts(a, at < rows ? lse : kNegInf);
+                    }
+                }
+                // the keys that every row sees
+                const int inner_lo = a.window > 0 ? past + n - a.window : 0, inner_hi = a.tree ? past : past + 1;
+                for (; key < last; key += kStep) {
+                    const K k = next;
+                    if (key + kStep < last) {
+                        next.load(a, head, key + kStep, end, entry, weights, held);
+                        look_up(key + 2 * kStep, entry);
+                    }
+                    const bool edge = key < inner_lo || min(key + 32, end) > inner_hi;
+                    float total[2];
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float sum = 0.0f;
+                        bf16x8 operand[K::kSlices];
+#pragma unroll
+                        for (int m = 0; m < K::kSlices; ++m) operand[m] = k.operand(u, m);
+#pragma unroll
+                        for (int t = 0; t < RT; ++t) {
+                            floatx4 x = {0, 0, 0, 0};
+#pragma unroll
+                            for (int m = 0; m < K::kSlices; ++m)
+                                x = __builtin_amdgcn_mfma_f32_16x16x32_bf16(q[t][m], operand[m], x, 0, 0, 0);
+                            float w[4];
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) w[e] = exp2_fast(__builtin_fmaf(x[e], a.scale_log2, -fact[t][e].r));
+                            if (edge) {
+                                const int j = key + 16 * u + c, bit = j - past;
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const int i = WeighRow(a, min(base + 16 * t + 4 * g + e, rows - 1)).i, pos = past + i;
+                                    bool seen = j <= pos && (a.window == 0 || j > pos - a.window);
+                                    if (a.tree && bit >= 0) seen = bit < min(n, 64) && a.tree[begin + i] >> (bit & 63) & 1;
+                                    w[e] = seen ? w[e] : 0.0f;
+                                }
+                            }
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) sum = __builtin_fmaf(w[e], fact[t][e].factor, sum);
+                        }
+                        total[u] = column_sum(sum);
+                    }
+                    const int at = key + lane;
+                    if (lane < 32 && at < end)
+                        weights[at] = gathered(lane < 16 ? total[0] : total[1], k.has >> (lane >> 4) & 1, k.old, keep);
+                }
+            }
+        }
+    }
+}
+
+// -------------------------------------------------------- rows past many keys
+//
+// A wave holds 64 keys as A operands of v_mfma_f32_32x32x16_bf16 and the workgroup walks
+// the query rows, 32 at a time, as B through shared memory: a lane of the accumulator has
+// 16 keys' scores of one row, whose log-sum-exp it holds too, and adds its weights to
+// running sums.  Only at the end are the sums of the 32 rows' lanes added.  RW waves of
+// the four share keys, each with its own rows; their sums meet in shared memory.
+//
+// A step's rows go straight to shared memory two steps ahead, into a ring of three, so
+// that one barrier a step is enough.  16-byte chunks of a row stand exchanged by the
+// row's number, without which the lanes of a read would meet in the same banks.
+
+constexpr int kWideKeys = 64;              // of a wave
+constexpr int kWideRows = 32;              // of a wave's step
+
+typedef __attribute__((address_space(1))) const void GlobalMem;
+typedef __attribute__((address_space(3))) void SharedMem;
+
+// A 32-key operand of head `head` from position `key` on.
 template <int D, int BITS>
 struct KeyOperand {
     typedef KvSide<D, BITS> S;
     static constexpr int kSteps = D / 16, kHalf = S::kPieces / 2, kPer = S::kPieceDims / 8;
     bf16x8 k[kSteps];
-    bool some[2];          // whether the first and the second 16 keys have a page
+    unsigned has;          // whether the first and the second 16 keys have a page
 
     // The element at which a lane's eight of step m start.
     static __device__ __forceinline__ int element(int m, int half) {
@@ -50,17 +255,14 @@ struct KeyOperand {
         const int lane = threadIdx.x & 63, r = lane & 15, half = lane >> 5;
         const int pos = key + (lane & 16);
         const int page = pos < end ? v.page_in(v.entry_at(s, pos), pos) : -1;
-        const unsigned long long has = __ballot(page >= 0);
-        some[0] = has & 1;
-        some[1] = has >> 16 & 1;
+        const unsigned long long lanes = __ballot(page >= 0);
+        has = unsigned(lanes & 1) | unsigned(lanes >> 15 & 2);
         const int64_t unit = v.unit_of(max(page, 0), head, pos);
-        uint32_t w[kHalf][S::kPiece / 4] = {}, scale[(S::kBlocks + 3) / 4] = {};
-        if (page >= 0) {
-            const uint8_t *codes = v.codes[0] + unit * S::kUnitCodes + (half * kKvUnit + r) * S::kPiece;
+        uint32_t w[kHalf][S::kPiece / 4], scale[(S::kBlocks + 3) / 4];
+        const uint8_t *codes = v.codes[0] + unit * S::kUnitCodes + (half * kKvUnit + r) * S::kPiece;
 #pragma unroll
-            for (int j = 0; j < kHalf; ++j) load_words<S::kPiece>(codes + 2 * j * kKvUnit * S::kPiece, w[j]);
-            load_words<S::kBlocks>(v.scales[0] + unit * S::kUnitScales + r * S::kBlocks, scale);
-        }
+        for (int j = 0; j < kHalf; ++j) load_words<S::kPiece>(codes + 2 * j * kKvUnit * S::kPiece, w[j]);
+        load_words<S::kBlocks>(v.scales[0] + unit * S::kUnitScales + r * S::kBlocks, scale);
 #pragma unroll
         for (int m = 0; m < kSteps; ++m) {
             const int j = m / kPer, e = m % kPer;
@@ -72,6 +274,19 @@ struct KeyOperand {
         }
     }
 };
+
+// Which of the 64 keys from position `key` on new token i (row `token` of the batch) sees.
+__device__ __forceinline__ unsigned long long seen_keys(const WeighArgs &a, int past, int n, int i, int token, int key) {
+    const auto below = [](int k) { return k <= 0 ? 0ull : k >= 64 ? ~0ull : (1ull << k) - 1; };
+    const int pos = past + i;
+    if (a.tree) {
+        const unsigned long long word = a.tree[token] & below(n);
+        const int d = past - key;
+        return below(d) | (d >= 64 || d <= -64 ? 0ull : d >= 0 ? word << d : word >> -d);
+    }
+    const unsigned long long old = a.window > 0 ? below(pos - a.window + 1 - key) : 0ull;
+    return below(pos + 1 - key) & ~old;
+}
 
 // The sum over the 32 lanes of each half of the wave of x[r], for the r that the lane's
 // low four bits are.
@@ -88,101 +303,187 @@ __device__ __forceinline__ float column_sums(const float (&x)[16]) {
     return v + __shfl_xor(v, 16);
 }
 
-template <int D, int BITS>
-__global__ void __launch_bounds__(kWeighThreads) kv_weights_kernel(WeighArgs a) {
+template <int D, int RW>
+struct WideShape {
+    static constexpr int kChunks = D / 8;                            // 16-byte chunks of a row
+    static constexpr int kStepRows = RW * kWideRows;
+    static constexpr int kRowBytes = kStepRows * D * 2;              // of a step's rows; their log-sum-exps stand behind
+    static constexpr int kStepBytes = kRowBytes + kStepRows * 4;
+    static constexpr int kLoads = kStepRows * kChunks / kWeighThreads;   // a thread's of a step's rows
+    static constexpr int kLds = 3 * kStepBytes;
+    // The place of chunk c of row r: rows 128 bytes apart take turns in pairs.
+    static __device__ __forceinline__ int place(int r, int c) {
+        return r * kChunks + (c ^ (D == 64 ? r >> 1 & 7 : r & 15));
+    }
+};
+
+template <int D, int BITS, int RW>
+__global__ void __launch_bounds__(kWeighThreads, 2) weigh_many_kernel(WeighArgs a) {
     typedef KeyOperand<D, BITS> K;
-    __shared__ float meet[kWeighThreads];
+    typedef WideShape<D, RW> W;
+    constexpr int kKeyWaves = kWeighWaves / RW;
+    constexpr unsigned kKeys = kKeyWaves * kWideKeys;
+    extern __shared__ __align__(16) uint8_t lds[];
     const int lane = threadIdx.x & 63, c = lane & 31, half = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int key_waves = kWeighWaves / a.row_waves;
-    const int key_wave = wave % key_waves, row_wave = wave / key_waves;
+    const int key_wave = wave % kKeyWaves, row_wave = wave / kKeyWaves;
     const int head = blockIdx.y;
-    const unsigned group_keys = key_waves * kWeighTile;
     for (int s = blockIdx.z; s < a.kv.seqs; s += gridDim.z) {
         int begin, stop, past;
         a.kv.sequence(s, begin, stop, past);
         const int n = stop - begin, rows = n * a.group, end = int(min(unsigned(past) + unsigned(n), unsigned(a.kv.capacity)));
-        if (n == 0) continue;
-        for (unsigned first = blockIdx.x * group_keys; first < unsigned(end); first += gridDim.x * group_keys) {
-            const int key = int(first) + key_wave * kWeighTile;
-            K k;
-            k.load(a.kv, s, head, key, end);
-            // the rows that may see some of the keys
-            const int i_lo = a.tree ? 0 : max(0, min(key, end) - past);
-            const int i_hi = a.window > 0 ? max(0, int(min(int64_t(n), int64_t(key) + kWeighTile - 1 + a.window - past))) : n;
-            const int row_lo = i_lo * a.group & ~(kWeighTile - 1), row_hi = key < end ? i_hi * a.group : 0;
-            float sum[16] = {};
-            for (int row0 = row_lo + row_wave * kWeighTile; row0 < row_hi; row0 += a.row_waves * kWeighTile) {
-                const int row = row0 + c;
-                const bool in = row < rows;
-                const int i = in ? row / a.group : 0, token = begin + i, qhead = head * a.group + (in ? row - i * a.group : 0);
-                const float lse = in ? a.lse[int64_t(token) * a.q_heads + qhead] : kNegInf;
-                const bool counts = fabsf(lse) < __builtin_inff();
-                const uint16_t *src = a.q + token * a.q_stride + qhead * D;
-                bf16x8 q[K::kSteps];
+        if (n == 0 || rows <= a.few_rows) continue;
+        const uint16_t *const q = a.q + int64_t(begin) * a.q_stride + head * a.group * D;
+        const float *const lses = a.lse + int64_t(begin) * a.q_heads + head * a.group;
+        for (unsigned first = blockIdx.x * kKeys; first < unsigned(end); first += gridDim.x * kKeys) {
+            const int key = int(first) + key_wave * kWideKeys;
+            K k[2];
 #pragma unroll
-                for (int m = 0; m < K::kSteps; ++m) {
-                    u32x4 w = {0, 0, 0, 0};
-                    if (counts) w = *reinterpret_cast<const u32x4 *>(src + K::element(m, half));
-                    q[m] = __builtin_bit_cast(bf16x8, w);
+            for (int u = 0; u < 2; ++u) k[u].load(a.kv, s, head, key + 32 * u, end);
+            // the rows that may see some of the workgroup's keys
+            const int i_lo = a.tree ? 0 : max(0, int(first) - past);
+            const int i_hi = a.window > 0 ? max(0, int(min(int64_t(n), int64_t(first) + kKeys - 1 + a.window - past))) : n;
+            const int row_lo = i_lo * a.group & ~(kWideRows - 1), row_hi = i_hi * a.group;
+            float sum[2][16] = {};
+            // the rows that see all of the wave's keys
+            const int64_t full_lo = a.tree ? (key + kWideKeys <= past ? 0 : rows) : int64_t(key + kWideKeys - 1 - past) * a.group;
+            const int64_t full_hi = a.window > 0 ? (int64_t(key) + a.window - past) * a.group : rows;
+
+            // a step's rows and log-sum-exps on their way to shared memory
+            const auto send = [&](int row0, int slot) {
+#pragma unroll
+                for (int l = 0; l < W::kLoads; ++l) {
+                    const int p = l * kWeighThreads + threadIdx.x, r = p / W::kChunks;
+                    const int chunk = W::place(r, p % W::kChunks) % W::kChunks;      // the exchange is its own inverse
+                    const WeighRow w(a, min(row0 + r, rows - 1));
+                    const uint16_t *from = q + w.i * a.q_stride + w.g * D + chunk * 8;
+                    __builtin_amdgcn_global_load_lds((GlobalMem *)from,
+                                                     (SharedMem *)(lds + slot * W::kStepBytes + (l * kWeighThreads + wave * kLanes) * 16),
+                                                     16, 0, 0);
                 }
-                floatx16 x = {};
+                if (lane < W::kStepRows / kWeighWaves) {
+                    const WeighRow w(a, min(row0 + wave * (W::kStepRows / kWeighWaves) + lane, rows - 1));
+                    __builtin_amdgcn_global_load_lds((GlobalMem *)(lses + int64_t(w.i) * a.q_heads + w.g),
+                                                     (SharedMem *)(lds + slot * W::kStepBytes + W::kRowBytes + wave * W::kStepRows),
+                                                     4, 0, 0);
+                }
+            };
+            __syncthreads();                           // the ring's last readers
+            if (row_lo < row_hi) send(row_lo, 0);
+            if (row_lo + W::kStepRows < row_hi) send(row_lo + W::kStepRows, 1);
+            int slot = 0;
+            for (int row0 = row_lo; row0 < row_hi; row0 += W::kStepRows) {
+                // This step's loads have come, the next one's may be on their way: a bare barrier,
+                // since a fence would wait for them too.
+                if (row0 + W::kStepRows < row_hi) __builtin_amdgcn_s_waitcnt(kWaitLoads | (W::kLoads + 1));
+                else __builtin_amdgcn_s_waitcnt(kWaitLoads);
+                asm volatile("s_barrier" ::: "memory");
+                if (row0 + 2 * W::kStepRows < row_hi) send(row0 + 2 * W::kStepRows, slot == 0 ? 2 : slot - 1);
+                const int tile0 = row0 + row_wave * kWideRows;
+                const uint8_t *const tile = lds + slot * W::kStepBytes + row_wave * kWideRows * D * 2;
+                const float mine = *reinterpret_cast<const float *>(lds + slot * W::kStepBytes + W::kRowBytes +
+                                                                    (row_wave * kWideRows + c) * 4);
+                slot = slot == 2 ? 0 : slot + 1;
+                floatx16 x[2] = {};
 #pragma unroll
-                for (int m = 0; m < K::kSteps; ++m) x = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k.k[m], q[m], x, 0, 0, 0);
-                constexpr float kLog2eRest = 1.92596299e-8f;       // log2(e) - kLog2e
-                const float r = counts ? lse * kLog2e : 0.0f;
-                const float rest = __builtin_fmaf(lse, kLog2e, -r) + lse * kLog2eRest;
-                const float factor = counts ? exp2_fast(__builtin_fmaf(lse, a.lost, -rest)) : 0.0f;
-                float w[16];
+                for (int m0 = 0; m0 < K::kSteps; m0 += 4) {
+                    bf16x8 b[4];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) w[e] = exp2_fast(__builtin_fmaf(x[e], a.scale_log2, -r));
-                // where not every row sees every key
-                const int pos = past + i;
-                const int i0 = __builtin_amdgcn_readfirstlane(i), i1 = min(row0 + kWeighTile, rows) - 1;
-                const bool whole = a.tree ? key + kWeighTile <= past
-                                          : key + kWeighTile - 1 <= past + i0 && (a.window == 0 || key > past + i1 / a.group - a.window);
-                if (!whole) {
-                    const int at = key + 4 * half;
-                    if (a.tree) {
-                        const unsigned long long tree = in ? a.tree[token] : 0ull;
-                        const int drafted = min(n, 64);
+                    for (int m = 0; m < 4; ++m)
+                        b[m] = *reinterpret_cast<const bf16x8 *>(tile + W::place(c, K::element(m0 + m, half) / 8) * 16);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+                            x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[u].k[m0 + m], b[m], x[u], 0, 0, 0);
+                }
+                const bool in = counts(mine) && tile0 + c < rows;
+                const RowFacts f = row_facts(a, in ? mine : kNegInf);
+                float w[2][16];
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) w[u][e] = exp2_fast(__builtin_fmaf(x[u][e], a.scale_log2, -f.r));
+                // where not every row sees every key, or some row does not count
+                if (tile0 < full_lo || tile0 + kWideRows > full_hi || !__all(in)) {
+                    const int i = WeighRow(a, min(tile0 + c, rows - 1)).i;
+                    unsigned long long seen = in ? seen_keys(a, past, n, i, begin + i, key) : 0ull;
+                    seen >>= 4 * half;
+#pragma unroll
+                    for (int u = 0; u < 2; ++u)
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
-                            const int j = at + 8 * (e / 4) + e % 4 - past;
-                            w[e] = j < 0 || (j < drafted && tree >> (j & 63) & 1) ? w[e] : 0.0f;
+                            const int bit = __builtin_amdgcn_sbfe(int(seen >> 32 * u), 8 * (e / 4) + e % 4, 1);
+                            w[u][e] = __uint_as_float(__float_as_uint(w[u][e]) & uint32_t(bit));
                         }
-                    } else {
-                        const int lo = a.window > 0 ? pos - a.window : -1;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int j = at + 8 * (e / 4) + e % 4;
-                            w[e] = j <= pos && j > lo ? w[e] : 0.0f;
-                        }
-                    }
                 }
 #pragma unroll
-                for (int e = 0; e < 16; ++e) sum[e] = __builtin_fmaf(w[e], factor, sum[e]);
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) sum[u][e] = __builtin_fmaf(w[u][e], f.factor, sum[u][e]);
             }
-            float total = column_sums(sum);
-            // the lane's key of the wave's 32
-            const int mine = 8 * (lane >> 2 & 3) + 4 * half + (lane & 3);
-            if (a.row_waves > 1) {
-                __syncthreads();                       // of the tile before
-                if ((lane & 16) == 0) meet[wave * kWeighTile + mine] = total;
+            // lanes with bit 4 clear take the sums of the first 32 keys, the others those of the second
+            const float both[2] = {column_sums(sum[0]), column_sums(sum[1])};
+            const int u = lane >> 4 & 1, of_tile = 8 * (lane >> 2 & 3) + 4 * half + (lane & 3);
+            float total = u ? both[1] : both[0];
+            const unsigned has = (u ? k[1].has : k[0].has) >> (of_tile >> 4);
+            const int of_wave = 32 * u + of_tile;
+            if constexpr (RW > 1) {
+                float *const meet = reinterpret_cast<float *>(lds);
+                __syncthreads();                       // the last step's readers
+                meet[wave * kWideKeys + of_wave] = total;
                 __syncthreads();
                 total = 0.0f;
-                for (int w = 0; w < a.row_waves; ++w) total += meet[(w * key_waves + key_wave) * kWeighTile + mine];
+#pragma unroll
+                for (int w = 0; w < RW; ++w) total += meet[(w * kKeyWaves + key_wave) * kWideKeys + of_wave];
             }
-            const int at = key + mine;
-            if (row_wave == 0 && (lane & 16) == 0 && at < end) {
-                // a key with a NaN or an infinity, or without a page, adds nothing
-                if (!(total < __builtin_inff()) || !k.some[mine >> 4]) total = 0.0f;
-                float *to = a.weights + (int64_t(s) * a.kv.heads + head) * a.width + at;
-                if (a.decay != 0.0f && at < past) total = __builtin_fmaf(*to, a.decay, total);
-                *to = total;
+            const int at = key + of_wave;
+            if (row_wave == 0 && at < end) {
+                float *const to = a.weights + (int64_t(s) * a.kv.heads + head) * a.width + at;
+                const float old = a.decay != 0.0f && at < past ? *to : 0.0f;
+                *to = gathered(total, has & 1, old, a.decay);
             }
         }
     }
+}
+
+// Workgroups along a launch's x for `tiles`; what is past them, and past the bounds, the
+// workgroups walk.
+static dim3 weigh_grid(const WeighArgs &a, int64_t tiles) {
+    const int64_t most = 1 << 20;
+    return dim3(unsigned(tiles < 1 ? 1 : tiles < most ? tiles : most), a.kv.heads, a.kv.seqs < 65535 ? a.kv.seqs : 65535);
+}
+
+constexpr int kFewGroups = 1024, kFewMostKeys = 2048;
+
+template <int D, int BITS>
+static int launch_few(WeighArgs &a, int64_t context, int64_t most_rows, hipStream_t stream) {
+    const int64_t items = int64_t(a.kv.seqs) * a.kv.heads, each = ceil_div(context * items, kFewGroups);
+    a.keys = int(ceil_div(each < 1 ? 1 : each > kFewMostKeys ? kFewMostKeys : each, 128) * 128);
+    const dim3 grid = weigh_grid(a, ceil_div(context, a.keys));
+    if (most_rows <= 16) weigh_few_kernel<D, BITS, 1><<<grid, kWeighThreads, 0, stream>>>(a);
+    else if (most_rows <= 32) weigh_few_kernel<D, BITS, 2><<<grid, kWeighThreads, 0, stream>>>(a);
+    else weigh_few_kernel<D, BITS, 4><<<grid, kWeighThreads, 0, stream>>>(a);
+    return launch_status();
+}
+
+template <int D, int BITS, int RW>
+static int launch_many_as(const WeighArgs &a, int64_t context, hipStream_t stream) {
+    typedef WideShape<D, RW> W;
+    if constexpr (W::kLds > 64 * 1024)
+        if (!raise_lds<weigh_many_kernel<D, BITS, RW>>(W::kLds)) return NVFP4_EHIP;
+    const dim3 grid = weigh_grid(a, ceil_div(context, kWeighWaves / RW * kWideKeys));
+    weigh_many_kernel<D, BITS, RW><<<grid, kWeighThreads, W::kLds, stream>>>(a);
+    return launch_status();
+}
+
+template <int D, int BITS>
+static int launch_many(const WeighArgs &a, int64_t context, hipStream_t stream) {
+    // Waves share keys where there are not enough of them to give every CU two workgroups.
+    const int64_t groups = ceil_div(context, kWeighWaves * kWideKeys) * a.kv.heads * a.kv.seqs;
+    if (groups >= 512) return launch_many_as<D, BITS, 1>(a, context, stream);
+    if (groups >= 256 || D == 256) return launch_many_as<D, BITS, 2>(a, context, stream);
+    return launch_many_as<D, BITS, D == 256 ? 2 : 4>(a, context, stream);
 }
 
 }  // namespace nvfp4
@@ -209,22 +510,25 @@ NVFP4_API int nvfp4_kv_weights(const nvfp4_kv_cache *cache, const nvfp4_kv_batch
     a.width = width;
     a.q_heads = q_heads;
     a.group = q_heads / cache->heads;
+    a.group_magic = 0xFFFFFFFFu / uint32_t(a.group);
     a.window = window;
     const double c = double(scale) * 1.4426950408889634074;
     a.scale_log2 = float(c);
     a.lost = float((c - a.scale_log2) / scale);
     a.decay = decay;
+    a.keys = 0;
+    // Which kernels, by the bounds: that for few rows alone, that for many alone where all
+    // sequences are as long, or each for its own sequences.
     const int64_t most_rows = int64_t(batch->max_new > 1 ? batch->max_new : 1) * a.group;
-    a.row_waves = most_rows > 64 ? kWeighWaves : 1;
-    const int keys = kWeighWaves / a.row_waves * kWeighTile;
-    const int context = batch->max_context < a.kv.capacity ? batch->max_context : a.kv.capacity;
-    // workgroups walk what is past the grid, and past the bounds
-    const int64_t tiles = ceil_div(context > 1 ? context : 1, keys), most = 1 << 20;
-    const dim3 grid(unsigned(tiles < most ? tiles : most), cache->heads, batch->seqs < 65535 ? batch->seqs : 65535);
+    const bool even = batch->tokens == int64_t(batch->seqs) * batch->max_new;      // all of the same length
+    a.few_rows = most_rows <= kFewRows ? 0x7FFFFFFF : even ? -1 : kFewRows;
+    const int64_t context = batch->max_context < a.kv.capacity ? batch->max_context : a.kv.capacity;
     return kv_dim(cache->head_dim, [&](auto dim) {
         return kv_bits(cache->k_format, [&](auto bits) {
-            kv_weights_kernel<decltype(dim)::value, decltype(bits)::value><<<grid, kWeighThreads, 0, stream>>>(a);
-            return launch_status();
+            constexpr int D = decltype(dim)::value, BITS = decltype(bits)::value;
+            if (most_rows <= kFewRows || !even)
+                if (int st = launch_few<D, BITS>(a, context, most_rows, stream)) return st;
+            return most_rows > kFewRows ? launch_many<D, BITS>(a, context, stream) : NVFP4_OK;
         });
     });
 }
