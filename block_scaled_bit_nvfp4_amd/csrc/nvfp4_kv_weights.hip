@@ -25,7 +25,6 @@ struct WeighArgs {
     int q_heads, group, window;
     uint32_t group_magic;  // (2^32 - 1) / group
     int few_rows;          // sequences of at most so many rows are the first kernel's
-    int keys;              // of a workgroup of the first kernel
     float scale_log2;      // c as rounded
     float lost;            // (scale * log2(e) - c) / scale
     float decay;
@@ -42,6 +41,15 @@ struct WeighRow {
         g -= less ? a.group : 0;
     }
 };
+
+// KvView::sequence by scalar loads, for `s` that is the same in the whole wave.
+__device__ __forceinline__ void sequence(const KvView &v, int s, int &begin, int &end, int &before) {
+    typedef __attribute__((address_space(4))) const int32_t Constant;
+    s = __builtin_amdgcn_readfirstlane(s);
+    begin = min(max(((Constant *)v.offsets)[s], 0), v.tokens);
+    end = min(max(((Constant *)v.offsets)[s + 1], begin), v.tokens);
+    before = min(max(((Constant *)v.past)[s], 0), v.capacity);
+}
 
 // What turns a row's scores into weights.
 struct RowFacts {
@@ -69,8 +77,21 @@ __device__ __forceinline__ float gathered(float total, bool page, float old, flo
 // Q as the A operand of v_mfma_f32_16x16x32_bf16, RT tiles of 16 rows that stay in
 // registers, and keys, 32 of a wave's step, as B: a lane of the accumulator has four
 // rows' scores of one key, whose sum it takes with two exchanges between lanes for the
-// other rows.  Codes of the step to come are loaded ahead, the table's entries a step
-// before that.
+// other rows.  Workgroups take equal shares of all sequences' steps (64 ragged sequences
+// 33.6 us, in pieces of 2048 keys 46.8).  Codes of the two steps to come are loaded ahead, past the caches, the
+// table's entries a step before that.
+
+// A load of BYTES that nobody repeats.
+template <int BYTES>
+__device__ __forceinline__ void load_once(const uint8_t *p, uint32_t *w) {
+    if constexpr (BYTES == 16) {
+        const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(p));
+        w[0] = t[0]; w[1] = t[1]; w[2] = t[2]; w[3] = t[3];
+    } else {
+        const u32x2 t = __builtin_nontemporal_load(reinterpret_cast<const u32x2 *>(p));
+        w[0] = t[0]; w[1] = t[1];
+    }
+}
 
 template <int D, int BITS>
 struct KeyTile {
@@ -80,24 +101,24 @@ struct KeyTile {
     float old;
     int has;               // which units have a page
 
-    // `weights`: read below position `held`.
-    __device__ __forceinline__ void load(const WeighArgs &a, int head, int key, int end, const int (&entry)[2],
-                                         const float *weights, int held) {
+    // The tile at `key` of keys before `last`; past them any tile.  `weights`: any of the
+    // sequence's where the tile is past `last`.
+    __device__ __forceinline__ void load(const WeighArgs &a, int head, int key, int last, const int (&entry)[2],
+                                         const float *weights) {
         const int lane = threadIdx.x & 63, r = lane & 15;
         has = 0;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int pos = key + u * kKvUnit;
-            const int page = pos < end ? a.kv.page_in(entry[u], pos) : -1;
-            has |= (page >= 0) << u;
-            const int64_t unit = a.kv.unit_of(max(page, 0), head, pos);
+            const bool some = pos < last && uint32_t(entry[u]) < uint32_t(a.kv.pages);
+            has |= int(some) << u;
+            const int64_t unit = a.kv.unit_of(some ? entry[u] : 0, head, some ? pos : 0);
             const uint8_t *codes = a.kv.codes[0] + unit * S::kUnitCodes + lane * S::kPiece;
 #pragma unroll
-            for (int j = 0; j < kLoads; ++j) load_words<S::kPiece>(codes + j * kLanes * S::kPiece, w[u][j]);
+            for (int j = 0; j < kLoads; ++j) load_once<S::kPiece>(codes + j * kLanes * S::kPiece, w[u][j]);
             load_words<S::kBlocks>(a.kv.scales[0] + unit * S::kUnitScales + r * S::kBlocks, scale[u]);
         }
-        old = 0.0f;
-        if (lane < 32 && key + lane < held) old = weights[key + lane];
+        old = weights[min(key + (lane & 31), last - 1)];
     }
     __device__ __forceinline__ bf16x8 operand(int u, int m) const {
         const int g = (threadIdx.x & 63) >> 4, j = m / kPer, e = m % kPer;
@@ -118,68 +139,99 @@ __device__ __forceinline__ float column_sum(float v) {
 }
 
 template <int D, int BITS, int RT>
-__global__ void __launch_bounds__(kWeighThreads) weigh_few_kernel(WeighArgs a) {
+__global__ void __launch_bounds__(kWeighThreads, RT * D <= 128 ? 4 : RT * D <= 256 ? 2 : 1) weigh_few_kernel(WeighArgs a) {
     typedef KeyTile<D, BITS> K;
     constexpr int kStep = kWeighWaves * 32;
+    __shared__ unsigned long long words[kWeighWaves][16 * RT];       // each wave's rows' trees
     const int lane = threadIdx.x & 63, c = lane & 15, g = lane >> 4;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int head = blockIdx.y;
-    for (int s = blockIdx.z; s < a.kv.seqs; s += gridDim.z) {
-        int begin, stop, past;
-        a.kv.sequence(s, begin, stop, past);
-        const int n = stop - begin, rows = n * a.group, end = int(min(unsigned(past) + unsigned(n), unsigned(a.kv.capacity)));
-        if (n == 0 || rows > a.few_rows) continue;
-        float *const weights = a.weights + (int64_t(s) * a.kv.heads + head) * a.width;
-        const auto look_up = [&](int key, int (&entry)[2]) {
+    // The workgroup's share of the head's steps, those of one sequence after another: the
+    // lanes hold 64 sequences' facts at a time.
+    int begins, stops, pasts, steps, upto;
+    const auto sequences = [&](int base) {
+        const int s = min(base + lane, a.kv.seqs - 1);
+        a.kv.sequence(s, begins, stops, pasts);
+        const int rows = (stops - begins) * a.group;
+        const bool mine = base + lane < a.kv.seqs && rows > 0 && rows <= a.few_rows;
+        steps = mine ? int((min(unsigned(pasts) + unsigned(stops - begins), unsigned(a.kv.capacity)) + kStep - 1) / kStep) : 0;
+        upto = steps;
 #pragma unroll
-            for (int u = 0; u < 2; ++u) entry[u] = a.kv.entry_at_scalar(s, key + u * kKvUnit);
-        };
-        for (unsigned first = blockIdx.x * a.keys; first < unsigned(end); first += gridDim.x * a.keys) {
-            const int last = int(min(first + a.keys, unsigned(end)));
-            const int start = int(first) + wave * 32;
-            if (start >= last) break;
+        for (int d = 1; d < kLanes; d <<= 1) {
+            const int v = __shfl_up(upto, d);
+            upto += lane >= d ? v : 0;
+        }
+        return __builtin_amdgcn_readlane(upto, 63);
+    };
+    uint64_t all = 0;
+    int here = 0;
+    for (int base = 0; base < a.kv.seqs; base += kLanes) all += uint64_t(here = sequences(base));
+    uint64_t at = all * blockIdx.x / gridDim.x;
+    const uint64_t to = all * (blockIdx.x + 1) / gridDim.x;
+    uint64_t before = 0;
+    for (int base = 0; at < to; base += kLanes) {
+        if (a.kv.seqs > kLanes) here = sequences(base);
+        while (at < to && at < before + uint64_t(here)) {
+            const int rel = int(at - before), l = __popcll(__ballot(upto <= rel));
+            const int s = base + l;
+            const int begin = __builtin_amdgcn_readlane(begins, l), past = __builtin_amdgcn_readlane(pasts, l);
+            const int n = __builtin_amdgcn_readlane(stops, l) - begin, rows = n * a.group;
+            const int end = int(min(unsigned(past) + unsigned(n), unsigned(a.kv.capacity)));
+            const int own = __builtin_amdgcn_readlane(steps, l), done = rel - (__builtin_amdgcn_readlane(upto, l) - own);
+            const int take = int(min(uint64_t(own - done), to - at));
+            const int last = min((done + take) * kStep, end);
+            at += take;
+            float *const weights = a.weights + (int64_t(s) * a.kv.heads + head) * a.width;
+            const auto look_up = [&](int key, int (&entry)[2]) {
+#pragma unroll
+                for (int u = 0; u < 2; ++u) entry[u] = a.kv.entry_at_scalar(s, key + u * kKvUnit);
+            };
+            const int start = done * kStep + wave * 32;
+            if (start >= last) continue;
             // more rows than the bounds said take more passes
             for (int base = 0; base < rows; base += 16 * RT) {
                 const float keep = base == 0 ? a.decay : 1.0f;
                 const int held = base == 0 ? (a.decay != 0.0f ? past : 0) : end;
                 int key = start, entry[2];
-                K next;
+                K tile[2];
                 look_up(key, entry);
-                next.load(a, head, key, end, entry, weights, held);
+                tile[0].load(a, head, key, last, entry, weights);
                 look_up(key + kStep, entry);
+                tile[1].load(a, head, key + kStep, last, entry, weights);
+                look_up(key + 2 * kStep, entry);
                 // the rows' operands and facts
                 bf16x8 q[RT][K::kSlices];
                 RowFacts fact[RT][4];
+                float lse[RT][5];          // of the lane's four rows of the accumulator, and of its row of the operand
 #pragma unroll
                 for (int t = 0; t < RT; ++t) {
-                    const int row = base + 16 * t + c;
-                    const WeighRow w(a, min(row, rows - 1));
+                    const WeighRow w(a, min(base + 16 * t + c, rows - 1));
                     const int64_t token = begin + w.i, qhead = head * a.group + w.g;
-                    const bool in = row < rows && counts(a.lse[token * a.q_heads + qhead]);
                     const uint16_t *src = a.q + token * a.q_stride + qhead * D;
 #pragma unroll
                     for (int m = 0; m < K::kSlices; ++m) {
                         const int d = (4 * (m / K::kPer) + g) * K::S::kPieceDims + 8 * (m % K::kPer);
-                        u32x4 x = {0, 0, 0, 0};
-                        if (in) x = *reinterpret_cast<const u32x4 *>(src + d);
-                        q[t][m] = __builtin_bit_cast(bf16x8, x);
+                        q[t][m] = *reinterpret_cast<const bf16x8 *>(src + d);
                     }
+                    lse[t][4] = a.lse[token * a.q_heads + qhead];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int at = base + 16 * t + 4 * g + e;
-                        const WeighRow v(a, min(at, rows - 1));
-                        const float lse = a.lse[int64_t(begin + v.i) * a.q_heads + head * a.group + v.g];
-                        fact[t][e] = row_facts(a, at < rows ? lse : kNegInf);
+                        const WeighRow v(a, min(base + 16 * t + 4 * g + e, rows - 1));
+                        lse[t][e] = a.lse[int64_t(begin + v.i) * a.q_heads + head * a.group + v.g];
                     }
+                    if (a.tree) words[wave][16 * t + c] = a.tree[token];
+                }
+#pragma unroll
+                for (int t = 0; t < RT; ++t) {
+                    const bool in = base + 16 * t + c < rows && counts(lse[t][4]);
+#pragma unroll
+                    for (int m = 0; m < K::kSlices; ++m) q[t][m] = in ? q[t][m] : bf16x8{};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) fact[t][e] = row_facts(a, base + 16 * t + 4 * g + e < rows ? lse[t][e] : kNegInf);
                 }
                 // the keys that every row sees
                 const int inner_lo = a.window > 0 ? past + n - a.window : 0, inner_hi = a.tree ? past : past + 1;
-                for (; key < last; key += kStep) {
-                    const K k = next;
-                    if (key + kStep < last) {
-                        next.load(a, head, key + kStep, end, entry, weights, held);
-                        look_up(key + 2 * kStep, entry);
-                    }
+                const auto work = [&](const K &k, int key) {
                     const bool edge = key < inner_lo || min(key + 32, end) > inner_hi;
                     float total[2];
 #pragma unroll
@@ -203,7 +255,7 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_few_kernel(WeighArgs a) {
                                 for (int e = 0; e < 4; ++e) {
                                     const int i = WeighRow(a, min(base + 16 * t + 4 * g + e, rows - 1)).i, pos = past + i;
                                     bool seen = j <= pos && (a.window == 0 || j > pos - a.window);
-                                    if (a.tree && bit >= 0) seen = bit < min(n, 64) && a.tree[begin + i] >> (bit & 63) & 1;
+                                    if (a.tree && bit >= 0) seen = bit < min(n, 64) && words[wave][16 * t + 4 * g + e] >> (bit & 63) & 1;
                                     w[e] = seen ? w[e] : 0.0f;
                                 }
                             }
@@ -213,11 +265,21 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_few_kernel(WeighArgs a) {
                         total[u] = column_sum(sum);
                     }
                     const int at = key + lane;
-                    if (lane < 32 && at < end)
-                        weights[at] = gathered(lane < 16 ? total[0] : total[1], k.has >> (lane >> 4) & 1, k.old, keep);
+                    if (lane < 32 && at < last)
+                        weights[at] = gathered(lane < 16 ? total[0] : total[1], k.has >> (lane >> 4) & 1, at < held ? k.old : 0.0f, keep);
+                };
+                for (; key < last; key += 2 * kStep) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        work(tile[t], key + t * kStep);
+                        if (key + (t + 1) * kStep >= last) break;
+                        tile[t].load(a, head, key + (2 + t) * kStep, last, entry, weights);
+                        look_up(key + (3 + t) * kStep, entry);
+                    }
                 }
             }
         }
+        before += uint64_t(here);
     }
 }
 
@@ -330,7 +392,7 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_many_kernel(WeighArgs 
     const int head = blockIdx.y;
     for (int s = blockIdx.z; s < a.kv.seqs; s += gridDim.z) {
         int begin, stop, past;
-        a.kv.sequence(s, begin, stop, past);
+        sequence(a.kv, s, begin, stop, past);
         const int n = stop - begin, rows = n * a.group, end = int(min(unsigned(past) + unsigned(n), unsigned(a.kv.capacity)));
         if (n == 0 || rows <= a.few_rows) continue;
         const uint16_t *const q = a.q + int64_t(begin) * a.q_stride + head * a.group * D;
@@ -447,6 +509,8 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_many_kernel(WeighArgs 
     }
 }
 
+constexpr int kFewFill = 4096;
+
 // Workgroups along a launch's x for `tiles`; what is past them, and past the bounds, the
 // workgroups walk.
 static dim3 weigh_grid(const WeighArgs &a, int64_t tiles) {
@@ -454,13 +518,14 @@ static dim3 weigh_grid(const WeighArgs &a, int64_t tiles) {
     return dim3(unsigned(tiles < 1 ? 1 : tiles < most ? tiles : most), a.kv.heads, a.kv.seqs < 65535 ? a.kv.seqs : 65535);
 }
 
-constexpr int kFewGroups = 1024, kFewMostKeys = 2048;
-
 template <int D, int BITS>
-static int launch_few(WeighArgs &a, int64_t context, int64_t most_rows, hipStream_t stream) {
-    const int64_t items = int64_t(a.kv.seqs) * a.kv.heads, each = ceil_div(context * items, kFewGroups);
-    a.keys = int(ceil_div(each < 1 ? 1 : each > kFewMostKeys ? kFewMostKeys : each, 128) * 128);
-    const dim3 grid = weigh_grid(a, ceil_div(context, a.keys));
+static int launch_few(const WeighArgs &a, int64_t context, int64_t most_rows, hipStream_t stream) {
+    const int64_t steps = ceil_div(context, kWeighWaves * 32) * a.kv.seqs, all = steps * a.kv.heads;
+    // Two workgroups a CU, or as many as fit where there are steps for them (32000 keys of 8
+    // heads 9.5 us, with four 10.2; 64 sequences of 4095 keys 32.6, with two 37.1): with
+    // more than one tile of rows two fit (8 tokens over 16385 keys 14.7 us, with four 23.5).
+    const int64_t groups = all < kFewFill || most_rows > 16 ? 512 : 1024, each = ceil_div(groups, a.kv.heads);
+    const dim3 grid(unsigned(steps < 1 ? 1 : steps < each ? steps : each), a.kv.heads);
     if (most_rows <= 16) weigh_few_kernel<D, BITS, 1><<<grid, kWeighThreads, 0, stream>>>(a);
     else if (most_rows <= 32) weigh_few_kernel<D, BITS, 2><<<grid, kWeighThreads, 0, stream>>>(a);
     else weigh_few_kernel<D, BITS, 4><<<grid, kWeighThreads, 0, stream>>>(a);
@@ -516,7 +581,6 @@ NVFP4_API int nvfp4_kv_weights(const nvfp4_kv_cache *cache, const nvfp4_kv_batch
     a.scale_log2 = float(c);
     a.lost = float((c - a.scale_log2) / scale);
     a.decay = decay;
-    a.keys = 0;
     // Which kernels, by the bounds: that for few rows alone, that for many alone where all
     // sequences are as long, or each for its own sequences.
     const int64_t most_rows = int64_t(batch->max_new > 1 ? batch->max_new : 1) * a.group;
