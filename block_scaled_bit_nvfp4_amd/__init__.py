@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 
 import torch
@@ -62,12 +63,6 @@ class _KvBatch(ctypes.Structure):
     """struct nvfp4_kv_batch of nvfp4.h."""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("page_table", "offsets", "past")] + [("tokens", ctypes.c_int64)] +
                 [(n, ctypes.c_int32) for n in ("seqs", "table_width", "max_new", "max_context")])
-
-
-class _RopeRows(ctypes.Structure):
-    """struct nvfp4_rope_rows of nvfp4.h."""
-    _fields_ = ([("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_stride", ctypes.c_int64),
-                 ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32), ("out_type", ctypes.c_int32)])
 
 
 class NVFP4Error(RuntimeError):
@@ -436,7 +431,7 @@ class KvBatch:
                  ("past", past, _I32, 4 * seqs, False))
         self.arrays = (page_table, offsets, past)
         self.device, self._index = page_table.device, page_table.get_device()
-        self.tokens = int(tokens)
+        self.tokens, self._seqs = int(tokens), seqs
         self.max_new, self.max_context = _int32("max_new", max_new), _int32("max_context", max_context)
         self._c = _KvBatch(*[t.data_ptr() for t in self.arrays], self.tokens, seqs, width, self.max_new,
                            self.max_context)
@@ -551,23 +546,41 @@ def nvfp4_kv_attention(cache, batch, Q, scale, out, lse=None, window=0, tree=Non
 
 # ------------------------------------------------------------ rotary positions
 
-def _heads_of(name, t, dtypes, shape, index):
+def _device_of(name, t, dtype, index=None):
+    """The GPU of a contiguous tensor of a type, the same as an earlier one's."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.is_contiguous()):
+        raise ValueError("%s must be a contiguous %s tensor" % (name, dtype))
+    at = t.get_device()
+    if at < 0:
+        raise ValueError("%s must be in GPU memory (is on %s)" % (name, t.device))
+    if index is not None and at != index:
+        raise ValueError("%s is on %s, other arguments on cuda:%d" % (name, t.device, index))
+    return at
+
+
+def _call_stream(stream, index):
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(index)
+        return torch.cuda.current_stream(index).cuda_stream
+    return int(stream)
+
+
+def _token_stride(name, t, shape, index):
     """Check a [tokens, heads, dim] tensor whose tokens may be strided (the heads of a
-    token are not); its token stride in elements.  shape: what the last call's tensors
-    share, (tokens, dim)."""
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("%s: expected a torch.Tensor, got %r" % (name, type(t)))
-    if t.dtype not in dtypes:
-        raise ValueError("%s: dtype %s, expected %s" % (name, t.dtype, " or ".join(map(str, dtypes))))
-    if t.dim() != 3 or (t.shape[0], t.shape[2]) != shape:
-        raise ValueError("%s has shape %s, expected (%d, heads, %d)" % (name, tuple(t.shape), *shape))
+    token are not); its token stride in elements."""
+    if t.shape != shape:
+        raise ValueError("%s has shape %s, expected %s" % (name, tuple(t.shape), tuple(shape)))
     token, head, element = t.stride()
-    tokens, heads, dim = t.shape
-    if tokens and ((dim > 1 and element != 1) or (heads > 1 and head != dim)):
+    tokens, heads, dim = shape
+    if tokens and (element != 1 or (heads > 1 and head != dim)):
         raise ValueError("%s: the heads of a token must be contiguous" % name)
-    if not t.is_cuda or t.get_device() != index:
+    if t.get_device() != index:
         raise ValueError("%s is on %s, the positions on cuda:%d" % (name, t.device, index))
     return token if tokens > 1 else heads * dim
+
+
+_rope_rows = struct.Struct("QQqqii")         # struct nvfp4_rope_rows of nvfp4.h
 
 
 def nvfp4_rope(rows, positions, freqs, axis=None, adjacent=False, factor=1.0, stream=None):
@@ -576,43 +589,56 @@ def nvfp4_rope(rows, positions, freqs, axis=None, adjacent=False, factor=1.0, st
     either; a pair of the same tensor is rotated in place), positions int32 [axes, tokens]
     or [tokens], freqs float64 [pairs] (radians for each position), axis uint8 [pairs] or
     None (all pairs follow the first axis)."""
-    rows = list(rows)
-    if not rows or not all(isinstance(r, (tuple, list)) and len(r) == 2 and isinstance(r[0], torch.Tensor)
-                           for r in rows) or rows[0][0].dim() != 3:
-        raise ValueError("rows must be a list of (in, out) pairs of [tokens, heads, head_dim] tensors")
-    _checked(("positions", positions, _I32, 0, False), ("freqs", freqs, (torch.float64,), 0, False),
-             ("axis", axis, _U8, 0, True))
-    first = rows[0][0]
-    tokens, dim = shape = (first.shape[0], first.shape[2])
-    if positions.dim() not in (1, 2) or positions.shape[-1] != tokens:
-        raise ValueError("positions has shape %s, expected ([axes,] %d)" % (tuple(positions.shape), tokens))
+    index = _device_of("positions", positions, torch.int32)
+    _device_of("freqs", freqs, torch.float64, index)
     pairs = freqs.numel()
-    if axis is not None and axis.numel() != pairs:
-        raise ValueError("axis has %d elements, freqs %d" % (axis.numel(), pairs))
-    index = positions.get_device()
-    arr = (_RopeRows * len(rows))()
-    for i, (x, out) in enumerate(rows):
-        xs = _heads_of("rows[%d] in" % i, x, (first.dtype,) if i else _KV_DTYPE, shape, index)
-        os_ = _heads_of("rows[%d] out" % i, out, _KV_DTYPE, shape, index)
-        if x.shape != out.shape:
-            raise ValueError("rows[%d]: in has shape %s, out %s" % (i, tuple(x.shape), tuple(out.shape)))
-        arr[i] = _RopeRows(x.data_ptr(), out.data_ptr(), xs, os_, x.shape[1], _KV_DTYPE[out.dtype])
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    _check(load().nvfp4_rope(arr, len(rows), _KV_DTYPE[first.dtype], tokens, dim, 2 * pairs, int(bool(adjacent)),
-                             positions.data_ptr(), axes, freqs.data_ptr(), None if axis is None else axis.data_ptr(),
-                             float(factor), _stream(stream, positions)), "nvfp4_rope")
+    if axis is not None:
+        _device_of("axis", axis, torch.uint8, index)
+        if axis.numel() != pairs:
+            raise ValueError("axis has %d elements, freqs %d" % (axis.numel(), pairs))
+    packed, dtype, first = b"", None, None
+    for row in rows:
+        if not (isinstance(row, (tuple, list)) and len(row) == 2 and isinstance(row[0], torch.Tensor) and
+                isinstance(row[1], torch.Tensor) and row[0].dim() == 3):
+            raise ValueError("rows must be a list of (in, out) pairs of [tokens, heads, head_dim] tensors")
+        x, out = row
+        shape = x.shape
+        if first is None:
+            first, dtype = shape, x.dtype
+            if dtype not in _KV_DTYPE:
+                raise ValueError("rows: dtype %s, expected bfloat16 or float32" % dtype)
+        elif shape[0] != first[0] or shape[2] != first[2] or x.dtype is not dtype:
+            raise ValueError("rows: %s %s beside %s %s" % (tuple(shape), x.dtype, tuple(first), dtype))
+        if out.dtype not in _KV_DTYPE:
+            raise ValueError("rows: out is %s, expected bfloat16 or float32" % out.dtype)
+        packed += _rope_rows.pack(x.data_ptr(), out.data_ptr(), _token_stride("rows in", x, shape, index),
+                                  _token_stride("rows out", out, shape, index), shape[1], _KV_DTYPE[out.dtype])
+    if first is None:
+        raise ValueError("rows is empty")
+    tokens, _, dim = first
+    if dim > 1024 or pairs > 512:        # before they are cut to 32 bits
+        raise NVFP4Error(-2, "nvfp4_rope")
+    axes = positions.shape
+    if not 1 <= len(axes) <= 2 or axes[-1] != tokens:
+        raise ValueError("positions has shape %s, expected ([axes,] %d)" % (tuple(axes), tokens))
+    status = (_lib or load()).nvfp4_rope(
+        packed, len(packed) // _rope_rows.size, _KV_DTYPE[dtype], tokens, dim, 2 * pairs, 1 if adjacent else 0,
+        positions.data_ptr(), axes[0] if len(axes) == 2 else 1, freqs.data_ptr(),
+        None if axis is None else axis.data_ptr(), float(factor), _call_stream(stream, index))
+    if status:
+        raise NVFP4Error(status, "nvfp4_rope")
 
 
 # ------------------------------------- eviction by gathered attention weight
 
 def _weights(name, t, cache, batch):
     """Check a [seqs, heads, width] tensor of weights; its width."""
-    seqs = batch.arrays[0].shape[0]
-    if not (isinstance(t, torch.Tensor) and t.dtype == torch.float32 and t.dim() == 3 and t.is_contiguous() and
-            t.shape[0] == seqs and t.shape[1] == cache.heads and t.get_device() == cache._index):
+    shape = t.shape if isinstance(t, torch.Tensor) else ()
+    if not (len(shape) == 3 and shape[0] == batch._seqs and shape[1] == cache.heads and t.dtype is torch.float32 and
+            t.is_contiguous() and t.get_device() == cache._index):
         raise ValueError("%s must be a contiguous float32 tensor [%d, %d, width] on %s" % (
-            name, seqs, cache.heads, cache.device))
-    return t.shape[2]
+            name, batch._seqs, cache.heads, cache.device))
+    return shape[2]
 
 
 def nvfp4_kv_weights(cache, batch, Q, scale, lse, weights, decay=1.0, window=0, tree=None, stream=None):
@@ -626,7 +652,7 @@ def nvfp4_kv_weights(cache, batch, Q, scale, lse, weights, decay=1.0, window=0, 
     width = _weights("weights", weights, cache, batch)
     if tree is not None:
         _flat("tree", tree, cache, torch.int64, batch.tokens)
-    _check(load().nvfp4_kv_weights(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale),
+    _check((_lib or load()).nvfp4_kv_weights(cache._ref, batch._ref, Q.data_ptr(), qs, heads, float(scale),
                                    _int32("window", window), None if tree is None else tree.data_ptr(),
                                    lse.data_ptr(), float(decay), weights.data_ptr(), width,
                                    _kv_stream(stream, cache)), "nvfp4_kv_weights")
@@ -638,13 +664,13 @@ def nvfp4_kv_evict(cache, batch, weights, budget, kept, left, weights_out=None, 
     stay, and move to the front.  kept int32 [seqs, heads, budget], left int32 [seqs] (may
     be the batch's past), weights_out as weights, or None: in place."""
     _kv_pair(cache, batch)
-    seqs, budget = batch.arrays[0].shape[0], _int32("budget", budget)
+    seqs, budget = batch._seqs, _int32("budget", budget)
     width = _weights("weights", weights, cache, batch)
     if weights_out is not None and _weights("weights_out", weights_out, cache, batch) != width:
         raise ValueError("weights_out is %d wide, weights %d" % (weights_out.shape[2], width))
     _flat("kept", kept, cache, torch.int32, seqs * cache.heads * max(budget, 0))
     _flat("left", left, cache, torch.int32, seqs)
-    _check(load().nvfp4_kv_evict(cache._ref, batch._ref, budget, _int32("first", first), _int32("recent", recent),
+    _check((_lib or load()).nvfp4_kv_evict(cache._ref, batch._ref, budget, _int32("first", first), _int32("recent", recent),
                                  weights.data_ptr(), (weights if weights_out is None else weights_out).data_ptr(),
                                  width, kept.data_ptr(), left.data_ptr(), _kv_stream(stream, cache)),
            "nvfp4_kv_evict")
@@ -656,15 +682,22 @@ def nvfp4_logprobs_workspace_bytes(n: int, vocab: int, top: int) -> int:
     return int(load().nvfp4_logprobs_workspace_bytes(int(n), int(vocab), _int32("top", top)))
 
 
-def _second(name, t, n):
-    if not isinstance(t, torch.Tensor) or t.dim() != 2 or t.shape[0] != n:
-        raise ValueError("%s must be an int32 tensor [%d, ...]" % (name, n))
-    return t.shape[1]
+def _second(name, t, n, dtype, index):
+    """The second extent of a contiguous [n, ...] tensor."""
+    _device_of(name, t, dtype, index)
+    shape = t.shape
+    if len(shape) != 2 or shape[0] != n:
+        raise ValueError("%s must be a %s tensor [%d, ...]" % (name, dtype, n))
+    return _int32("the extent of %s" % name, shape[1])
 
 
-def _like(name, t, shape):
-    if not isinstance(t, torch.Tensor) or tuple(t.shape) != shape:
-        raise ValueError("%s must be a float32 tensor of shape %s" % (name, shape))
+def _row_values(name, t, n, index):
+    if t is None:
+        return None
+    _device_of(name, t, torch.float32, index)
+    if t.numel() < n:
+        raise ValueError("%s holds %d values, the call needs %d" % (name, t.numel(), n))
+    return t.data_ptr()
 
 
 def nvfp4_logprobs(logits, tokens=None, logp=None, lse=None, entropy=None, top_logp=None, top_index=None, scale=1.0,
@@ -675,26 +708,36 @@ def nvfp4_logprobs(logits, tokens=None, logp=None, lse=None, entropy=None, top_l
     None is not computed."""
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits: expected a torch.Tensor, got %r" % type(logits))
-    if logits.dtype not in _KV_DTYPE or logits.dim() != 2:
+    dtype = _KV_DTYPE.get(logits.dtype)
+    if dtype is None or logits.dim() != 2:
         raise ValueError("logits must be a float32 or bfloat16 tensor [n, vocab]")
     n, vocab = logits.shape
-    if vocab > 1 and logits.stride(1) != 1:
+    stride, element = logits.stride()
+    if vocab > 1 and element != 1:
         raise ValueError("the logits of a row must be contiguous")
+    index = logits.get_device()
+    if index < 0:
+        raise ValueError("logits must be in GPU memory (is on %s)" % logits.device)
     if (tokens is None) != (logp is None) or (top_logp is None) != (top_index is None):
         raise ValueError("tokens and logp, and top_logp and top_index, come together")
-    given = top = 0
+    given = top = nbytes = 0
     if tokens is not None:
-        given = _second("tokens", tokens, n)
-        _like("logp", logp, (n, given))
+        given = _second("tokens", tokens, n, torch.int32, index)
+        if _second("logp", logp, n, torch.float32, index) != given:
+            raise ValueError("logp must have the shape of tokens, %s" % (tuple(tokens.shape),))
     if top_index is not None:
-        top = _second("top_index", top_index, n)
-        _like("top_logp", top_logp, (n, top))
-    _checked(("logits", logits[:, :0], _KV_DTYPE, 0, False), ("tokens", tokens, _I32, 0, True),
-             ("logp", logp, _F32, 0, True), ("lse", lse, _F32, 4 * n, True), ("entropy", entropy, _F32, 4 * n, True),
-             ("top_logp", top_logp, _F32, 0, True), ("top_index", top_index, _I32, 0, True),
-             ("workspace", workspace, _ANY, 0, True))
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(load().nvfp4_logprobs(_KV_DTYPE[logits.dtype], _ptr(logits), n, vocab,
-                                 logits.stride(0) if n > 1 else vocab, float(scale), _ptr(tokens), given, _ptr(logp),
-                                 _ptr(lse), _ptr(entropy), top, _ptr(top_logp), _ptr(top_index), _ptr(workspace),
-                                 nbytes, _stream(stream, logits)), "nvfp4_logprobs")
+        top = _second("top_index", top_index, n, torch.int32, index)
+        if _second("top_logp", top_logp, n, torch.float32, index) != top:
+            raise ValueError("top_logp must have the shape of top_index, %s" % (tuple(top_index.shape),))
+    if workspace is not None:
+        if not workspace.is_contiguous() or workspace.get_device() != index:
+            raise ValueError("workspace must be contiguous, on %s" % logits.device)
+        nbytes = workspace.numel() * workspace.element_size()
+    status = (_lib or load()).nvfp4_logprobs(
+        dtype, logits.data_ptr(), n, vocab, stride if n > 1 else vocab, float(scale),
+        tokens.data_ptr() if given else None, given, logp.data_ptr() if given else None,
+        _row_values("lse", lse, n, index), _row_values("entropy", entropy, n, index), top,
+        top_logp.data_ptr() if top else None, top_index.data_ptr() if top else None,
+        workspace.data_ptr() if nbytes else None, nbytes, _call_stream(stream, index))
+    if status:
+        raise NVFP4Error(status, "nvfp4_logprobs")

@@ -1,19 +1,20 @@
 // nvfp4_logprobs.hip -- log probabilities of given tokens, entropy and the likeliest
 // tokens of rows of logits (gfx950).
 //
-// One pass over the logits: a workgroup holds kChunk of a row in registers and leaves,
+// One pass over the logits: a workgroup holds a chunk of a row in registers and leaves,
 // of z = scale * x, the maximum m, l = sum e^(z - m), t = sum e^(z - m) (z - m), and the
 // `top` largest logits as keys.  A second launch joins a row's chunks,
 //   l = sum l_c e^(m_c - m),  t = sum e^(m_c - m) (t_c + l_c (m_c - m)),
 //   lse = m + log l,  entropy = log l - t / l,
 // and looks the given tokens up.
 //
-// The largest logits of a chunk are found without sorting it: the top-th largest of a
+// The largest logits of a chunk are found without sorting it.  The top-th largest of a
 // wave's 64 lane maxima is no larger than the chunk's top-th largest, since that many
-// elements reach it.  What reaches the largest such bound of the waves, a few more than
-// `top` of them, goes to shared memory, where an element's rank is the number of larger
-// ones.  Where too many reach it (long runs of equal logits) the maximum is taken `top`
-// times.
+// elements reach it, and neither is the least, over the four waves, of their
+// (top / 4)-th largest; the larger of the two is close.  What reaches it, a few more than
+// `top`, goes to shared memory, where an element's rank is the number of larger ones.
+// Where too many reach it (equal logits, such as masked ones) the bound is taken again,
+// among all threads' maxima with their places, which no two share.
 #include "nvfp4_host.h"
 
 namespace nvfp4 {
@@ -21,15 +22,17 @@ namespace nvfp4 {
 typedef unsigned long long Key;           // order of the value, then of falling index; 0: none
 
 constexpr int kLogpThreads = 256, kLogpWaves = kLogpThreads / kLanes;
-constexpr int kChunk = 32 * kLogpThreads;            // logits of a workgroup
+constexpr int kLong = 32, kShort = 8;      // logits of a thread
 constexpr int kCandidates = 512;
+constexpr int64_t kMaxGroups = (int64_t(1) << 32) / kLogpThreads - 1;     // of a launch: its threads stay below 2^32
+constexpr int64_t kLogpFill = 512;                // workgroups with long chunks from which on they are taken
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 
 struct LogpArgs {
     const void *logits;
     int64_t stride;
-    int n, vocab, chunks, given, top;
+    int vocab, chunks, given, top;
     float scale;
     const int *tokens;
     float *logp, *lse, *entropy, *top_logp;
@@ -50,6 +53,25 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 __device__ __forceinline__ Key key_of(uint32_t order, int index) { return Key(order) << 32 | (0xFFFFFFFFu - uint32_t(index)); }
 __device__ __forceinline__ int index_of(Key k) { return int(0xFFFFFFFFu - uint32_t(k)); }
 
+// Values over the whole wave, in every lane: exchanges within rows of 16 lanes, then of rows.
+template <int CTRL>
+__device__ __forceinline__ float lane_of(float v) {
+    return __uint_as_float(uint32_t(__builtin_amdgcn_update_dpp(0, int(__float_as_uint(v)), CTRL, 0xF, 0xF, false)));
+}
+template <class F>
+__device__ __forceinline__ float over_wave(float v, F f) {
+    v = f(v, lane_of<0xB1>(v));      // quad_perm [1,0,3,2]
+    v = f(v, lane_of<0x4E>(v));      // quad_perm [2,3,0,1]
+    v = f(v, lane_of<0x141>(v));     // row_half_mirror
+    v = f(v, lane_of<0x140>(v));     // row_mirror
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ __forceinline__ float wave_sum(float v) { return over_wave(v, [](float x, float y) { return x + y; }); }
+__device__ __forceinline__ float wave_largest(float v) { return over_wave(v, [](float x, float y) { return fmaxf(x, y); }); }
+
 // A number that `k` lanes of the wave at least reach, the k-th largest but for the bits
 // below the top 20.
 __device__ __forceinline__ uint32_t reached_by(uint32_t v, int k) {
@@ -62,39 +84,61 @@ __device__ __forceinline__ uint32_t reached_by(uint32_t v, int k) {
     return bound;
 }
 
-__device__ __forceinline__ Key wave_max(Key v) { return lanes_max_u64<64>(v); }
-
-// The `top` largest of a workgroup's keys (absent ones 0) to out[0 .. top - 1], in order.
-// Each thread's keys are 0 .. count - 1 of `key`, their orders' largest is `most`.
-// Threads need not hold `top` keys together: what is missing is 0.
 struct TopShared {
-    Key list[kCandidates];
-    Key wave[kLogpWaves];
-    uint32_t bound[kLogpWaves];
+    Key list[kCandidates], most[kLogpThreads];
+    Key wave[kLogpWaves], least;
+    uint32_t every[kLogpWaves], quarter[kLogpWaves];
     int found;
 };
-template <int UNROLL, class KeyAt>
-__device__ __forceinline__ void largest(TopShared &sh, int top, int count, uint32_t most, KeyAt key, Key *out) {
+
+// The `top` largest of a workgroup's keys to out[0 .. top - 1], in order; 0 where it has
+// fewer.  A thread's largest order is `most` (0 if it has none); offer(bound, take) calls
+// take for each of its keys whose order is at least `bound`, each(f) calls f for all of them.
+template <class Offer, class Each>
+__device__ __forceinline__ void largest(TopShared &sh, int top, uint32_t most, Offer offer, Each each, Key *out) {
     const int tid = threadIdx.x, wave = tid / kLanes;
-    const uint32_t mine = reached_by(most, top);
-    if ((tid & 63) == 0) sh.bound[wave] = mine;
-    if (tid == 0) sh.found = 0;
+    const uint32_t every = reached_by(most, top), quarter = reached_by(most, (top + kLogpWaves - 1) / kLogpWaves);
+    if ((tid & 63) == 0) {
+        sh.every[wave] = every;
+        sh.quarter[wave] = quarter;
+    }
+    if (tid == 0) {
+        sh.found = 0;
+        sh.least = ~Key(0);
+    }
     __syncthreads();
-    uint32_t bound = sh.bound[0];
+    uint32_t bound = sh.every[0], all = sh.quarter[0];
 #pragma unroll
-    for (int w = 1; w < kLogpWaves; ++w) bound = max(bound, sh.bound[w]);
-    const Key least = max(Key(bound) << 32, Key(1));
-    if (Key(most) << 32 >= (least & 0xFFFFFFFF00000000ull))
-#pragma unroll UNROLL
-        for (int i = 0; i < count; ++i) {
-            const Key k = key(i);
-            if (k >= least) {
-                const int at = atomicAdd(&sh.found, 1);
-                if (at < kCandidates) sh.list[at] = k;
-            }
-        }
+    for (int w = 1; w < kLogpWaves; ++w) {
+        bound = max(bound, sh.every[w]);
+        all = min(all, sh.quarter[w]);
+    }
+    bound = max(bound, all);
+    const auto take = [&](Key k) {
+        const int at = atomicAdd(&sh.found, 1);
+        if (at < kCandidates) sh.list[at] = k;
+    };
+    if (most >= bound) offer(bound, take);
     __syncthreads();
-    const int found = sh.found;
+    int found = sh.found;
+    if (found > kCandidates) {
+        Key mine = 0;
+        each([&](Key k) { mine = max(mine, k); });
+        sh.most[tid] = mine;
+        __syncthreads();
+        int larger = 0;
+        for (int i = 0; i < kLogpThreads; ++i) larger += sh.most[i] > mine;
+        if (tid == 0) sh.found = 0;
+        if (larger < top) atomicMin(&sh.least, mine);
+        __syncthreads();
+        const Key least = max(sh.least, Key(1));
+        if (mine >= least)
+            each([&](Key k) {
+                if (k >= least) take(k);
+            });
+        __syncthreads();
+        found = sh.found;
+    }
     if (found <= kCandidates) {
         for (int i = tid; i < max(found, top); i += kLogpThreads) {
             if (i >= found) {
@@ -103,19 +147,17 @@ __device__ __forceinline__ void largest(TopShared &sh, int top, int count, uint3
             }
             const Key k = sh.list[i];
             int rank = 0;
+#pragma unroll 8
             for (int j = 0; j < found; ++j) rank += sh.list[j] > k;
             if (rank < top) out[rank] = k;
         }
     } else {
+        // a few threads hold most of the largest: one after another
         Key last = ~Key(0);
         for (int r = 0; r < top; ++r) {
             Key best = 0;
-#pragma unroll UNROLL
-            for (int i = 0; i < count; ++i) {
-                const Key k = key(i);
-                if (k < last && k > best) best = k;
-            }
-            best = wave_max(best);
+            each([&](Key k) { best = k < last ? max(best, k) : best; });
+            best = lanes_max_u64<64>(best);
             if ((tid & 63) == 0) sh.wave[wave] = best;
             __syncthreads();
             last = sh.wave[0];
@@ -125,17 +167,6 @@ __device__ __forceinline__ void largest(TopShared &sh, int top, int count, uint3
             __syncthreads();
         }
     }
-}
-
-__device__ __forceinline__ float wave_sum(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v += __shfl_xor(v, d);
-    return v;
-}
-__device__ __forceinline__ float wave_largest(float v) {
-#pragma unroll
-    for (int d = 32; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor(v, d));
-    return v;
 }
 
 // Sums of one part relative to its maximum.
@@ -150,60 +181,68 @@ __device__ __forceinline__ Sums moved(Sums s, float m) {
     return Sums{m, s.l * w, w * __builtin_fmaf(s.l, d, s.t)};
 }
 
-template <class T>
-__device__ __forceinline__ void load_logits(const T *row, int first, int vocab, float (&x)[32]);
-template <>
-__device__ __forceinline__ void load_logits<float>(const float *row, int first, int vocab, float (&x)[32]) {
+__device__ __forceinline__ float logit(const float *row, int at) { return row[at]; }
+__device__ __forceinline__ float logit(const uint16_t *row, int at) { return __uint_as_float(uint32_t(row[at]) << 16); }
+
+// A thread's N logits, four in a row at place(0), place(4), ...: all in flight together.
+// A chunk that the row's end cuts is read one by one, minus infinity past it.
+template <int N, class Place>
+__device__ __forceinline__ void load_logits(const float *row, bool full, int vocab, Place place, float (&x)[N]) {
     typedef float F4 __attribute__((ext_vector_type(4), aligned(4)));
+    if (full) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int at = first + (i * kLogpThreads + int(threadIdx.x)) * 4;
-        if (at + 4 <= vocab) {
-            const F4 v = *reinterpret_cast<const F4 *>(row + at);
+        for (int i = 0; i < N; i += 4) {
+            const F4 v = *reinterpret_cast<const F4 *>(row + place(i));
 #pragma unroll
-            for (int j = 0; j < 4; ++j) x[4 * i + j] = v[j];
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[4 * i + j] = at + j < vocab ? row[at + j] : kNegInf;
+            for (int j = 0; j < 4; ++j) x[i + j] = v[j];
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = place(i) < vocab ? row[place(i)] : kNegInf;
     }
 }
-template <>
-__device__ __forceinline__ void load_logits<uint16_t>(const uint16_t *row, int first, int vocab, float (&x)[32]) {
+template <int N, class Place>
+__device__ __forceinline__ void load_logits(const uint16_t *row, bool full, int vocab, Place place, float (&x)[N]) {
     typedef unsigned int U2 __attribute__((ext_vector_type(2), aligned(2)));
+    uint32_t w[N / 2];
+    if (full) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int at = first + (i * kLogpThreads + int(threadIdx.x)) * 4;
-        if (at + 4 <= vocab) {
-            const U2 v = *reinterpret_cast<const U2 *>(row + at);
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[4 * i + j] = __uint_as_float(j & 1 ? v[j / 2] & 0xFFFF0000u : v[j / 2] << 16);
-        } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                x[4 * i + j] = at + j < vocab ? __uint_as_float(uint32_t(row[at + j]) << 16) : kNegInf;
+        for (int i = 0; i < N; i += 4) {
+            const U2 v = *reinterpret_cast<const U2 *>(row + place(i));
+            w[i / 2] = v[0];
+            w[i / 2 + 1] = v[1];
         }
+    } else {
+        constexpr uint32_t kMasked = 0xFF80;             // minus infinity
+#pragma unroll
+        for (int i = 0; i < N; i += 2)
+            w[i / 2] = (place(i) < vocab ? uint32_t(row[place(i)]) : kMasked) |
+                       (place(i + 1) < vocab ? uint32_t(row[place(i + 1)]) : kMasked) << 16;
     }
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
 }
 
-template <class T>
-__global__ void __launch_bounds__(kLogpThreads) logprobs_chunk_kernel(LogpArgs a) {
+template <class T, int N>
+__global__ void __launch_bounds__(kLogpThreads, 8) logprobs_chunk_kernel(LogpArgs a) {
     __shared__ TopShared sh;
     __shared__ Sums sums[kLogpWaves];
     const int tid = threadIdx.x, wave = tid / kLanes;
     const int chunk = int(blockIdx.x % unsigned(a.chunks)), r = int(blockIdx.x / unsigned(a.chunks));
-    const int first = chunk * kChunk;
-    float x[32];
-    load_logits<T>(static_cast<const T *>(a.logits) + r * a.stride, first, a.vocab, x);
+    const int first = chunk * (N * kLogpThreads);
+    const T *const row = static_cast<const T *>(a.logits) + r * a.stride;
+    const auto place = [&](int i) { return first + (i / 4 * kLogpThreads + tid) * 4 + i % 4; };
+    float x[N];
+    const bool full = first + N * kLogpThreads <= a.vocab;
+    load_logits<N>(row, full, a.vocab, place, x);
     float most = x[0];
 #pragma unroll
-    for (int i = 1; i < 32; ++i) most = fmaxf(most, x[i]);
+    for (int i = 1; i < N; ++i) most = fmaxf(most, x[i]);
     const float top = wave_largest(most);
     Sums s = {top * a.scale, 0.0f, 0.0f};
     const float base = s.m == kNegInf ? 0.0f : s.m;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
+    for (int i = 0; i < N; ++i) {
         const float d = __builtin_fmaf(x[i], a.scale, -base);
         const float e = __builtin_amdgcn_exp2f(d * kLog2e);
         s.l += e;
@@ -214,17 +253,33 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_chunk_kernel(LogpArgs a
     if ((tid & 63) == 0) sums[wave] = s;
     const int64_t part = int64_t(r) * a.chunks + chunk;
     if (a.top > 0) {
-        const auto key = [&](int i) {
-            const int at = first + (i / 4 * kLogpThreads + tid) * 4 + i % 4;
-            return at < a.vocab ? key_of(order_of(x[i]), at) : Key(0);
-        };
         uint32_t reach = order_of(most);
-        if (first + kChunk > a.vocab) {                  // places past the row reach nothing
+        if (!full) {                                     // places past the row reach nothing
             reach = 0;
 #pragma unroll
-            for (int i = 0; i < 32; ++i) reach = max(reach, uint32_t(key(i) >> 32));
+            for (int i = 0; i < N; ++i) reach = place(i) < a.vocab ? max(reach, order_of(x[i])) : reach;
         }
-        largest<32>(sh, a.top, 32, reach, key, a.keys + part * a.top);
+        const auto offer = [&](uint32_t bound, auto take) {
+            // by value; NaN only where anything is taken, and below -infinity's order there is no value
+            const float limit = bound < 0x007FFFFFu ? kNegInf : value_of(bound);
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if ((x[i] >= limit || bound == 0) && (full || place(i) < a.vocab)) take(key_of(order_of(x[i]), place(i)));
+        };
+        // Rarely needed, so read again: what the rare path keeps through the kernel costs the
+        // common one its occupancy.
+        const auto each = [&](auto f) {
+#pragma unroll 2
+            for (int j = 0; j < N; j += 4) {
+                float y[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] = place(j) + e < a.vocab ? logit(row, place(j) + e) : 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (place(j) + e < a.vocab) f(key_of(order_of(y[e]), place(j) + e));
+            }
+        };
+        largest(sh, a.top, reach, offer, each, a.keys + part * a.top);
     } else {
         __syncthreads();
     }
@@ -252,6 +307,14 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
     __shared__ Key best[NVFP4_MAX_TOP];
     const int tid = threadIdx.x, wave = tid / kLanes, r = blockIdx.x;
     const float *parts = a.parts + int64_t(r) * a.chunks * 4;
+    // the chunks' keys, the first of them in registers
+    constexpr int kKept = 8;
+    const int64_t all_keys = int64_t(a.chunks) * a.top;
+    const Key *const keys = a.keys + r * all_keys;
+    Key mine[kKept];
+    uint32_t reach = 0;
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) mine[i] = tid + i * kLogpThreads < all_keys ? keys[tid + i * kLogpThreads] : Key(0);
     float m = kNegInf;
     for (int c = tid; c < a.chunks; c += kLogpThreads) m = fmaxf(m, parts[4 * c]);
     m = wave_largest(m);
@@ -291,18 +354,25 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
         const int token = a.tokens[at];
         float y = __builtin_nanf("");
         if (token >= 0 && token < a.vocab)
-            y = logp(dtype == NVFP4_KV_F32 ? static_cast<const float *>(a.logits)[row + token]
-                                           : __uint_as_float(uint32_t(static_cast<const uint16_t *>(a.logits)[row + token]) << 16));
+            y = logp(dtype == NVFP4_KV_F32 ? logit(static_cast<const float *>(a.logits) + row, token)
+                                           : logit(static_cast<const uint16_t *>(a.logits) + row, token));
         a.logp[at] = y;
     }
     if (a.top == 0) return;
-    const int64_t all_keys = int64_t(a.chunks) * a.top;
-    const Key *keys = a.keys + r * all_keys;
-    const int count = int((all_keys - tid + kLogpThreads - 1) / kLogpThreads);
-    uint32_t most = 0;
-    for (int i = 0; i < count; ++i) most = max(most, uint32_t(keys[tid + int64_t(i) * kLogpThreads] >> 32));
-    __syncthreads();
-    largest<1>(sh, a.top, count, most, [&](int i) { return keys[tid + int64_t(i) * kLogpThreads]; }, best);
+#pragma unroll
+    for (int i = 0; i < kKept; ++i) reach = max(reach, uint32_t(mine[i] >> 32));
+    for (int64_t i = tid + kKept * kLogpThreads; i < all_keys; i += kLogpThreads) reach = max(reach, uint32_t(keys[i] >> 32));
+    const auto each = [&](auto f) {                    // 0 where there is none
+#pragma unroll
+        for (int i = 0; i < kKept; ++i) f(mine[i]);
+        for (int64_t i = tid + kKept * kLogpThreads; i < all_keys; i += kLogpThreads) f(keys[i]);
+    };
+    const auto offer = [&](uint32_t bound, auto take) {
+        each([&](Key k) {
+            if (k && uint32_t(k >> 32) >= bound) take(k);
+        });
+    };
+    largest(sh, a.top, reach, offer, each, best);
     __syncthreads();
     for (int i = tid; i < a.top; i += kLogpThreads) {
         a.top_index[int64_t(r) * a.top + i] = index_of(best[i]);
@@ -310,10 +380,17 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
     }
 }
 
+// Logits of a workgroup: chunks of 2048 where longer ones would leave CUs idle (one row of
+// 151936: 10.6 us, of 8192 13.7; 16 rows 13.4 and 15.3), else of 8192 (128 rows 28 us, of
+// 2048 36; 512 rows 70 and 115).
+static int64_t logprobs_chunk(int64_t n, int64_t vocab) {
+    return (n * ceil_div(vocab, kLong * kLogpThreads) < kLogpFill ? kShort : kLong) * kLogpThreads;
+}
+
 static bool logprobs_shape_ok(int64_t n, int64_t vocab, int top) {
     if (n < 0 || n > (int64_t(1) << 30) || vocab < 1 || vocab > (int64_t(1) << 30)) return false;
     if (top < 0 || top > NVFP4_MAX_TOP || top > vocab) return false;
-    return n * ceil_div(vocab, kChunk) <= 0x7FFFFFFF;
+    return n * ceil_div(vocab, logprobs_chunk(n, vocab)) <= kMaxGroups;
 }
 
 }  // namespace nvfp4
@@ -322,7 +399,7 @@ using namespace nvfp4;
 
 NVFP4_API size_t nvfp4_logprobs_workspace_bytes(int64_t n, int64_t vocab, int top) {
     if (!logprobs_shape_ok(n, vocab, top)) return 0;
-    return size_t(n) * size_t(ceil_div(vocab, kChunk)) * (4 * sizeof(float) + size_t(top) * sizeof(Key));
+    return size_t(n) * size_t(ceil_div(vocab, logprobs_chunk(n, vocab))) * (4 * sizeof(float) + size_t(top) * sizeof(Key));
 }
 
 NVFP4_API int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t vocab, int64_t stride, float scale,
@@ -346,9 +423,9 @@ NVFP4_API int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t v
     LogpArgs a = {};
     a.logits = logits;
     a.stride = stride;
-    a.n = int(n);
     a.vocab = int(vocab);
-    a.chunks = int(ceil_div(vocab, kChunk));
+    const bool short_chunks = logprobs_chunk(n, vocab) == kShort * kLogpThreads;
+    a.chunks = int(ceil_div(vocab, logprobs_chunk(n, vocab)));
     a.given = given;
     a.top = top;
     a.scale = scale;
@@ -361,8 +438,9 @@ NVFP4_API int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t v
     a.parts = static_cast<float *>(workspace);
     a.keys = reinterpret_cast<Key *>(a.parts + size_t(n) * a.chunks * 4);
     const unsigned groups = unsigned(n * a.chunks);
-    if (dtype == NVFP4_KV_F32) logprobs_chunk_kernel<float><<<groups, kLogpThreads, 0, stream>>>(a);
-    else logprobs_chunk_kernel<uint16_t><<<groups, kLogpThreads, 0, stream>>>(a);
+    const auto launch = [&](auto kernel) { kernel<<<groups, kLogpThreads, 0, stream>>>(a); };
+    if (dtype == NVFP4_KV_F32) launch(short_chunks ? logprobs_chunk_kernel<float, kShort> : logprobs_chunk_kernel<float, kLong>);
+    else launch(short_chunks ? logprobs_chunk_kernel<uint16_t, kShort> : logprobs_chunk_kernel<uint16_t, kLong>);
     if (int st = launch_status()) return st;
     logprobs_join_kernel<<<unsigned(n), kLogpThreads, 0, stream>>>(a, dtype);
     return launch_status();

@@ -137,6 +137,24 @@ def test_ties(vocab, levels):
         _check(_run(logits, tokens, top), logits, tokens, top, 1.0, "%d levels, top %d" % (levels, top))
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n", [2, 600])
+def test_few_threads_hold_the_largest(n, dtype):
+    """Runs of four logits 1024 apart, as one thread reads them: 63 such columns are above
+    all else, so that the 64th largest of the threads' maxima bounds next to nothing; and
+    rows of a few allowed tokens, where all others are equal."""
+    vocab, top = 9000, 64
+    logits, _ = _logits(n, vocab, 21, dtype)
+    at = torch.arange(vocab, device=G.DEV) // 4 % 256
+    logits[:, at < 63] += 50
+    for r, allowed in ((0, [8999, 17, 4096]), (1, [])):
+        logits[r] = -INF
+        logits[r, allowed] = 1.5
+    tokens = torch.full((n, 1), 17, dtype=torch.int32, device=G.DEV)
+    G.note("logprobs, the largest in few threads, %d rows %s" % (n, dtype))
+    _check(_run(logits, tokens, top), logits, tokens, top, 1.0, "few threads")
+
+
 @pytest.mark.parametrize("rising", [True, False])
 def test_sorted_rows(rising):
     """The largest logits all in one chunk, one wave, one thread."""

@@ -45,8 +45,9 @@ def test_no_rows_are_no_error(lib):
 
 def test_workspace_sizes():
     size = nv.nvfp4_logprobs_workspace_bytes
-    assert size(3, 1000, 5) == 3 * (16 + 5 * 8) and size(3, 8192, 0) == 3 * 16 and size(3, 8193, 0) == 3 * 2 * 16
-    assert size(2, 151936, 20) == 2 * 19 * (16 + 160)
+    # four numbers a chunk, of 2048 logits for a few rows and 8192 for many, and its keys
+    assert size(3, 1000, 5) == 3 * (16 + 5 * 8) and size(3, 8192, 0) == 3 * 4 * 16 and size(3, 8193, 0) == 3 * 5 * 16
+    assert size(2, 151936, 20) == 2 * 75 * (16 + 160) and size(512, 151936, 20) == 512 * 19 * (16 + 160)
     assert size(0, 1000, 5) == 0 and size(1, 0, 0) == 0 and size(1, 10, 11) == 0 and size(1, 100, 65) == 0
 
 

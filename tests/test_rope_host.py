@@ -14,6 +14,12 @@ A = 1 << 20          # an address that is aligned and never followed
 B = 2 << 20
 
 
+class Rows(ctypes.Structure):
+    """struct nvfp4_rope_rows of nvfp4.h."""
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("in_stride", ctypes.c_int64),
+                ("out_stride", ctypes.c_int64), ("heads", ctypes.c_int32), ("out_type", ctypes.c_int32)]
+
+
 @pytest.fixture(scope="module")
 def lib():
     return nv.load()
@@ -21,7 +27,7 @@ def lib():
 
 def call(lib, rows=((A, B, 1024, 1024, 8, 0),), count=None, dtype=0, tokens=5, dim=128, rotary=128, adjacent=0,
          positions=A, axes=3, freqs=A, axis=A, factor=1.0):
-    arr = None if rows is None else (nv._RopeRows * 8)(*[nv._RopeRows(*r) for r in rows])
+    arr = None if rows is None else (Rows * 8)(*[Rows(*r) for r in rows])
     return lib.nvfp4_rope(arr, len(rows or ()) if count is None else count, dtype, tokens, dim, rotary, adjacent,
                           positions, axes, freqs, axis, factor, None)
 
@@ -54,6 +60,11 @@ def test_refusals(lib, kw, status):
 def test_nothing_to_do_is_no_error(lib):
     assert call(lib, tokens=0) == OK
     assert call(lib, rows=rows(in_=None, out=None), tokens=0, positions=None) == OK
+
+
+def test_binding_packs_the_struct():
+    assert nv._rope_rows.size == ctypes.sizeof(Rows)
+    assert nv._rope_rows.pack(A, B, 1 << 35, -3, 7, 1) == bytes(Rows(A, B, 1 << 35, -3, 7, 1))
 
 
 def test_binding_refuses_before_the_library():
