@@ -26,7 +26,7 @@ struct WeighArgs {
     uint32_t group_magic;  // (2^32 - 1) / group
     int few_rows;          // sequences of at most so many rows are the first kernel's
     float scale_log2;      // c as rounded
-    float lost;            // (scale * log2(e) - c) / scale
+    float lost;            // (scale * log2(e) - c) / scale, less what kLog2e is short of log2(e)
     float decay;
 };
 
@@ -56,13 +56,11 @@ struct RowFacts {
     float r, factor;
 };
 __device__ __forceinline__ bool counts(float lse) { return fabsf(lse) < __builtin_inff(); }
-__device__ __forceinline__ RowFacts row_facts(const WeighArgs &a, float lse) {
-    constexpr float kLog2eRest = 1.92596299e-8f;             // log2(e) - kLog2e
-    const bool in = counts(lse);
+__device__ __forceinline__ RowFacts row_facts(const WeighArgs &a, float lse, bool in) {
     lse = in ? lse : 0.0f;
     const float r = lse * kLog2e;
-    const float rest = __builtin_fmaf(lse, kLog2e, -r) + lse * kLog2eRest;
-    return RowFacts{r, in ? exp2_fast(__builtin_fmaf(lse, a.lost, -rest)) : 0.0f};
+    const float factor = exp2_fast(__builtin_fmaf(lse, a.lost, -__builtin_fmaf(lse, kLog2e, -r)));
+    return RowFacts{r, in ? factor : 0.0f};
 }
 
 // The new weight of a key from what its rows add and what it had (0 for none); a key with
@@ -78,8 +76,9 @@ __device__ __forceinline__ float gathered(float total, bool page, float old, flo
 // registers, and keys, 32 of a wave's step, as B: a lane of the accumulator has four
 // rows' scores of one key, whose sum it takes with two exchanges between lanes for the
 // other rows.  Workgroups take equal shares of all sequences' steps (64 ragged sequences
-// 33.6 us, in pieces of 2048 keys 46.8).  Codes of the two steps to come are loaded ahead, past the caches, the
-// table's entries a step before that.
+// 33.6 us, in pieces of 2048 keys 46.8).  Codes of the two steps to come are loaded ahead,
+// past the caches, the table's entries a step before that.  Bound by reading the keys' codes
+// (131008 keys of 8 heads of 128 dims: 28 us, 4.9 TB/s).
 
 // A load of BYTES that nobody repeats.
 template <int BYTES>
@@ -227,7 +226,7 @@ __global__ void __launch_bounds__(kWeighThreads, RT * D <= 128 ? 4 : RT * D <= 2
 #pragma unroll
                     for (int m = 0; m < K::kSlices; ++m) q[t][m] = in ? q[t][m] : bf16x8{};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) fact[t][e] = row_facts(a, base + 16 * t + 4 * g + e < rows ? lse[t][e] : kNegInf);
+                    for (int e = 0; e < 4; ++e) fact[t][e] = row_facts(a, lse[t][e], base + 16 * t + 4 * g + e < rows && counts(lse[t][e]));
                 }
                 // the keys that every row sees
                 const int inner_lo = a.window > 0 ? past + n - a.window : 0, inner_hi = a.tree ? past : past + 1;
@@ -288,12 +287,16 @@ __global__ void __launch_bounds__(kWeighThreads, RT * D <= 128 ? 4 : RT * D <= 2
 // A wave holds 64 keys as A operands of v_mfma_f32_32x32x16_bf16 and the workgroup walks
 // the query rows, 32 at a time, as B through shared memory: a lane of the accumulator has
 // 16 keys' scores of one row, whose log-sum-exp it holds too, and adds its weights to
-// running sums.  Only at the end are the sums of the 32 rows' lanes added.  RW waves of
-// the four share keys, each with its own rows; their sums meet in shared memory.
+// running sums.  Only at the end are the sums of the 32 rows' lanes added.  RW
+// waves of the four share keys, each with its own rows; their sums meet in shared memory.
 //
 // A step's rows go straight to shared memory two steps ahead, into a ring of three, so
 // that one barrier a step is enough.  16-byte chunks of a row stand exchanged by the
 // row's number, without which the lanes of a read would meet in the same banks.
+// 2048 tokens of 32 heads over 32768 keys: 705 us, 950 TFLOP/s.  Matrix instructions take
+// 36% of the cycles, the exponentials' multiply-adds and the steps' other vector work most
+// of the rest: two waves a SIMD overlap them only in part, four kept in one wave's
+// registers (1154 us) or both woven into one stream of instructions (798 us) do no better.
 
 constexpr int kWideKeys = 64;              // of a wave
 constexpr int kWideRows = 32;              // of a wave's step
@@ -365,21 +368,31 @@ __device__ __forceinline__ float column_sums(const float (&x)[16]) {
     return v + __shfl_xor(v, 16);
 }
 
+// s_waitcnt operand: until at most n loads from memory are on their way.
+constexpr int loads_left(int n) { return kWaitLoads | (n & 15) | n >> 4 << 14; }
+
 template <int D, int RW>
 struct WideShape {
     static constexpr int kChunks = D / 8;                            // 16-byte chunks of a row
+    static constexpr int kLoadRows = kWeighThreads / kChunks;        // rows that the workgroup loads at a time
+    static constexpr int kTileLoads = kWideRows / kLoadRows;         // a thread's loads of a tile
+    static constexpr int kTileBytes = kWideRows * D * 2;
     static constexpr int kStepRows = RW * kWideRows;
-    static constexpr int kRowBytes = kStepRows * D * 2;              // of a step's rows; their log-sum-exps stand behind
-    static constexpr int kStepBytes = kRowBytes + kStepRows * 4;
-    static constexpr int kLoads = kStepRows * kChunks / kWeighThreads;   // a thread's of a step's rows
+    static constexpr int kRowBytes = RW * kTileBytes;                // of a step's tiles; each wave's log-sum-exps stand behind
+    static constexpr int kStepBytes = kRowBytes + kWeighWaves * kLanes * 4;
+    static constexpr int kLoads = RW * kTileLoads;
     static constexpr int kLds = 3 * kStepBytes;
-    // The place of chunk c of row r: rows 128 bytes apart take turns in pairs.
-    static __device__ __forceinline__ int place(int r, int c) {
-        return r * kChunks + (c ^ (D == 64 ? r >> 1 & 7 : r & 15));
+    // Which chunk stands in place c of row r, and the other way round: the same for all rows
+    // that a thread loads, and other ones for rows whose chunks would share banks.
+    static __device__ __forceinline__ int exchanged(int r, int c) {
+        return c ^ (D == 64 ? r >> 1 & 7 : D == 128 ? r & 15 : r & 7);
     }
 };
 
-template <int D, int BITS, int RW>
+// FLAT: tiles of 32 rows one after another, token by token, of sequences of few tokens;
+// else tiles of 32 tokens of one head of the group, whose addresses take no arithmetic of
+// the lanes.  RW: waves that share keys.
+template <int D, int BITS, int RW, bool FLAT>
 __global__ void __launch_bounds__(kWeighThreads, 2) weigh_many_kernel(WeighArgs a) {
     typedef KeyOperand<D, BITS> K;
     typedef WideShape<D, RW> W;
@@ -390,6 +403,18 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_many_kernel(WeighArgs 
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int key_wave = wave % kKeyWaves, row_wave = wave / kKeyWaves;
     const int head = blockIdx.y;
+    // where the lane's operands stand in a step's rows
+    int from[K::kSteps];
+#pragma unroll
+    for (int m = 0; m < K::kSteps; ++m)
+        from[m] = ((row_wave * kWideRows + c) * W::kChunks + W::exchanged(c, K::element(m, half) / 8)) * 16;
+    const int load_row = threadIdx.x / W::kChunks, load_chunk = W::exchanged(load_row, threadIdx.x % W::kChunks);
+    // what a lane adds to a tile's address (32 tokens span less than 2^32 bytes, which the host checks)
+    uint32_t offset[W::kTileLoads];
+#pragma unroll
+    for (int l = 0; l < W::kTileLoads; ++l)
+        offset[l] = (uint32_t(load_row + l * W::kLoadRows) * uint32_t(a.q_stride) + load_chunk * 8) * 2;
+    const uint32_t offset_lse = uint32_t(c) * a.q_heads * 4;
     for (int s = blockIdx.z; s < a.kv.seqs; s += gridDim.z) {
         int begin, stop, past;
         sequence(a.kv, s, begin, stop, past);
@@ -402,87 +427,128 @@ __global__ void __launch_bounds__(kWeighThreads, 2) weigh_many_kernel(WeighArgs 
             K k[2];
 #pragma unroll
             for (int u = 0; u < 2; ++u) k[u].load(a.kv, s, head, key + 32 * u, end);
-            // the rows that may see some of the workgroup's keys
-            const int i_lo = a.tree ? 0 : max(0, int(first) - past);
-            const int i_hi = a.window > 0 ? max(0, int(min(int64_t(n), int64_t(first) + kKeys - 1 + a.window - past))) : n;
-            const int row_lo = i_lo * a.group & ~(kWideRows - 1), row_hi = i_hi * a.group;
-            float sum[2][16] = {};
-            // the rows that see all of the wave's keys
-            const int64_t full_lo = a.tree ? (key + kWideKeys <= past ? 0 : rows) : int64_t(key + kWideKeys - 1 - past) * a.group;
-            const int64_t full_hi = a.window > 0 ? (int64_t(key) + a.window - past) * a.group : rows;
+            // The tokens that may see some of the workgroup's keys, the tiles of their rows, and the
+            // tokens that see all of the wave's keys.
+            const int i_lo = (a.tree ? 0 : max(0, int(first) - past)) & (FLAT ? -1 : -kWideRows);
+            const int i_hi = a.window > 0 ? max(i_lo, int(min(int64_t(n), int64_t(first) + kKeys - 1 + a.window - past))) : n;
+            const int row_lo = i_lo * a.group & -kWideRows;
+            const int tiles = FLAT ? max(0, i_hi * a.group - row_lo + kWideRows - 1) / kWideRows
+                                   : (i_hi - i_lo + kWideRows - 1) / kWideRows * a.group;
+            const int full_lo = a.tree ? (key + kWideKeys <= past ? 0 : n) : key + kWideKeys - 1 - past;
+            const int full_hi = a.window > 0 ? int(min(int64_t(n), int64_t(key) + a.window - past)) : n;
 
-            // a step's rows and log-sum-exps on their way to shared memory
-            const auto send = [&](int row0, int slot) {
-#pragma unroll
-                for (int l = 0; l < W::kLoads; ++l) {
-                    const int p = l * kWeighThreads + threadIdx.x, r = p / W::kChunks;
-                    const int chunk = W::place(r, p % W::kChunks) % W::kChunks;      // the exchange is its own inverse
-                    const WeighRow w(a, min(row0 + r, rows - 1));
-                    const uint16_t *from = q + w.i * a.q_stride + w.g * D + chunk * 8;
-                    __builtin_amdgcn_global_load_lds((GlobalMem *)from,
-                                                     (SharedMem *)(lds + slot * W::kStepBytes + (l * kWeighThreads + wave * kLanes) * 16),
-                                                     16, 0, 0);
-                }
-                if (lane < W::kStepRows / kWeighWaves) {
-                    const WeighRow w(a, min(row0 + wave * (W::kStepRows / kWeighWaves) + lane, rows - 1));
-                    __builtin_amdgcn_global_load_lds((GlobalMem *)(lses + int64_t(w.i) * a.q_heads + w.g),
-                                                     (SharedMem *)(lds + slot * W::kStepBytes + W::kRowBytes + wave * W::kStepRows),
-                                                     4, 0, 0);
+            // A tile's first token and head of the group.
+            const auto advance = [&](int &i, int &g) __attribute__((always_inline)) {
+                if (++g == a.group) {
+                    g = 0;
+                    i += kWideRows;
                 }
             };
+            // The rows and log-sum-exps of the step of tiles `tile`, .. on their way to shared memory
+            // (where there is no such tile, or no such row, those of any); i, g: the first one's.
+            const auto send = [&](int tile, int &i, int &g, int slot) __attribute__((always_inline)) {
+                uint8_t *const to = lds + slot * W::kStepBytes;
+                int mine_i = i, mine_g = g;
+#pragma unroll
+                for (int j = 0; j < RW; ++j) {
+                    if (j == row_wave) {
+                        mine_i = i;
+                        mine_g = g;
+                    }
+                    const bool whole = !FLAT && i + kWideRows <= n;
+                    const uint8_t *const at = reinterpret_cast<const uint8_t *>(q + i * a.q_stride + g * D);
+#pragma unroll
+                    for (int l = 0; l < W::kTileLoads; ++l) {
+                        const uint8_t *from = at + offset[l];
+                        if (!whole) {
+                            const int r = load_row + l * W::kLoadRows;
+                            const WeighRow w(a, min(row_lo + (tile + j) * kWideRows + r, rows - 1));
+                            const int token = FLAT ? w.i : min(i + r, n - 1), of_group = FLAT ? w.g : g;
+                            from = reinterpret_cast<const uint8_t *>(q + token * a.q_stride + of_group * D + load_chunk * 8);
+                        }
+                        __builtin_amdgcn_global_load_lds(
+                            (GlobalMem *)from, (SharedMem *)(to + ((j * W::kTileLoads + l) * kWeighThreads + wave * kLanes) * 16), 16, 0, 0);
+                    }
+                    if (!FLAT) advance(i, g);
+                }
+                // each wave's own
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(lses + int64_t(mine_i) * a.q_heads + mine_g) + offset_lse;
+                if (FLAT || mine_i + kWideRows > n) {
+                    const WeighRow w(a, min(row_lo + (tile + row_wave) * kWideRows + c, rows - 1));
+                    const int token = FLAT ? w.i : min(mine_i + c, n - 1), of_group = FLAT ? w.g : mine_g;
+                    from = reinterpret_cast<const uint8_t *>(lses + int64_t(token) * a.q_heads + of_group);
+                }
+                __builtin_amdgcn_global_load_lds((GlobalMem *)from, (SharedMem *)(to + W::kRowBytes + wave * kLanes * 4), 4, 0, 0);
+            };
+            constexpr int kSent = W::kLoads + 1;       // a wave's loads of a step
+
+            float sum[2][16] = {};
+            int next_i = i_lo, next_g = 0, mine_i = i_lo, mine_g = 0;      // of the step to be sent, of the wave's tile
+            if (!FLAT)
+                for (int j = 0; j < row_wave; ++j) advance(mine_i, mine_g);
             __syncthreads();                           // the ring's last readers
-            if (row_lo < row_hi) send(row_lo, 0);
-            if (row_lo + W::kStepRows < row_hi) send(row_lo + W::kStepRows, 1);
-            int slot = 0;
-            for (int row0 = row_lo; row0 < row_hi; row0 += W::kStepRows) {
-                // This step's loads have come, the next one's may be on their way: a bare barrier,
-                // since a fence would wait for them too.
-                if (row0 + W::kStepRows < row_hi) __builtin_amdgcn_s_waitcnt(kWaitLoads | (W::kLoads + 1));
-                else __builtin_amdgcn_s_waitcnt(kWaitLoads);
-                asm volatile("s_barrier" ::: "memory");
-                if (row0 + 2 * W::kStepRows < row_hi) send(row0 + 2 * W::kStepRows, slot == 0 ? 2 : slot - 1);
-                const int tile0 = row0 + row_wave * kWideRows;
-                const uint8_t *const tile = lds + slot * W::kStepBytes + row_wave * kWideRows * D * 2;
-                const float mine = *reinterpret_cast<const float *>(lds + slot * W::kStepBytes + W::kRowBytes +
-                                                                    (row_wave * kWideRows + c) * 4);
-                slot = slot == 2 ? 0 : slot + 1;
-                floatx16 x[2] = {};
+            if (tiles > 0) send(0, next_i, next_g, 0);
+            if (tiles > RW) send(RW, next_i, next_g, 1);
+            for (int tile = 0; tile < tiles;) {
 #pragma unroll
-                for (int m0 = 0; m0 < K::kSteps; m0 += 4) {
-                    bf16x8 b[4];
+                for (int slot = 0; slot < 3; ++slot) {
+                    // This step's loads have come, the next one's may be on their way: a bare
+                    // barrier, since a fence would wait for them too.
+                    if (tile + RW < tiles) __builtin_amdgcn_s_waitcnt(loads_left(kSent));
+                    else __builtin_amdgcn_s_waitcnt(loads_left(0));
+                    asm volatile("s_barrier" ::: "memory");
+                    const uint8_t *const step = lds + slot * W::kStepBytes;
+                    const float lse = *reinterpret_cast<const float *>(step + W::kRowBytes + wave * kLanes * 4 + c * 4);
+                    if (tile + 2 * RW < tiles) send(tile + 2 * RW, next_i, next_g, slot == 0 ? 2 : slot - 1);
+                    floatx16 x[2] = {};
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
-                        b[m] = *reinterpret_cast<const bf16x8 *>(tile + W::place(c, K::element(m0 + m, half) / 8) * 16);
+                    for (int m0 = 0; m0 < K::kSteps; m0 += 4) {
+                        bf16x8 b[4];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m)
+                        for (int m = 0; m < 4; ++m) b[m] = *reinterpret_cast<const bf16x8 *>(step + from[m0 + m]);
+#pragma unroll
+                        for (int m = 0; m < 4; ++m)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u)
+                                x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[u].k[m0 + m], b[m], x[u], 0, 0, 0);
+                    }
+                    // Where not every row sees every key, or some row does not count: what is not seen
+                    // is minus infinity, a weight of 0.
+                    bool in = counts(lse);
+                    int i = mine_i, last = mine_i + kWideRows - 1;
+                    if (FLAT) {
+                        const int row = row_lo + (tile + row_wave) * kWideRows;
+                        i = WeighRow(a, min(row, rows - 1)).i;
+                        last = row + kWideRows <= rows ? WeighRow(a, row + kWideRows - 1).i : n;
+                    }
+                    if (i < full_lo || last >= full_hi || tile + row_wave >= tiles || !__all(in)) {
+                        int token = mine_i + c;
+                        in = in && token < n && tile + row_wave < tiles;
+                        if (FLAT) {
+                            const int row = row_lo + (tile + row_wave) * kWideRows + c;
+                            in = counts(lse) && row < rows;
+                            token = WeighRow(a, min(row, rows - 1)).i;
+                        }
+                        unsigned long long sees = in ? seen_keys(a, past, n, min(token, n - 1), begin + min(token, n - 1), key) : 0ull;
+                        sees >>= 4 * half;
 #pragma unroll
                         for (int u = 0; u < 2; ++u)
-                            x[u] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(k[u].k[m0 + m], b[m], x[u], 0, 0, 0);
-                }
-                const bool in = counts(mine) && tile0 + c < rows;
-                const RowFacts f = row_facts(a, in ? mine : kNegInf);
-                float w[2][16];
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) w[u][e] = exp2_fast(__builtin_fmaf(x[u][e], a.scale_log2, -f.r));
-                // where not every row sees every key, or some row does not count
-                if (tile0 < full_lo || tile0 + kWideRows > full_hi || !__all(in)) {
-                    const int i = WeighRow(a, min(tile0 + c, rows - 1)).i;
-                    unsigned long long seen = in ? seen_keys(a, past, n, i, begin + i, key) : 0ull;
-                    seen >>= 4 * half;
+                            for (int e = 0; e < 16; ++e)
+                                x[u][e] = unsigned(sees >> 32 * u) >> (8 * (e / 4) + e % 4) & 1 ? x[u][e] : kNegInf;
+                    }
+                    const RowFacts f = row_facts(a, lse, in);
 #pragma unroll
                     for (int u = 0; u < 2; ++u)
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int bit = __builtin_amdgcn_sbfe(int(seen >> 32 * u), 8 * (e / 4) + e % 4, 1);
-                            w[u][e] = __uint_as_float(__float_as_uint(w[u][e]) & uint32_t(bit));
-                        }
+                        for (int e = 0; e < 16; ++e)
+                            sum[u][e] = __builtin_fmaf(exp2_fast(__builtin_fmaf(x[u][e], a.scale_log2, -f.r)), f.factor, sum[u][e]);
+                    if (!FLAT)
+#pragma unroll
+                        for (int j = 0; j < RW; ++j) advance(mine_i, mine_g);
+                    tile += RW;
+                    if (tile >= tiles) break;
                 }
-#pragma unroll
-                for (int u = 0; u < 2; ++u)
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) sum[u][e] = __builtin_fmaf(w[u][e], f.factor, sum[u][e]);
             }
             // lanes with bit 4 clear take the sums of the first 32 keys, the others those of the second
             const float both[2] = {column_sums(sum[0]), column_sums(sum[1])};
@@ -533,22 +599,32 @@ static int launch_few(const WeighArgs &a, int64_t context, int64_t most_rows, hi
 }
 
 template <int D, int BITS, int RW>
-static int launch_many_as(const WeighArgs &a, int64_t context, hipStream_t stream) {
+static int launch_many_as(const WeighArgs &a, int64_t context, bool flat, hipStream_t stream) {
     typedef WideShape<D, RW> W;
-    if constexpr (W::kLds > 64 * 1024)
-        if (!raise_lds<weigh_many_kernel<D, BITS, RW>>(W::kLds)) return NVFP4_EHIP;
     const dim3 grid = weigh_grid(a, ceil_div(context, kWeighWaves / RW * kWideKeys));
-    weigh_many_kernel<D, BITS, RW><<<grid, kWeighThreads, W::kLds, stream>>>(a);
-    return launch_status();
+    const auto launch = [&](auto is_flat) {
+        constexpr bool FLAT = decltype(is_flat)::value;
+        if constexpr (W::kLds > 64 * 1024)
+            if (!raise_lds<weigh_many_kernel<D, BITS, RW, FLAT>>(W::kLds)) return int(NVFP4_EHIP);
+        weigh_many_kernel<D, BITS, RW, FLAT><<<grid, kWeighThreads, W::kLds, stream>>>(a);
+        return launch_status();
+    };
+    return flat ? launch(IntC<1>()) : launch(IntC<0>());
 }
 
 template <int D, int BITS>
-static int launch_many(const WeighArgs &a, int64_t context, hipStream_t stream) {
+static int launch_many(const WeighArgs &a, int64_t context, bool even, hipStream_t stream) {
+    // Tiles of a head's tokens leave places of the last one empty, half of them where the
+    // lengths differ: taken where that is less than an eighth (2048 tokens over 32768 keys
+    // 705 us, of rows one after another 784; 64 over 8192 11.5 against 12.2; but 4 x 40
+    // tokens over 16k keys 74 against 49, 1 to 301 tokens of 7 sequences 74 against 65).
+    const int64_t mean = a.kv.tokens / a.kv.seqs, places = ceil_div(mean, 32) * 32 + (even ? 0 : 16);
+    const bool flat = 8 * places > 9 * mean || a.q_stride >= int64_t(1) << 25 || a.q_heads >= 1 << 24;
     // Waves share keys where there are not enough of them to give every CU two workgroups.
     const int64_t groups = ceil_div(context, kWeighWaves * kWideKeys) * a.kv.heads * a.kv.seqs;
-    if (groups >= 512) return launch_many_as<D, BITS, 1>(a, context, stream);
-    if (groups >= 256 || D == 256) return launch_many_as<D, BITS, 2>(a, context, stream);
-    return launch_many_as<D, BITS, D == 256 ? 2 : 4>(a, context, stream);
+    if (groups >= 512) return launch_many_as<D, BITS, 1>(a, context, flat, stream);
+    if (groups >= 256 || D == 256) return launch_many_as<D, BITS, 2>(a, context, flat, stream);
+    return launch_many_as<D, BITS, D == 256 ? 2 : 4>(a, context, flat, stream);
 }
 
 }  // namespace nvfp4
@@ -579,7 +655,7 @@ NVFP4_API int nvfp4_kv_weights(const nvfp4_kv_cache *cache, const nvfp4_kv_batch
     a.window = window;
     const double c = double(scale) * 1.4426950408889634074;
     a.scale_log2 = float(c);
-    a.lost = float((c - a.scale_log2) / scale);
+    a.lost = float((c - a.scale_log2) / scale - (1.4426950408889634074 - double(kLog2e)));
     a.decay = decay;
     // Which kernels, by the bounds: that for few rows alone, that for many alone where all
     // sequences are as long, or each for its own sequences.
@@ -592,7 +668,7 @@ NVFP4_API int nvfp4_kv_weights(const nvfp4_kv_cache *cache, const nvfp4_kv_batch
             constexpr int D = decltype(dim)::value, BITS = decltype(bits)::value;
             if (most_rows <= kFewRows || !even)
                 if (int st = launch_few<D, BITS>(a, context, most_rows, stream)) return st;
-            return most_rows > kFewRows ? launch_many<D, BITS>(a, context, stream) : NVFP4_OK;
+            return most_rows > kFewRows ? launch_many<D, BITS>(a, context, even, stream) : NVFP4_OK;
         });
     });
 }
