@@ -2,19 +2,24 @@
 quantised, paged key/value cache, as a program uses them:
 
     qkv = Wqkv x              nvfp4_gemv, float32
+    q, k turned by position   nvfp4_rope, where the layer has frequencies
     cache <- k, v             nvfp4_kv_append, from the product's own rows
     o = attention(q, cache)   nvfp4_kv_attention
+    weights <- p(q, cache)    nvfp4_kv_weights, where the step is given weights
     y = Wo o                  nvfp4_gemv
 
 One AttentionLayer serves prefill chunks, decode steps, batches of both, and the
 verify of a tree of drafted tokens.  A decode step has no host-side state but the
 batch's bounds, so it can be captured in a graph that advances the sequences by
-itself.  Normalisation and the rotation of q and k by position are not part of it.
+itself.  A cache that is to stay within a budget is cut by `evict`, which keeps the
+keys that the gathered weights name (nvfp4_kv_evict); tokens keep the positions that
+they were turned by.  Normalisation is not part of it.
 
     python -m block_scaled_bit_nvfp4_amd.attention_layer
 
 runs one: a prompt in two chunks, decode steps replayed from a graph, and a verify
-of seven drafted tokens, and prints what each took.
+of seven drafted tokens, decode steps that gather their weights and the eviction
+of half of the cache, and prints what each took.
 """
 from __future__ import annotations
 
@@ -28,10 +33,13 @@ import block_scaled_bit_nvfp4_amd as nv
 class AttentionLayer:
     """Weights [rows, cols] float32 on the GPU, quantised to NVFP4 here: wqkv
     [(q_heads + 2 * heads) * head_dim, hidden] (queries, keys, values), wo [hidden,
-    q_heads * head_dim].  max_tokens: the most tokens of a step."""
+    q_heads * head_dim].  max_tokens: the most tokens of a step.  freqs, axis, adjacent
+    and rope_factor: how q and k are turned, as nvfp4_rope takes them; not at all
+    without freqs."""
 
     def __init__(self, wqkv, wo, q_heads, heads, head_dim, max_tokens, pages, page_tokens=64,
-                 k_format=nv.NVFP4_KV_MXFP8, v_format=nv.NVFP4_KV_MXFP8):
+                 k_format=nv.NVFP4_KV_MXFP8, v_format=nv.NVFP4_KV_MXFP8, freqs=None, axis=None, adjacent=False,
+                 rope_factor=1.0):
         self.q_heads, self.heads, self.head_dim = q_heads, heads, head_dim
         self.hidden = wo.shape[0]
         rows = (q_heads + 2 * heads) * head_dim
@@ -42,13 +50,14 @@ class AttentionLayer:
         self.wqkv, self.wo = self._weights(wqkv), self._weights(wo)
         self.cache = nv.alloc_kv_cache(pages, page_tokens, heads, head_dim, k_format, v_format, self.device)
         self.scale = head_dim ** -0.5
+        self.freqs, self.axis, self.adjacent, self.rope_factor = freqs, axis, adjacent, rope_factor
 
         def buffer(width, dtype):
             return torch.empty(max_tokens, width, dtype=dtype, device=self.device)
 
         self.qkv = buffer(rows, torch.float32)
         self.q, self.o = buffer(q_heads * head_dim, torch.bfloat16), buffer(q_heads * head_dim, torch.bfloat16)
-        self.y = buffer(self.hidden, torch.float32)
+        self.y, self.lse = buffer(self.hidden, torch.float32), buffer(q_heads, torch.float32)
         self.workspace = torch.empty(0, dtype=torch.uint8, device=self.device)
         self.retired = []            # outgrown workspaces, see reserve
 
@@ -79,13 +88,23 @@ class AttentionLayer:
                 self.retired.append(self.workspace)
             self.workspace = torch.empty(max(need, 2 * have), dtype=torch.uint8, device=self.device)
 
-    def step(self, x, batch, window=0, tree=None):
+    def alloc_weights(self, batch):
+        """Weights of 0 for the sequences of `batch`: of every key its page table can name."""
+        seqs, width = batch.arrays[0].shape
+        return torch.zeros(seqs, self.heads, width * self.cache.page_tokens, device=self.device)
+
+    def step(self, x, batch, window=0, tree=None, positions=None, weights=None, decay=1.0):
         """x bfloat16 [tokens, hidden], the batch's new tokens in its order; the
-        result float32 [tokens, hidden], overwritten by the next step."""
+        result float32 [tokens, hidden], overwritten by the next step.  positions int32
+        [tokens] or [axes, tokens]: the tokens' own, for a layer that turns q and k (after
+        an eviction they are no longer their places in the cache).  weights: of
+        alloc_weights, to which the step adds the attention that each key receives."""
         n = batch.tokens
         if n > self.max_tokens or tuple(x.shape) != (n, self.hidden):
             raise ValueError("x has shape %s, expected (%d, %d) with at most %d tokens" % (
                 tuple(x.shape), n, self.hidden, self.max_tokens))
+        if (positions is None) != (self.freqs is None):
+            raise ValueError("positions come with a layer that has freqs, and only with one")
         if n == 0:
             return self.y[:0]
         self.reserve(batch)
@@ -93,13 +112,27 @@ class AttentionLayer:
         nv.nvfp4_gemv(*self.wqkv, x, n, qkv)
         q, o = self.q[:n].view(n, self.q_heads, self.head_dim), self.o[:n].view(n, self.q_heads, self.head_dim)
         heads = qkv.view(n, -1, self.head_dim)
-        q.copy_(heads[:, :self.q_heads])
-        nv.nvfp4_kv_append(self.cache, batch, heads[:, self.q_heads:self.q_heads + self.heads],
-                           heads[:, self.q_heads + self.heads:])
-        nv.nvfp4_kv_attention(self.cache, batch, q, self.scale, o, window=window, tree=tree,
+        k = heads[:, self.q_heads:self.q_heads + self.heads]
+        if self.freqs is None:
+            q.copy_(heads[:, :self.q_heads])
+        else:
+            nv.nvfp4_rope([(heads[:, :self.q_heads], q), (k, k)], positions, self.freqs, self.axis, self.adjacent,
+                          self.rope_factor)
+        nv.nvfp4_kv_append(self.cache, batch, k, heads[:, self.q_heads + self.heads:])
+        lse = None if weights is None else self.lse[:n]
+        nv.nvfp4_kv_attention(self.cache, batch, q, self.scale, o, lse=lse, window=window, tree=tree,
                               workspace=self.workspace)
+        if weights is not None:
+            nv.nvfp4_kv_weights(self.cache, batch, q, self.scale, lse, weights, decay=decay, window=window, tree=tree)
         nv.nvfp4_gemv(*self.wo, o.view(n, wide), n, self.y[:n])
         return self.y[:n]
+
+    def evict(self, batch, weights, budget, kept, first=0, recent=0):
+        """Cut the batch's sequences that hold more than `budget` tokens (`past`, without
+        the step's new ones) down to it, past itself included: of each head the first
+        `first`, the last `recent` and the keys of the largest weights stay.  kept int32
+        [seqs, heads, budget] gets their places before the cut; weights move with them."""
+        nv.nvfp4_kv_evict(self.cache, batch, weights, budget, kept, batch.arrays[2], first=first, recent=recent)
 
 
 def chain_mask(n, device):
@@ -117,7 +150,9 @@ def main(hidden=5120, q_heads=40, heads=8, head_dim=128, prompt=4096, steps=64, 
     pages = -(-room // page)
     layer = AttentionLayer(torch.randn((q_heads + 2 * heads) * head_dim, hidden, device=device) * 0.02,
                            torch.randn(hidden, q_heads * head_dim, device=device) * 0.02,
-                           q_heads, heads, head_dim, chunk, pages, page)
+                           q_heads, heads, head_dim, chunk, pages, page,
+                           freqs=10000.0 ** -(torch.arange(head_dim // 2, dtype=torch.float64, device=device) * 2 / head_dim))
+    place = torch.arange(room, dtype=torch.int32, device=device)
     table = torch.randperm(pages, device=device).to(torch.int32).view(1, pages)
     past = torch.zeros(1, dtype=torch.int32, device=device)
 
@@ -137,28 +172,43 @@ def main(hidden=5120, q_heads=40, heads=8, head_dim=128, prompt=4096, steps=64, 
     for at in (0, chunk):                        # the prompt, in two chunks
         past.fill_(at)
         b = batch(chunk, at + chunk)
-        timed("prefill of %d tokens after %d" % (chunk, at), lambda: layer.step(x, b))
+        timed("prefill of %d tokens after %d" % (chunk, at),
+              lambda: layer.step(x, b, positions=place[at:at + chunk]))
     past.fill_(prompt)
 
-    # Decode: one token a step; the graph moves `past` on by itself.
-    token, b = x[:1].clone(), batch(1, room)
+    # Decode: one token a step; the graph moves `past` and the position on by itself.
+    token, b, at = x[:1].clone(), batch(1, room), past.clone()
     layer.reserve(b)
     stream = torch.cuda.Stream()
     stream.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(stream):
-        layer.step(token, b)
+        layer.step(token, b, positions=at)
     torch.cuda.current_stream().wait_stream(stream)
     graph = torch.cuda.CUDAGraph()
     with torch.cuda.graph(graph):
-        y = layer.step(token, b)
+        y = layer.step(token, b, positions=at)
         token.copy_(y)                           # a stand-in for the rest of the layers
         past.add_(1)
+        at.add_(1)
     timed("decode step after %d tokens (graph)" % prompt, graph.replay, steps - 1)
 
     # Verify: seven drafted tokens and the one before them, as a tree of one chain.
     n = 8
     b, tree = batch(n, room), chain_mask(n, device)
-    timed("verify of %d tokens (tree)" % n, lambda: layer.step(x[:n], b, tree=tree), 20)
+    timed("verify of %d tokens (tree)" % n,
+          lambda: layer.step(x[:n], b, tree=tree, positions=place[prompt + steps:prompt + steps + n]), 20)
+
+    # A budget: steps that gather what the keys receive, and the cut to half of the cache.
+    b = batch(1, room)
+    weights, kept = layer.alloc_weights(b), torch.empty(1, heads, prompt // 2, dtype=torch.int32, device=device)
+    timed("decode step that gathers weights", lambda: layer.step(token, b, positions=at, weights=weights), 20)
+
+    def cut():
+        past.fill_(prompt)
+        layer.evict(b, weights, prompt // 2, kept, first=4, recent=64)
+
+    timed("eviction of %d tokens of %d" % (prompt - prompt // 2, prompt), cut, 20)
+    timed("decode step after it", lambda: layer.step(token, b, positions=at, weights=weights), 20)
 
 
 if __name__ == "__main__":
