@@ -67,7 +67,10 @@ def _split(qkv, heads, dim):
 @pytest.mark.parametrize("tokens,heads,dim,rotary,axes", [
     (1, (32, 8), 128, 128, 1), (2, (5,), 8, 8, 2), (63, (3, 1, 2), 72, 72, 2), (300, (16, 16), 80, 40, 3),
     (7, (1, 1, 1, 1), 1024, 64, 1), (1500, (40, 8), 128, 128, 3), (33, (12, 2), 256, 64, 3), (129, (4,), 64, 24, 4),
-    (4099, (7,), 72, 72, 2)])
+    (4099, (7,), 72, 72, 2),
+    # enough of them for sines and cosines that are shared: heads in ranges, units of every kind
+    (1300, (16, 16), 80, 40, 3), (400, (1, 1, 1, 1), 1024, 64, 1), (101, (23, 2), 1024, 1024, 2), (9001, (5,), 64, 24, 4),
+    (50001, (5, 1), 8, 8, 2), (1500, (3, 70), 256, 256, 1)])
 def test_against_the_oracle(tokens, heads, dim, rotary, axes, dtype, adjacent):
     rng = np.random.default_rng(tokens + dim)
     pairs = rotary // 2
@@ -78,14 +81,35 @@ def test_against_the_oracle(tokens, heads, dim, rotary, axes, dtype, adjacent):
     kept = qkv.clone()
     ins = _split(qkv, heads, dim)
     # outputs of either type, one of them in rows of its own stride
-    outs = [torch.full((tokens, h + i, dim), float("nan"), dtype=(BF16, F32)[i % 2], device=G.DEV)[:, :h]
+    wide = [torch.full((tokens, h + i, dim), float("nan"), dtype=(BF16, F32)[i % 2], device=G.DEV)
             for i, h in enumerate(heads)]
+    outs = [w[:, :h] for w, h in zip(wide, heads)]
     G.note("rope %d tokens, heads %s of %d, %d turn, %d axes, %s" % (tokens, heads, dim, rotary, axes, dtype))
     nv.nvfp4_rope(list(zip(ins, outs)), _dev(positions, torch.int32), _dev(freqs, torch.float64),
                   None if axis is None else _dev(axis, torch.uint8), adjacent, factor)
     assert torch.equal(qkv, kept)
     for i, (x, out) in enumerate(zip(ins, outs)):
         _check(out, x, positions, freqs, axis, adjacent, factor, "set %d" % i)
+        assert wide[i][:, heads[i]:].isnan().all()
+
+
+@pytest.mark.parametrize("adjacent", [False, True])
+@pytest.mark.parametrize("dtype,dim,rotary", [(BF16, 128, 128), (BF16, 72, 72), (F32, 128, 96)])
+def test_a_token_alone_and_among_many(dtype, dim, rotary, adjacent):
+    """A token's result does not depend on how many others the call has."""
+    tokens, heads = 2500, (12, 3)
+    rng = np.random.default_rng(dim)
+    positions = _dev(rng.integers(0, 1 << 16, (2, tokens)), torch.int32)
+    freqs, axis = _dev(_freqs(rotary // 2), torch.float64), _dev(rng.integers(0, 2, rotary // 2), torch.uint8)
+    ins = _split(_qkv(tokens, heads, dim, dtype, 5), heads, dim)
+    outs = [torch.empty(tokens, h, dim, dtype=BF16, device=G.DEV) for h in heads]
+    G.note("rope, a token among many, %s" % dtype)
+    nv.nvfp4_rope(list(zip(ins, outs)), positions, freqs, axis, adjacent, 1.5)
+    for t in (0, 1, 1249, tokens - 1):
+        one = [torch.empty(1, h, dim, dtype=BF16, device=G.DEV) for h in heads]
+        nv.nvfp4_rope(list(zip([x[t:t + 1] for x in ins], one)), positions[:, t:t + 1].contiguous(), freqs, axis, adjacent, 1.5)
+        for a, b in zip(one, outs):
+            assert torch.equal(a[0], b[t])
 
 
 @pytest.mark.parametrize("adjacent", [False, True])
