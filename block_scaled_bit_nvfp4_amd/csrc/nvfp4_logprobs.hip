@@ -6,7 +6,9 @@
 // `top` largest logits as keys.  A second launch joins a row's chunks,
 //   l = sum l_c e^(m_c - m),  t = sum e^(m_c - m) (t_c + l_c (m_c - m)),
 //   lse = m + log l,  entropy = log l - t / l,
-// and looks the given tokens up.
+// and looks the given tokens up.  Bound by reading the logits once: 512 rows of 151936 in
+// fp32 take 59 us and the join 6.5 (5.3 TB/s, a large copy's rate); one row 6 and 4.8, two
+// launches.
 //
 // The largest logits of a chunk are found without sorting it.  The top-th largest of a
 // wave's 64 lane maxima is no larger than the chunk's top-th largest, since that many
@@ -29,6 +31,13 @@ constexpr int64_t kLogpFill = 512;                // workgroups with long chunks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 
+// Sums of one part relative to its maximum.  l is in 64 bits: where one token is all but
+// certain, l is 1 and a little, and that little is all of its log probability.
+struct Sums {
+    float m, t;
+    double l;
+};
+
 struct LogpArgs {
     const void *logits;
     int64_t stride;
@@ -37,7 +46,7 @@ struct LogpArgs {
     const int *tokens;
     float *logp, *lse, *entropy, *top_logp;
     int *top_index;
-    float *parts;          // [n][chunks][4]: m, l, t, unused
+    Sums *parts;           // [n][chunks]
     Key *keys;             // [n][chunks][top]
 };
 
@@ -68,6 +77,28 @@ __device__ __forceinline__ float over_wave(float v, F f) {
     v = f(__uint_as_float(a[0]), __uint_as_float(a[1]));
     const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
     return f(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+// The same sum of a 64-bit number, both of whose halves go between the lanes.
+template <int CTRL>
+__device__ __forceinline__ double lane_of(double v) {
+    const u32x2 w = __builtin_bit_cast(u32x2, v);
+    const u32x2 y = {uint32_t(__builtin_amdgcn_update_dpp(0, int(w[0]), CTRL, 0xF, 0xF, false)),
+                     uint32_t(__builtin_amdgcn_update_dpp(0, int(w[1]), CTRL, 0xF, 0xF, false))};
+    return __builtin_bit_cast(double, y);
+}
+__device__ __forceinline__ double wave_sum(double v) {
+    v += lane_of<0xB1>(v);
+    v += lane_of<0x4E>(v);
+    v += lane_of<0x141>(v);
+    v += lane_of<0x140>(v);
+    u32x2 w = __builtin_bit_cast(u32x2, v);
+    const auto a0 = __builtin_amdgcn_permlane16_swap(w[0], w[0], false, false);
+    const auto a1 = __builtin_amdgcn_permlane16_swap(w[1], w[1], false, false);
+    v = __builtin_bit_cast(double, u32x2{a0[0], a1[0]}) + __builtin_bit_cast(double, u32x2{a0[1], a1[1]});
+    w = __builtin_bit_cast(u32x2, v);
+    const auto b0 = __builtin_amdgcn_permlane32_swap(w[0], w[0], false, false);
+    const auto b1 = __builtin_amdgcn_permlane32_swap(w[1], w[1], false, false);
+    return __builtin_bit_cast(double, u32x2{b0[0], b1[0]}) + __builtin_bit_cast(double, u32x2{b0[1], b1[1]});
 }
 __device__ __forceinline__ float wave_sum(float v) { return over_wave(v, [](float x, float y) { return x + y; }); }
 __device__ __forceinline__ float wave_largest(float v) { return over_wave(v, [](float x, float y) { return fmaxf(x, y); }); }
@@ -169,16 +200,12 @@ __device__ __forceinline__ void largest(TopShared &sh, int top, uint32_t most, O
     }
 }
 
-// Sums of one part relative to its maximum.
-struct Sums {
-    float m, l, t;
-};
 // A part's sums relative to m >= s.m; parts of nothing (m = -infinity, l = 0) stay
 // nothing, and a difference past fp32's range has no infinity to multiply a weight of 0.
 __device__ __forceinline__ Sums moved(Sums s, float m) {
     const float d = s.m == kNegInf ? 0.0f : fmaxf(s.m - m, -1e30f);
     const float w = __builtin_amdgcn_exp2f(d * kLog2e);
-    return Sums{m, s.l * w, w * __builtin_fmaf(s.l, d, s.t)};
+    return Sums{m, w * __builtin_fmaf(float(s.l), d, s.t), s.l * w};
 }
 
 __device__ __forceinline__ float logit(const float *row, int at) { return row[at]; }
@@ -223,6 +250,18 @@ __device__ __forceinline__ void load_logits(const uint16_t *row, bool full, int 
     for (int i = 0; i < N; ++i) x[i] = __uint_as_float(i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
 }
 
+// log x for x > 0 (NaN stays NaN): of the power of two in 64 bits, of what is left, which
+// is within 0.7 .. 1.4, by its distance from 1, so that the result is good to 2^-22 of
+// itself also next to x = 1.
+__device__ __forceinline__ double log_of(double x) {
+    double part = __builtin_amdgcn_frexp_mant(x);
+    int power = __builtin_amdgcn_frexp_exp(x);
+    const bool low = part < 0.70710678118654752440;
+    part = low ? part + part : part;
+    power -= low;
+    return power * 0.69314718055994530942 + log1pf(float(part - 1.0));
+}
+
 template <class T, int N>
 __global__ void __launch_bounds__(kLogpThreads, 8) logprobs_chunk_kernel(LogpArgs a) {
     __shared__ TopShared sh;
@@ -239,13 +278,13 @@ __global__ void __launch_bounds__(kLogpThreads, 8) logprobs_chunk_kernel(LogpArg
 #pragma unroll
     for (int i = 1; i < N; ++i) most = fmaxf(most, x[i]);
     const float top = wave_largest(most);
-    Sums s = {top * a.scale, 0.0f, 0.0f};
+    Sums s = {top * a.scale, 0.0f, 0.0};
     const float base = s.m == kNegInf ? 0.0f : s.m;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float d = __builtin_fmaf(x[i], a.scale, -base);
         const float e = __builtin_amdgcn_exp2f(d * kLog2e);
-        s.l += e;
+        s.l += double(e);
         s.t = __builtin_fmaf(e, fmaxf(d, -1e30f), s.t);
     }
     s.l = wave_sum(s.l);
@@ -287,17 +326,14 @@ __global__ void __launch_bounds__(kLogpThreads, 8) logprobs_chunk_kernel(LogpArg
         float m = sums[0].m;
 #pragma unroll
         for (int w = 1; w < kLogpWaves; ++w) m = fmaxf(m, sums[w].m);
-        Sums all = {m, 0.0f, 0.0f};
+        Sums all = {m, 0.0f, 0.0};
 #pragma unroll
         for (int w = 0; w < kLogpWaves; ++w) {
             const Sums o = moved(sums[w], m);
             all.l += o.l;
             all.t += o.t;
         }
-        float *p = a.parts + part * 4;
-        p[0] = all.m;
-        p[1] = all.l;
-        p[2] = all.t;
+        a.parts[part] = all;
     }
 }
 
@@ -306,7 +342,7 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
     __shared__ Sums sums[kLogpWaves];
     __shared__ Key best[NVFP4_MAX_TOP];
     const int tid = threadIdx.x, wave = tid / kLanes, r = blockIdx.x;
-    const float *parts = a.parts + int64_t(r) * a.chunks * 4;
+    const Sums *const parts = a.parts + int64_t(r) * a.chunks;
     // the chunks' keys, the first of them in registers
     constexpr int kKept = 8;
     const int64_t all_keys = int64_t(a.chunks) * a.top;
@@ -316,11 +352,11 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
 #pragma unroll
     for (int i = 0; i < kKept; ++i) mine[i] = tid + i * kLogpThreads < all_keys ? keys[tid + i * kLogpThreads] : Key(0);
     float m = kNegInf;
-    for (int c = tid; c < a.chunks; c += kLogpThreads) m = fmaxf(m, parts[4 * c]);
+    for (int c = tid; c < a.chunks; c += kLogpThreads) m = fmaxf(m, parts[c].m);
     m = wave_largest(m);
-    Sums s = {m, 0.0f, 0.0f};
+    Sums s = {m, 0.0f, 0.0};
     for (int c = tid; c < a.chunks; c += kLogpThreads) {
-        const Sums o = moved(Sums{parts[4 * c], parts[4 * c + 1], parts[4 * c + 2]}, m);
+        const Sums o = moved(parts[c], m);
         s.l += o.l;
         s.t += o.t;
     }
@@ -331,19 +367,19 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
     m = sums[0].m;
 #pragma unroll
     for (int w = 1; w < kLogpWaves; ++w) m = fmaxf(m, sums[w].m);
-    Sums all = {m, 0.0f, 0.0f};
+    Sums all = {m, 0.0f, 0.0};
 #pragma unroll
     for (int w = 0; w < kLogpWaves; ++w) {
         const Sums o = moved(sums[w], m);
         all.l += o.l;
         all.t += o.t;
     }
-    const bool nothing = m == kNegInf && all.l == 0.0f;
-    const float log_l = __builtin_logf(all.l);
-    const float lse = nothing ? kNegInf : m + log_l;
-    const float entropy = nothing ? 0.0f : log_l - all.t / all.l;
+    const bool nothing = m == kNegInf && all.l == 0.0;
+    const double log_l = log_of(all.l);
+    const float lse = nothing ? kNegInf : float(m + log_l);
+    const float entropy = nothing ? 0.0f : float(log_l - all.t / all.l);
     // z - lse without the rounding of a large lse
-    const auto logp = [&](float x) { return nothing ? kNegInf : __builtin_fmaf(x, a.scale, -m) - log_l; };
+    const auto logp = [&](float x) { return nothing ? kNegInf : float(__builtin_fma(double(x), double(a.scale), -double(m)) - log_l); };
     if (tid == 0) {
         if (a.lse) a.lse[r] = lse;
         if (a.entropy) a.entropy[r] = entropy;
@@ -381,7 +417,7 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
 }
 
 // Logits of a workgroup: chunks of 2048 where longer ones would leave CUs idle (one row of
-// 151936: 10.6 us, of 8192 13.7; 16 rows 13.4 and 15.3), else of 8192 (128 rows 28 us, of
+// 151936: 10.8 us, of 8192 14; 16 rows 13.7 and 15.6), else of 8192 (128 rows 28 us, of
 // 2048 36; 512 rows 70 and 115).
 static int64_t logprobs_chunk(int64_t n, int64_t vocab) {
     return (n * ceil_div(vocab, kLong * kLogpThreads) < kLogpFill ? kShort : kLong) * kLogpThreads;
@@ -435,8 +471,8 @@ NVFP4_API int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t v
     a.entropy = entropy;
     a.top_logp = top_logp;
     a.top_index = top_index;
-    a.parts = static_cast<float *>(workspace);
-    a.keys = reinterpret_cast<Key *>(a.parts + size_t(n) * a.chunks * 4);
+    a.parts = static_cast<Sums *>(workspace);
+    a.keys = reinterpret_cast<Key *>(a.parts + size_t(n) * a.chunks);
     const unsigned groups = unsigned(n * a.chunks);
     const auto launch = [&](auto kernel) { kernel<<<groups, kLogpThreads, 0, stream>>>(a); };
     if (dtype == NVFP4_KV_F32) launch(short_chunks ? logprobs_chunk_kernel<float, kShort> : logprobs_chunk_kernel<float, kLong>);

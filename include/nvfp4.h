@@ -494,7 +494,8 @@ int nvfp4_rope(const nvfp4_rope_rows *rows, int count, int dtype, int64_t tokens
  * has lse and all log probabilities -infinity and entropy 0; one with a z of +infinity
  * or NaN has lse, log probabilities and entropy NaN.  Outputs may each be NULL
  * (tokens and logp together, with given = 0; top_logp and top_index both, with top =
- * 0), but not all.  Sums are fp32 in a fixed order.  0 <= n, 1 <= vocab <= 2^30,
+ * 0), but not all.  Sums are taken in a fixed order, that of exp in 64 bits, so that
+ * log probabilities and entropy near 0 keep their digits.  0 <= n, 1 <= vocab <= 2^30,
  * 0 <= top <= min(vocab, NVFP4_MAX_TOP), stride >= vocab (else NVFP4_ESHAPE),
  * 0 <= given <= 2^20; logits need only their element's alignment, outputs 4 bytes.
  * workspace: nvfp4_logprobs_workspace_bytes(n, vocab, top) bytes, 16-byte aligned,

@@ -80,6 +80,30 @@ def _logits(n, vocab, seed, dtype, extra=0):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n,vocab", [(1, 151936), (3, 5003), (600, 9001)])
+def test_a_token_that_is_all_but_certain(n, vocab, dtype):
+    """Where l is 1 and a little, that little counts: log probability and entropy to a few
+    units of themselves.  Terms are 3 |d| + 2 units off, |d| at most 32, and log l four more:
+    102, below 128; t's terms are one more off and added in at most 64 steps: below 256."""
+    g = torch.Generator(G.DEV).manual_seed(vocab)
+    logits = torch.randn(n, vocab, generator=g, device=G.DEV).clamp(-5, 5)
+    at = torch.randint(0, vocab, (n,), generator=g, device=G.DEV)
+    logits[torch.arange(n, device=G.DEV), at] = torch.linspace(14, 27, n, device=G.DEV)
+    logits = logits.to(dtype)
+    G.note("logprobs of all but certain tokens, %d x %d %s" % (n, vocab, dtype))
+    out = _run(logits, at.view(n, 1).int(), 1)
+    assert torch.equal(out["top_index"][:, 0].long(), at)
+    z = logits.double().cpu()
+    d = z - z.amax(1, keepdim=True)
+    little = torch.where(d == 0, torch.zeros_like(d), d.exp()).sum(1)
+    logp = -torch.log1p(little)
+    entropy = torch.log1p(little) - (d.exp() * d).sum(1) / (1 + little)
+    for name, want, units in (("logp", logp, 128), ("top_logp", logp, 128), ("entropy", entropy, 256)):
+        got = out[name].double().cpu().view(-1)
+        assert ((got - want).abs() <= units * UNIT * want.abs()).all(), name
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
 @pytest.mark.parametrize("n,vocab,top,given,extra,scale", [
     (1, 1, 1, 1, 0, 1.0), (3, 2, 1, 2, 0, 1.0), (2, 63, 63, 0, 1, 0.5), (2, 64, 64, 1, 0, 1.0), (5, 100, 20, 3, 3, 2.0),
     (4, 1023, 5, 1, 0, 1.0), (1, 8191, 64, 1, 1, 1.0), (2, 8192, 64, 2, 0, 0.7), (2, 8193, 64, 1, 2, 1.0),
