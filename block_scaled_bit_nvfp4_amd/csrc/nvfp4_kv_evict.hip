@@ -7,15 +7,18 @@
 // keys are counted by their top 12 bits; the bin that holds the border usually holds few,
 // whose ranks are found by comparing all of them with all; only where it holds many (equal
 // weights) the next 12 bits are counted.  Then one walk in order writes the kept positions
-// and moves their weights.  Up to 8192 or 32768 positions stay in registers throughout.
+// and moves their weights.  Up to 8192, 16384 or 32768 positions, by the bound, stay in
+// registers throughout.  Bound by its chain of dependent steps: 10.6 us for 4607 positions.
 //
 // Move: a kept token's slot is never past its old one, and both rise together.  So one
 // workgroup can move a stretch of tokens at a time, all reads before all writes, and the
 // places that it overwrites are behind everything it has yet to read.  The bytes of a
 // unit are split over workgroups so that no two share any: a piece of the keys' codes, a
 // part of the values' rows, either side's scales.  What bounds it: three dependent loads
-// for a stretch (the kept position, its page, the bytes), so that a stretch is 4096 tokens;
-// and, in large batches, bytes, of which a line that holds one kept token is read whole.
+// for a stretch (the kept position, its page, the bytes), so that a stretch is 4096 tokens
+// (11.5 us for 4096 of 4607); and, in large batches, bytes, of which a line that holds one
+// kept token is read whole (64 sequences of 1 to 8191 to 2048: 104 us, 3.4 TB/s of what
+// memory moves).  512 threads: with 256 these two take 13 and 106 us, with 1024 12 and 113.
 #include "nvfp4_kv.h"
 
 namespace nvfp4 {
@@ -342,9 +345,12 @@ NVFP4_API int nvfp4_kv_evict(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *
     a.budget = budget;
     a.first = first;
     a.recent = recent;
-    // Eight positions a thread where the bound allows it: with fewer registers two workgroups
-    // fit a CU.
+    // The fewest positions a thread that the bound allows: with eight two workgroups fit a CU
+    // (4607 positions 21.7 us, both launches, with 32 a thread 29.0; 9000 positions 26.6 with 16,
+    // 31.2 with 32), but what does not stay in registers is read several times (32768 positions
+    // 38.8 us with 32 a thread, 45.7 with 8 or 16).
     if (batch->max_context <= 8 * kSelectThreads) kv_evict_select_kernel<8><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
+    else if (batch->max_context <= 16 * kSelectThreads) kv_evict_select_kernel<16><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
     else kv_evict_select_kernel<32><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
     if (int st = launch_status()) return st;
     const int kb = cache->k_format == NVFP4_KV_MXFP8 ? 8 : 4, vb = cache->v_format == NVFP4_KV_MXFP8 ? 8 : 4;

@@ -117,7 +117,8 @@ def test_sequences_that_stay():
     _run(table, keys, values, past, weights, page, budget, 2, 5)
 
 
-@pytest.mark.parametrize("length,budget", [(20000, 19000), (20000, 5000), (70001, 4096)])
+@pytest.mark.parametrize("length,budget", [(20000, 19000), (20000, 5000), (70001, 4096), (8193, 8000), (12000, 3001),
+                                           (16384, 140), (16385, 16384)])
 def test_long_sequences(length, budget):
     """Many stretches of tokens, and a page at the end that is filled in part."""
     rng = np.random.default_rng(3)
