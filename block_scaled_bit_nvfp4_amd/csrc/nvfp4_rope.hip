@@ -386,6 +386,8 @@ NVFP4_API int nvfp4_rope(const nvfp4_rope_rows *rows, int count, int dtype, int6
             return NVFP4_EALIGN;
         // in place a thread reads what it writes, and nothing else, only where both are laid out the same
         if (r.in && r.in == r.out && (r.out_type != dtype || r.in_stride != r.out_stride)) return NVFP4_EINVAL;
+        for (int k = 0; k < i; ++k)
+            if (r.out && (r.out == rows[k].out || r.out == rows[k].in || r.in == rows[k].out)) return NVFP4_EINVAL;
         a.set[i] = RopeSet{r.in, r.out, r.in_stride, r.out_stride, a.heads, r.out_type == NVFP4_KV_F32};
         a.heads += r.heads;
     }

@@ -459,7 +459,8 @@ int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch,
  * take one launch.  A set is [tokens][heads][head_dim] of `dtype` (NVFP4_KV_BF16 or
  * _F32), in_stride elements between tokens (column ranges of one projection's
  * output), written as out_type with out_stride.  A set may be rotated in place (out
- * the same pointer, type and stride as in); otherwise outputs overlap nothing else.
+ * the same pointer, type and stride as in); otherwise outputs overlap nothing else (an
+ * output that is another set's input or output is NVFP4_EINVAL).
  * head_dim is a multiple of 8 up to 1024, rotary_dim a multiple of 8 up to
  * head_dim (else NVFP4_ESHAPE); pointers 16-byte aligned with strides of whole 16
  * bytes, freqs 8-byte and positions 4-byte aligned (else NVFP4_EALIGN).  axis may
@@ -550,8 +551,8 @@ int nvfp4_kv_weights(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, c
  * pages, byte for byte.  What stands behind them is left as it was, and the pages
  * that hold no slot below the budget are free for other use.  A sequence some of
  * whose past[s] positions have no page is left as it is: kept -1, weights moved
- * nowhere, left[s] = past[s].  A page named by two sequences (a shared prefix)
- * must not be in one that is cut.  budget >= 1, first, recent >= 0, first + recent <= budget (else
+ * nowhere, left[s] = past[s].  A page that is named twice (a prefix that two
+ * sequences share) must not be in one that is cut.  budget >= 1, first, recent >= 0, first + recent <= budget (else
  * NVFP4_EINVAL); budget at most 2^30 / (seqs * heads), and width at least
  * table_width * page_tokens (else NVFP4_ESHAPE); arrays 4-byte aligned. */
 int nvfp4_kv_evict(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch, int budget, int first, int recent,

@@ -96,6 +96,35 @@ def test_against_the_oracle(new, past, dim, heads, q_heads, page, k_fmt):
         _run(rng, table, keys, values, new, past, q_heads, page, decay=decay)
 
 
+@pytest.mark.parametrize("context", [None, 40000, 200000])
+@pytest.mark.parametrize("dim,heads,q_heads,k_fmt", [(64, 2, 6, 8), (128, 1, 5, 4), (128, 2, 14, 8), (256, 1, 3, 8), (64, 1, 64, 4)])
+@pytest.mark.parametrize("new,past,window", [
+    ((64,), (0,), 0), ((96, 96), (130, 5), 0), ((333,), (70,), 0), ((500, 400), (0, 33), 0), ((256,), (400,), 90),
+    ((289,), (1,), 33), ((64, 64, 64), (0, 1, 200), 1)])
+def test_tiles_of_a_heads_tokens(new, past, window, dim, heads, q_heads, k_fmt, context):
+    """Sequences whose tokens fill tiles of 32, at the three ways of sharing keys and rows
+    among waves that the bound of the context picks."""
+    rng = np.random.default_rng(sum(new) + dim + window)
+    table, keys, values = K.filled(rng, new, past, heads, dim, k_fmt, 8, 32)
+    G.note("weights of tiles, %s after %s, %d/%d heads of %d, window %d" % (new, past, q_heads, heads, dim, window))
+
+    def spoil(q, lse):
+        lse[[0, 31, 32, sum(new) - 1], [0, q_heads - 1, 1, 0]] = np.nan, np.inf, -np.inf, np.nan
+
+    _run(rng, table, keys, values, new, past, q_heads, 32, decay=0.6, window=window, bounds=(None, context), spoil=spoil)
+
+
+@pytest.mark.parametrize("context", [None, 200000])
+def test_a_tree_that_fills_its_tiles(context):
+    rng = np.random.default_rng(11)
+    new, past = (64, 64), (90, 3)
+    table, keys, values = K.filled(rng, new, past, 2, 128, 8, 8, 16)
+    G.note("weights of full trees")
+    _run(rng, table, keys, values, new, past, 10, 16, tree=_tree(rng, new), bounds=(None, context))
+    # fewer tokens than the bounds say, in rows of no sequence
+    _run(rng, table, keys, values, (64, 32), past, 10, 16, bounds=(64, context), rows=32)
+
+
 @pytest.mark.parametrize("window", [1, 7, 50, 1000, 2 ** 31 - 1])
 @pytest.mark.parametrize("new,past", [((1,), (90,)), ((40, 3), (60, 0)), ((130,), (20,))])
 def test_windows(new, past, window):

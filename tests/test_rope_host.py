@@ -52,7 +52,10 @@ def rows(**kw):
     (dict(rows=rows(in_stride=1 << 41)), ESHAPE), (dict(tokens=1 << 30), ESHAPE),
     (dict(rows=rows(in_=A + 8)), EALIGN), (dict(rows=rows(out=B + 8)), EALIGN), (dict(rows=rows(in_stride=1028)), EALIGN),
     (dict(rows=rows(out_stride=1028)), EALIGN), (dict(rows=rows(out_stride=1026, out_type=1)), EALIGN),
-    (dict(freqs=A + 4), EALIGN), (dict(positions=A + 2), EALIGN)])
+    (dict(freqs=A + 4), EALIGN), (dict(positions=A + 2), EALIGN),
+    # the same set twice, and outputs that another set reads or writes
+    (dict(rows=rows(out=A) * 2), EINVAL), (dict(rows=rows() * 2), EINVAL), (dict(rows=rows() + rows(in_=B, out=B + 4096)), EINVAL),
+    (dict(rows=rows(in_=B, out=B + 4096) + rows()), EINVAL)])
 def test_refusals(lib, kw, status):
     assert call(lib, **kw) == status
 
