@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kWeighThreads, RT * D <= 128 ? 4 : RT * D <= 2
 // that one barrier a step is enough.  16-byte chunks of a row stand exchanged by the
 // row's number, without which the lanes of a read would meet in the same banks.
 // 2048 tokens of 32 heads over 32768 keys: 705 us, 950 TFLOP/s.  Matrix instructions take
-// 36% of the cycles, the exponentials' multiply-adds and the steps' other vector work most
+// 43% of the cycles, the exponentials' multiply-adds and the steps' other vector work most
 // of the rest: two waves a SIMD overlap them only in part, four kept in one wave's
 // registers (1154 us) or both woven into one stream of instructions (798 us) do no better.
 
