@@ -16,9 +16,8 @@
 // unit are split over workgroups so that no two share any: a piece of the keys' codes, a
 // part of the values' rows, either side's scales.  What bounds it: three dependent loads
 // for a stretch (the kept position, its page, the bytes), so that a stretch is 4096 tokens
-// (11.5 us for 4096 of 4607); and, in large batches, bytes, of which a line that holds one
-// kept token is read whole (64 sequences of 1 to 8191 to 2048: 104 us, 3.4 TB/s of what
-// memory moves).  512 threads: with 256 these two take 13 and 106 us, with 1024 12 and 113.
+// (9 us for 4096 of 4607; 64 sequences of 1 to 8191 to 2048: 96 us, 2.9 TB/s).  512
+// threads: with 256 these take 2 and 9 us more, with 1024 0.3 less and 23 more.
 #include "nvfp4_kv.h"
 
 namespace nvfp4 {
@@ -27,6 +26,10 @@ constexpr int kSelectThreads = 1024, kSelectWaves = kSelectThreads / kLanes;
 constexpr int kDigitBits = 12, kBins = 1 << kDigitBits;
 constexpr int kRanked = 512;                                      // keys that are compared with one another
 constexpr int kMoveThreads = 512, kMoveTokens = 4096;            // tokens of a stretch
+// A head's workgroups are put on one XCD, whose cache then serves the lines that its value
+// parts share (64 sequences 115 us, both launches, with the parts one after another 123;
+// 4096 of 4607 tokens 19.1 against 21.8).
+constexpr int kXcds = 8;
 constexpr int kMostParts = 32, kValueParts = 5;    // workgroups that move a head's tokens; those of its values
 
 struct EvictArgs {
@@ -306,7 +309,8 @@ __device__ __forceinline__ void move_side(const EvictArgs &a, int s, int head, c
 
 template <int D>
 __global__ void __launch_bounds__(kMoveThreads) kv_evict_move_kernel(EvictArgs a, int k_bits, int v_bits, int key_parts, int parts) {
-    const int row = blockIdx.x / parts, part = blockIdx.x % parts;
+    const int part = int(blockIdx.x / kXcds) % parts, row = int(blockIdx.x / (kXcds * parts)) * kXcds + int(blockIdx.x % kXcds);
+    if (row >= a.kv.seqs * a.kv.heads) return;
     const int head = row % a.kv.heads, s = row / a.kv.heads;
     const int *kept = a.kept + int64_t(row) * a.budget;
     if (part == 0 && head == 0 && threadIdx.x == 0) {
@@ -346,9 +350,8 @@ NVFP4_API int nvfp4_kv_evict(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *
     a.first = first;
     a.recent = recent;
     // The fewest positions a thread that the bound allows: with eight two workgroups fit a CU
-    // (4607 positions 21.7 us, both launches, with 32 a thread 29.0; 9000 positions 26.6 with 16,
-    // 31.2 with 32), but what does not stay in registers is read several times (32768 positions
-    // 38.8 us with 32 a thread, 45.7 with 8 or 16).
+    // (4607 positions 10.6 us, with 32 a thread 18; 9000 positions 15 with 16, 19.6 with 32), but what does not stay in registers is read several times (32768 positions
+    // 25 us with 32 a thread, 32 with 8 or 16).
     if (batch->max_context <= 8 * kSelectThreads) kv_evict_select_kernel<8><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
     else if (batch->max_context <= 16 * kSelectThreads) kv_evict_select_kernel<16><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
     else kv_evict_select_kernel<32><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
@@ -358,7 +361,7 @@ NVFP4_API int nvfp4_kv_evict(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *
         constexpr int D = decltype(dim)::value;
         static_assert(1 + KvSide<D, 8>::kPieces + kValueParts <= kMostParts);
         const int key_parts = 1 + (kb == 8 ? KvSide<D, 8>::kPieces : KvSide<D, 4>::kPieces);
-        kv_evict_move_kernel<D><<<unsigned(rows * (key_parts + kValueParts)), kMoveThreads, 0, stream>>>(
+        kv_evict_move_kernel<D><<<unsigned(ceil_div(rows, int64_t(kXcds)) * kXcds * (key_parts + kValueParts)), kMoveThreads, 0, stream>>>(
             a, kb, vb, key_parts, key_parts + kValueParts);
         return launch_status();
     });
