@@ -98,7 +98,9 @@ class AttentionLayer:
         result float32 [tokens, hidden], overwritten by the next step.  positions int32
         [tokens] or [axes, tokens]: the tokens' own, for a layer that turns q and k (after
         an eviction they are no longer their places in the cache).  weights: of
-        alloc_weights, to which the step adds the attention that each key receives."""
+        alloc_weights, to which the step adds the attention that each key receives; a cache
+        that is to be cut is given them in every step, since only such a step starts its
+        new keys at 0."""
         n = batch.tokens
         if n > self.max_tokens or tuple(x.shape) != (n, self.hidden):
             raise ValueError("x has shape %s, expected (%d, %d) with at most %d tokens" % (

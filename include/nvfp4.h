@@ -525,8 +525,10 @@ int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t vocab, int6
  *                      + sum over new tokens and query heads of head h of exp(z_j - lse)
  * for every position j < past[s] + new; the rest is left alone, and so are sequences
  * without new tokens.  decay is in 0..1; 1 gathers, 0 does not read what was there.
- * Rows whose lse is not finite add
- * nothing, nor do keys that hold a NaN or an infinity or have no page.  Scores
+ * What stands at the positions of tokens that were appended by a step without this call
+ * counts as theirs (after an eviction, weights of tokens that left): such a program
+ * clears them itself.  Rows whose lse is not finite add nothing, nor do keys that hold a
+ * NaN or an infinity or have no page.  Scores
  * accumulate in fp32, sums in fp32 in an order fixed by the arguments and the
  * arrays' values: the same bits on every run.  Requirements and errors as
  * nvfp4_kv_attention; weights and lse 4-byte aligned, a decay out of range
