@@ -350,11 +350,14 @@ NVFP4_API int nvfp4_kv_evict(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *
     a.first = first;
     a.recent = recent;
     // The fewest positions a thread that the bound allows: with eight two workgroups fit a CU
-    // (4607 positions 10.6 us, with 32 a thread 18; 9000 positions 15 with 16, 19.6 with 32), but what does not stay in registers is read several times (32768 positions
-    // 25 us with 32 a thread, 32 with 8 or 16).
-    if (batch->max_context <= 8 * kSelectThreads) kv_evict_select_kernel<8><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
-    else if (batch->max_context <= 16 * kSelectThreads) kv_evict_select_kernel<16><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
-    else kv_evict_select_kernel<32><<<unsigned(rows), kSelectThreads, 0, stream>>>(a);
+    // (4607 positions 10.6 us, with 32 a thread 18; 9000 positions 15 with 16, 19.6 with 32),
+    // but what does not stay in registers is read several times (32768 positions 25 us with
+    // 32 a thread, 32 with 8 or 16).
+    const unsigned groups = unsigned(rows);
+    const int held = ceil_div(batch->max_context, kSelectThreads);
+    if (held <= 8) kv_evict_select_kernel<8><<<groups, kSelectThreads, 0, stream>>>(a);
+    else if (held <= 16) kv_evict_select_kernel<16><<<groups, kSelectThreads, 0, stream>>>(a);
+    else kv_evict_select_kernel<32><<<groups, kSelectThreads, 0, stream>>>(a);
     if (int st = launch_status()) return st;
     const int kb = cache->k_format == NVFP4_KV_MXFP8 ? 8 : 4, vb = cache->v_format == NVFP4_KV_MXFP8 ? 8 : 4;
     return kv_dim(cache->head_dim, [&](auto dim) {
