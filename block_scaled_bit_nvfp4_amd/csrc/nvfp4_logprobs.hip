@@ -2,10 +2,10 @@
 // tokens of rows of logits (gfx950).
 //
 // One pass over the logits: a workgroup holds a chunk of a row in registers and leaves,
-// of z = scale * x, the maximum m, l = sum e^(z - m), t = sum e^(z - m) (z - m), and the
-// `top` largest logits as keys.  A second launch joins a row's chunks,
-//   l = sum l_c e^(m_c - m),  t = sum e^(m_c - m) (t_c + l_c (m_c - m)),
-//   lse = m + log l,  entropy = log l - t / l,
+// with d = scale * (x - m), the largest logit m, l = sum e^d, t = sum e^d d, and the `top`
+// largest logits as keys.  A second launch joins a row's chunks,
+//   l = sum l_c e^D,  t = sum e^D (t_c + l_c D)  with D = scale * (m_c - m),
+//   lse = scale * m + log l,  entropy = log l - t / l,
 // and looks the given tokens up.  Bound by reading the logits once: 512 rows of 151936 in
 // fp32 take 59 us and the join 6.5 (5.3 TB/s, a large copy's rate); one row 6 and 4.8, two
 // launches.
@@ -17,6 +17,8 @@
 // `top`, goes to shared memory, where an element's rank is the number of larger ones.
 // Where too many reach it (equal logits, such as masked ones) the bound is taken again,
 // among all threads' maxima with their places, which no two share.
+#include <math.h>
+
 #include "nvfp4_host.h"
 
 namespace nvfp4 {
@@ -31,8 +33,9 @@ constexpr int64_t kLogpFill = 512;                // workgroups with long chunks
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 
-// Sums of one part relative to its maximum.  l is in 64 bits: where one token is all but
-// certain, l is 1 and a little, and that little is all of its log probability.
+// Sums of one part relative to its largest logit, m.  l is in 64 bits: where one token is all
+// but certain, l is 1 and a little, and that little is all of its log probability.  The
+// reference is m and not scale * m, whose rounding would put the largest term off 1.
 struct Sums {
     float m, t;
     double l;
@@ -43,6 +46,8 @@ struct LogpArgs {
     int64_t stride;
     int vocab, chunks, given, top;
     float scale;
+    float pre, post;       // d = (pre * x - pre * m) * post, pre a power of two
+    float to_log2;         // post * log2(e)
     const int *tokens;
     float *logp, *lse, *entropy, *top_logp;
     int *top_index;
@@ -202,8 +207,10 @@ __device__ __forceinline__ void largest(TopShared &sh, int top, uint32_t most, O
 
 // A part's sums relative to m >= s.m; parts of nothing (m = -infinity, l = 0) stay
 // nothing, and a difference past fp32's range has no infinity to multiply a weight of 0.
-__device__ __forceinline__ Sums moved(Sums s, float m) {
-    const float d = s.m == kNegInf ? 0.0f : fmaxf(s.m - m, -1e30f);
+__device__ __forceinline__ Sums moved(const LogpArgs &a, Sums s, float m) {
+    // the powers of two below 1 alone: no product passes fp32's range
+    const float pre = fminf(a.pre, 1.0f), post = a.pre > 1.0f ? a.scale : a.post;
+    const float d = s.m == kNegInf ? 0.0f : fmaxf(__builtin_fmaf(s.m, pre, -(m * pre)) * post, -1e30f);
     const float w = __builtin_amdgcn_exp2f(d * kLog2e);
     return Sums{m, w * __builtin_fmaf(float(s.l), d, s.t), s.l * w};
 }
@@ -278,15 +285,19 @@ __global__ void __launch_bounds__(kLogpThreads, 8) logprobs_chunk_kernel(LogpArg
 #pragma unroll
     for (int i = 1; i < N; ++i) most = fmaxf(most, x[i]);
     const float top = wave_largest(most);
-    Sums s = {top * a.scale, 0.0f, 0.0};
-    const float base = s.m == kNegInf ? 0.0f : s.m;
+    Sums s = {top, 0.0f, 0.0};
+    // A `pre` of 2 is for scales whose product with log2(e) may pass fp32's range.  It is left
+    // out where 2 * top may: logits that far out differ by nothing or by so much that e is 0.
+    const float pre = fabsf(top) < 0x1p126f ? a.pre : fminf(a.pre, 1.0f);
+    const float base = top == kNegInf ? 0.0f : top * pre;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float d = __builtin_fmaf(x[i], a.scale, -base);
-        const float e = __builtin_amdgcn_exp2f(d * kLog2e);
+        const float y = __builtin_fmaf(x[i], pre, -base);            // d / post
+        const float e = __builtin_amdgcn_exp2f(y * a.to_log2);
         s.l += double(e);
-        s.t = __builtin_fmaf(e, fmaxf(d, -1e30f), s.t);
+        s.t = __builtin_fmaf(e, fmaxf(y, -1e30f), s.t);
     }
+    s.t *= a.post;
     s.l = wave_sum(s.l);
     s.t = wave_sum(s.t);
     if ((tid & 63) == 0) sums[wave] = s;
@@ -329,7 +340,7 @@ __global__ void __launch_bounds__(kLogpThreads, 8) logprobs_chunk_kernel(LogpArg
         Sums all = {m, 0.0f, 0.0};
 #pragma unroll
         for (int w = 0; w < kLogpWaves; ++w) {
-            const Sums o = moved(sums[w], m);
+            const Sums o = moved(a, sums[w], m);
             all.l += o.l;
             all.t += o.t;
         }
@@ -356,7 +367,7 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
     m = wave_largest(m);
     Sums s = {m, 0.0f, 0.0};
     for (int c = tid; c < a.chunks; c += kLogpThreads) {
-        const Sums o = moved(parts[c], m);
+        const Sums o = moved(a, parts[c], m);
         s.l += o.l;
         s.t += o.t;
     }
@@ -370,16 +381,16 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
     Sums all = {m, 0.0f, 0.0};
 #pragma unroll
     for (int w = 0; w < kLogpWaves; ++w) {
-        const Sums o = moved(sums[w], m);
+        const Sums o = moved(a, sums[w], m);
         all.l += o.l;
         all.t += o.t;
     }
     const bool nothing = m == kNegInf && all.l == 0.0;
     const double log_l = log_of(all.l);
-    const float lse = nothing ? kNegInf : float(m + log_l);
+    const float lse = nothing ? kNegInf : float(__builtin_fma(double(m), double(a.scale), log_l));
     const float entropy = nothing ? 0.0f : float(log_l - all.t / all.l);
     // z - lse without the rounding of a large lse
-    const auto logp = [&](float x) { return nothing ? kNegInf : float(__builtin_fma(double(x), double(a.scale), -double(m)) - log_l); };
+    const auto logp = [&](float x) { return nothing ? kNegInf : float((double(x) - double(m)) * double(a.scale) - log_l); };
     if (tid == 0) {
         if (a.lse) a.lse[r] = lse;
         if (a.entropy) a.entropy[r] = entropy;
@@ -465,6 +476,13 @@ NVFP4_API int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t v
     a.given = given;
     a.top = top;
     a.scale = scale;
+    // Of a scale below 1 the power of two goes to the logits, whose difference might pass
+    // fp32's range where its product does not; of the largest a 2.
+    int power;
+    const float part = frexpf(scale, &power);            // scale = part * 2^power, part in 1/2 .. 1
+    a.pre = scale < 1.0f ? ldexpf(1.0f, power - 1) : scale < 0x1p126f ? 1.0f : 2.0f;
+    a.post = scale < 1.0f ? 2.0f * part : scale / a.pre;
+    a.to_log2 = float(double(a.post) * 1.4426950408889634074);
     a.tokens = tokens;
     a.logp = logp;
     a.lse = lse;

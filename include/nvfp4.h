@@ -492,11 +492,13 @@ int nvfp4_rope(const nvfp4_rope_rows *rows, int count, int dtype, int64_t tokens
  *                  lowest token first; -0 and +0 tie, NaN counts least), and
  *   top_logp[r]  = their log probabilities.
  * Logits of minus infinity are tokens that are masked out.  A row of nothing else
- * has lse and all log probabilities -infinity and entropy 0; one with a z of +infinity
- * or NaN has lse, log probabilities and entropy NaN.  Outputs may each be NULL
+ * has lse and all log probabilities -infinity and entropy 0; one with a logit of +infinity
+ * or NaN has lse, log probabilities and entropy NaN.  A finite logit's z may pass fp32's
+ * range: lse is then rounded to an infinity, the rest is as ever.  Outputs may each be NULL
  * (tokens and logp together, with given = 0; top_logp and top_index both, with top =
- * 0), but not all.  Sums are taken in a fixed order, that of exp in 64 bits, so that
- * log probabilities and entropy near 0 keep their digits.  0 <= n, 1 <= vocab <= 2^30,
+ * 0), but not all.  Sums are taken in a fixed order, relative to the largest logit and
+ * that of exp in 64 bits, so that log probabilities and entropy near 0 keep their digits
+ * at any scale, down to 2^-47.  0 <= n, 1 <= vocab <= 2^30,
  * 0 <= top <= min(vocab, NVFP4_MAX_TOP), stride >= vocab (else NVFP4_ESHAPE),
  * 0 <= given <= 2^20; logits need only their element's alignment, outputs 4 bytes.
  * workspace: nvfp4_logprobs_workspace_bytes(n, vocab, top) bytes, 16-byte aligned,
