@@ -440,13 +440,21 @@ static bool logprobs_shape_ok(int64_t n, int64_t vocab, int top) {
     return n * ceil_div(vocab, logprobs_chunk(n, vocab)) <= kMaxGroups;
 }
 
+// What a call of n rows writes to its workspace.
+static size_t logprobs_need(int64_t n, int64_t vocab, int top) {
+    return size_t(n) * size_t(ceil_div(vocab, logprobs_chunk(n, vocab))) * (sizeof(Sums) + size_t(top) * sizeof(Key));
+}
+
 }  // namespace nvfp4
 
 using namespace nvfp4;
 
 NVFP4_API size_t nvfp4_logprobs_workspace_bytes(int64_t n, int64_t vocab, int top) {
     if (!logprobs_shape_ok(n, vocab, top)) return 0;
-    return size_t(n) * size_t(ceil_div(vocab, logprobs_chunk(n, vocab))) * (4 * sizeof(float) + size_t(top) * sizeof(Key));
+    // that of the most rows in short chunks may be larger
+    const int64_t most_short = (kLogpFill - 1) / ceil_div(vocab, kLong * kLogpThreads);
+    const size_t need = logprobs_need(n, vocab, top), fewer = logprobs_need(n < most_short ? n : most_short, vocab, top);
+    return need > fewer ? need : fewer;
 }
 
 NVFP4_API int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t vocab, int64_t stride, float scale,
@@ -464,8 +472,7 @@ NVFP4_API int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t v
         !aligned(entropy, 4) || !aligned(top_logp, 4) || !aligned(top_index, 4))
         return NVFP4_EALIGN;
     if (n == 0) return NVFP4_OK;
-    const size_t need = nvfp4_logprobs_workspace_bytes(n, vocab, top);
-    if (!workspace || workspace_bytes < need) return NVFP4_EWORKSPACE;
+    if (!workspace || workspace_bytes < logprobs_need(n, vocab, top)) return NVFP4_EWORKSPACE;
     if (!aligned(workspace, 16)) return NVFP4_EALIGN;
     LogpArgs a = {};
     a.logits = logits;

@@ -501,8 +501,9 @@ int nvfp4_rope(const nvfp4_rope_rows *rows, int count, int dtype, int64_t tokens
  * at any scale, down to 2^-47.  0 <= n, 1 <= vocab <= 2^30,
  * 0 <= top <= min(vocab, NVFP4_MAX_TOP), stride >= vocab (else NVFP4_ESHAPE),
  * 0 <= given <= 2^20; logits need only their element's alignment, outputs 4 bytes.
- * workspace: nvfp4_logprobs_workspace_bytes(n, vocab, top) bytes, 16-byte aligned,
- * any contents; not shared by calls that may overlap.  n = 0 is no error. */
+ * workspace: nvfp4_logprobs_workspace_bytes(n, vocab, top) bytes, which serve fewer rows
+ * and fewer likeliest tokens of that vocabulary too, 16-byte aligned, any contents; not
+ * shared by calls that may overlap.  n = 0 is no error. */
 #define NVFP4_MAX_TOP 64
 size_t nvfp4_logprobs_workspace_bytes(int64_t n, int64_t vocab, int top);
 int nvfp4_logprobs(int dtype, const void *logits, int64_t n, int64_t vocab, int64_t stride, float scale,
