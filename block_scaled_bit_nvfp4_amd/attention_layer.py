@@ -129,12 +129,16 @@ class AttentionLayer:
         nv.nvfp4_gemv(*self.wo, o.view(n, wide), n, self.y[:n])
         return self.y[:n]
 
-    def evict(self, batch, weights, budget, kept, first=0, recent=0):
+    def evict(self, batch, weights, budget, kept, first=0, recent=0, left=None):
         """Cut the batch's sequences that hold more than `budget` tokens (`past`, without
-        the step's new ones) down to it, past itself included: of each head the first
-        `first`, the last `recent` and the keys of the largest weights stay.  kept int32
-        [seqs, heads, budget] gets their places before the cut; weights move with them."""
-        nv.nvfp4_kv_evict(self.cache, batch, weights, budget, kept, batch.arrays[2], first=first, recent=recent)
+        the step's new ones) down to it: of each head the first `first`, the last `recent`
+        and the keys of the largest weights stay.  kept int32 [seqs, heads, budget] gets
+        their places before the cut; weights move with them.  left int32 [seqs] gets the
+        tokens held now; without it past itself does.  Where layers share a batch, all but the
+        last to be cut are given a `left`: a layer that finds the budget in past cuts
+        nothing, and would take its first tokens for all that it holds."""
+        nv.nvfp4_kv_evict(self.cache, batch, weights, budget, kept, batch.arrays[2] if left is None else left,
+                          first=first, recent=recent)
 
 
 def chain_mask(n, device):
