@@ -15,6 +15,7 @@ namespace nvfp4 {
 
 constexpr int kRopeThreads = 256;
 constexpr int64_t kRopeMost = int64_t(1) << 34;   // units of eight elements
+constexpr int64_t kRopeMostGroups = (int64_t(1) << 32) / kRopeThreads - 1;     // of a launch: its threads stay below 2^32
 // Workgroups from which rope_many_kernel is the faster one (256 tokens of 48 heads of 128,
 // 256 of them, 4.3 us against 5.3; 300 of 32 heads of 72, 57 of them, 5.3 against 3.9).
 constexpr int64_t kRopeFill = 128;
@@ -336,7 +337,7 @@ static int launch_rope_many(RopeArgs &a, hipStream_t stream) {
         f.last_magic = magic_of((f.heads - (f.ranges - 1) * f.per) * units);
         blocks += ceil_div(a.tokens, f.span) * f.ranges;
     }
-    if (blocks > 0x7FFFFFFF) return NVFP4_ESHAPE;
+    if (blocks > kRopeMostGroups) return NVFP4_ESHAPE;
     a.unit_magic = magic_of(units);
     a.pair_magic = magic_of(pairs);
     rope_many_kernel<T, WIDE, ITEMS><<<unsigned(blocks), kRopeThreads, 0, stream>>>(a);

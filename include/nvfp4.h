@@ -464,7 +464,8 @@ int nvfp4_kv_attention(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *batch,
  * head_dim is a multiple of 8 up to 1024, rotary_dim a multiple of 8 up to
  * head_dim (else NVFP4_ESHAPE); pointers 16-byte aligned with strides of whole 16
  * bytes, freqs 8-byte and positions 4-byte aligned (else NVFP4_EALIGN).  axis may
- * be NULL: all pairs follow axis 0.  factor is finite and > 0.  No tokens is no
+ * be NULL: all pairs follow axis 0.  factor is finite and > 0.  A call of more than
+ * 2^33 elements in all may be too large for one launch (NVFP4_ESHAPE).  No tokens is no
  * error, and the rows' pointers may then be NULL. */
 #define NVFP4_MAX_ROPE 4
 
