@@ -8,7 +8,9 @@
 // whose ranks are found by comparing all of them with all; only where it holds many (equal
 // weights) the next 12 bits are counted.  Then one walk in order writes the kept positions
 // and moves their weights.  Up to 8192, 16384 or 32768 positions, by the bound, stay in
-// registers throughout.  Bound by its chain of dependent steps: 10.6 us for 4607 positions.
+// registers throughout.  Bound by its chain of dependent steps, 10.6 us for 4607 positions, and
+// by a CU's issue where there are many: of 25 us for 32768 of eight heads, 13 are 2.5e5 vector
+// instructions of waves on eight CUs.
 //
 // Move: a kept token's slot is never past its old one, and both rise together.  So one
 // workgroup can move a stretch of tokens at a time, all reads before all writes, and the
@@ -16,8 +18,10 @@
 // unit are split over workgroups so that no two share any: a piece of the keys' codes, a
 // part of the values' rows, either side's scales.  What bounds it: three dependent loads
 // for a stretch (the kept position, its page, the bytes), so that a stretch is 4096 tokens
-// (9 us for 4096 of 4607; 64 sequences of 1 to 8191 to 2048: 96 us, 2.9 TB/s).  512
-// threads: with 256 these take 2 and 9 us more, with 1024 0.3 less and 23 more.
+// (9 us for 4096 of 4607), and for many sequences the lines that hold something that is
+// kept, twice the bytes themselves (64 sequences of 1 to 8191 to 2048: 96 us, 282 MB read
+// of 274 in such lines, 144 written, 4.4 TB/s).  512 threads: with 256 these take 2 and 9 us
+// more, with 1024 0.3 less and 23 more.
 #include "nvfp4_kv.h"
 
 namespace nvfp4 {
@@ -352,7 +356,9 @@ NVFP4_API int nvfp4_kv_evict(const nvfp4_kv_cache *cache, const nvfp4_kv_batch *
     // The fewest positions a thread that the bound allows: with eight two workgroups fit a CU
     // (4607 positions 10.6 us, with 32 a thread 18; 9000 positions 15 with 16, 19.6 with 32),
     // but what does not stay in registers is read several times (32768 positions 25 us with
-    // 32 a thread, 32 with 8 or 16).
+    // 32 a thread, 32 with 8 or 16).  The lengths are on the device, so a bound far above
+    // them has its price: both launches for 4607 positions take 19.4 us, under a bound of
+    // 131072 26.7; 9000 positions 25.7 and 30.5.
     const unsigned groups = unsigned(rows);
     const int held = ceil_div(batch->max_context, kSelectThreads);
     if (held <= 8) kv_evict_select_kernel<8><<<groups, kSelectThreads, 0, stream>>>(a);

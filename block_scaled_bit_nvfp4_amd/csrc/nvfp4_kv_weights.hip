@@ -11,7 +11,10 @@
 namespace nvfp4 {
 
 constexpr int kWeighWaves = 4, kWeighThreads = kWeighWaves * kLanes;
-constexpr int kFewRows = 64;               // the most rows (new tokens x group) of a sequence for the first kernel
+// The most rows (new tokens x group) of a sequence for the first kernel.  40 rows of 8 heads
+// take it 7.1 us over 2048 keys (the second kernel 9.5), 12.7 over 16384 (10.5) and 35 over
+// 131000 (44); 80 rows, two passes, 11 (9.5), 21 (12) and 64 (52).
+constexpr int kFewRows = 64;
 
 typedef float floatx16 __attribute__((ext_vector_type(16)));
 
@@ -293,7 +296,7 @@ __global__ void __launch_bounds__(kWeighThreads, RT * D <= 128 ? 4 : RT * D <= 2
 // A step's rows go straight to shared memory two steps ahead, into a ring of three, so
 // that one barrier a step is enough.  16-byte chunks of a row stand exchanged by the
 // row's number, without which the lanes of a read would meet in the same banks.
-// 2048 tokens of 32 heads over 32768 keys: 705 us, 950 TFLOP/s.  Matrix instructions take
+// 2048 tokens of 40 heads over 32768 keys: 705 us, 950 TFLOP/s.  Matrix instructions take
 // 43% of the cycles, the exponentials' multiply-adds and the steps' other vector work most
 // of the rest: two waves a SIMD overlap them only in part, four kept in one wave's
 // registers (1154 us) or both woven into one stream of instructions (798 us) do no better.
@@ -589,7 +592,7 @@ static int launch_few(const WeighArgs &a, int64_t context, int64_t most_rows, hi
     const int64_t steps = ceil_div(context, kWeighWaves * 32) * a.kv.seqs, all = steps * a.kv.heads;
     // Two workgroups a CU, or as many as fit where there are steps for them (32000 keys of 8
     // heads 9.5 us, with four 10.2; 64 sequences of 4095 keys 32.6, with two 37.1): with
-    // more than one tile of rows two fit (8 tokens over 16385 keys 14.7 us, with four 23.5).
+    // more than one tile of rows two fit (8 tokens of 40 heads over 16385 keys 12.7 us, with four 19.4).
     const int64_t groups = all < kFewFill || most_rows > 16 ? 512 : 1024, each = ceil_div(groups, a.kv.heads);
     const dim3 grid(unsigned(steps < 1 ? 1 : steps < each ? steps : each), a.kv.heads);
     if (most_rows <= 16) weigh_few_kernel<D, BITS, 1><<<grid, kWeighThreads, 0, stream>>>(a);
@@ -615,9 +618,9 @@ static int launch_many_as(const WeighArgs &a, int64_t context, bool flat, hipStr
 template <int D, int BITS>
 static int launch_many(const WeighArgs &a, int64_t context, bool even, hipStream_t stream) {
     // Tiles of a head's tokens leave places of the last one empty, half of them where the
-    // lengths differ: taken where that is less than an eighth (2048 tokens over 32768 keys
-    // 705 us, of rows one after another 784; 64 over 8192 11.5 against 12.2; but 4 x 40
-    // tokens over 16k keys 74 against 49, 1 to 301 tokens of 7 sequences 74 against 65).
+    // lengths differ: taken where that is less than an eighth (of 40 heads, 2048 tokens over
+    // 32768 keys 700 us, of rows one after another 778; 64 over 8192 12.1 against 12.9; but 4 x
+    // 40 tokens over 16384 keys 71 against 48, 1 to 301 tokens of 7 sequences 126 against 98).
     const int64_t mean = a.kv.tokens / a.kv.seqs, places = ceil_div(mean, 32) * 32 + (even ? 0 : 16);
     const bool flat = 8 * places > 9 * mean || a.q_stride >= int64_t(1) << 25 || a.q_heads >= 1 << 24;
     // Waves share keys where there are not enough of them to give every CU two workgroups.

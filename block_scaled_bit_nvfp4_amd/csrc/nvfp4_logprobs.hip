@@ -7,7 +7,7 @@
 //   l = sum l_c e^D,  t = sum e^D (t_c + l_c D)  with D = scale * (m_c - m),
 //   lse = scale * m + log l,  entropy = log l - t / l,
 // and looks the given tokens up.  Bound by reading the logits once: 512 rows of 151936 in
-// fp32 take 59 us and the join 6.5 (5.3 TB/s, a large copy's rate); one row 6 and 4.8, two
+// fp32 take 58 us and the join 6.9 (5.4 TB/s, a large copy's rate); one row 6.0 and 5.0, two
 // launches.
 //
 // The largest logits of a chunk are found without sorting it.  The top-th largest of a
@@ -428,8 +428,9 @@ __global__ void __launch_bounds__(kLogpThreads) logprobs_join_kernel(LogpArgs a,
 }
 
 // Logits of a workgroup: chunks of 2048 where longer ones would leave CUs idle (one row of
-// 151936: 10.8 us, of 8192 14; 16 rows 13.7 and 15.6), else of 8192 (128 rows 28 us, of
-// 2048 36; 512 rows 70 and 115).
+// 151936: 11.0 us, of 8192 13.7; 16 rows 13.9 and 15.0; from 24 to 27 rows either takes 16),
+// else of 8192 (48 rows 18.7 us, of 2048 20.6; 128 rows 26.5 and 35; 512 rows 66 and 108; in
+// bf16 17.7 and 20.1, 26 and 35, 56 and 107).
 static int64_t logprobs_chunk(int64_t n, int64_t vocab) {
     return (n * ceil_div(vocab, kLong * kLogpThreads) < kLogpFill ? kShort : kLong) * kLogpThreads;
 }
